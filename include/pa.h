@@ -110,6 +110,55 @@ int pa_cache_write(const pa_cache_desc* desc, const void* k_new, const void* v_n
                    const int64_t* slot_mapping, int32_t num_tokens, void* k_cache, void* v_cache,
                    void* stream);
 
+/* How pa_norm_rope_write prepares queries and keys. */
+typedef struct {
+  const void* q_weight;  /* device [head_dim], q_dtype, 16-byte aligned; NULL: queries are not normed */
+  const void* k_weight;  /* the same for keys */
+  float eps;             /* added to the mean square, finite and >= 0 */
+  const float* cos_sin;  /* device fp32 [num_positions][rot_dim], 16-byte aligned: a position's rot_dim / 2
+                            cosines, then its rot_dim / 2 sines; NULL: no rotation */
+  int32_t num_positions; /* rows of cos_sin */
+  int32_t rot_dim;       /* leading elements of a head that are rotated: a multiple of 8, <= head_dim */
+  int32_t interleaved;   /* 0: pairs (i, i + rot_dim / 2); 1: pairs (2i, 2i + 1) */
+} pa_qk_prep;
+
+/* pa_norm_rope_write: the step before the attention, in one pass over the new
+ * rows: per query and key head y = x * rsqrt(mean(x^2) + eps) * weight, then
+ * the rotation (a, b) -> (a cos - b sin, b cos + a sin) of its pairs at the
+ * token's position; queries to q_out, keys and values (as they are) to their
+ * slots as pa_cache_write stores them.  Computed in fp32 and rounded once:
+ * an e4m3 pool gets e4m3(y / scale) of the fp32 y.
+ *   q, k, v       device, q_dtype, [num_tokens] rows of [heads][head_dim];
+ *                 *_stride elements lie between two tokens' rows (slices of
+ *                 one projection's output need no copy); 16-byte aligned,
+ *                 strides whole 16-byte units, at least one row and at
+ *                 most 2^28 elements long
+ *   positions     device, int32 [num_tokens]; a token whose position is
+ *                 outside [0, num_positions) is left out whole: neither its
+ *                 q_out row nor its slot is written (without cos_sin: not
+ *                 read, may be NULL)
+ *   slot_mapping  device, int64 [num_tokens], as for pa_cache_write: a slot
+ *                 outside the pool writes no K and V (its q_out row is written)
+ *   q_out         device, [num_tokens][num_q_heads][head_dim], q_dtype; may be
+ *                 q itself when q_stride is one row; any other overlap of
+ *                 q_out with q, k or v is PA_ERR_INVALID_ARG
+ * Dtypes as for pa_cache_write.  Two tokens with the same slot race. */
+int pa_norm_rope_write(const pa_cache_desc* desc, const pa_qk_prep* prep, const void* q, int64_t q_stride,
+                       const void* k, int64_t k_stride, const void* v, int64_t v_stride, const int32_t* positions,
+                       const int64_t* slot_mapping, int32_t num_tokens, void* q_out, void* k_cache, void* v_cache,
+                       void* stream);
+
+/* pa_cache_read: pa_cache_write's inverse: row t of k_out and v_out becomes
+ * what the pools hold at slot_mapping[t]; a slot outside the pool leaves its
+ * rows as they were.  Rows of fp32 and bf16 pools are bit copies (query dtype =
+ * pool dtype, else PA_ERR_UNSUPPORTED); e4m3 codes come back as code * scale,
+ * rounded once to the query dtype (NaN codes as NaN).
+ *   slot_mapping  device, int64 [num_tokens]; a slot may come more than once
+ *   k_out, v_out  device, [num_tokens][num_kv_heads][head_dim], q_dtype, apart
+ *                 from each other and from the pools */
+int pa_cache_read(const pa_cache_desc* desc, const int64_t* slot_mapping, int32_t num_tokens, const void* k_cache,
+                  const void* v_cache, void* k_out, void* v_out, void* stream);
+
 /* pa_decode_fused: pa_cache_write of each sequence's new token and
  * pa_decode, in one launch (the write of "write(blocks[-1], kv)" in the
  * block-table snippet on "49 vLLM / PagedAttention", followed by the step's

@@ -101,6 +101,116 @@ def pa_cache_write(desc, k_new, v_new, slot_mapping, k_cache, v_cache, stream=No
                                 _ptr(k_cache), _ptr(v_cache), _stream(stream)), "pa_cache_write")
 
 
+def _rows(who, name, t, dtype, device, heads, dim, contiguous=True):
+    """Checks a [tokens][heads][dim] tensor and returns the elements between two tokens' rows."""
+    if t.dtype != dtype or t.device != device or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise PaError(1, f"{who}: {name} must be [tokens][{heads}][{dim}] of {dtype} on {device}, got "
+                         f"{tuple(t.shape)} of {t.dtype} on {t.device}")
+    step, head, one = t.stride()
+    n = t.shape[0]
+    if one != 1 or (heads > 1 and head != dim) or (n > 1 and (step != heads * dim if contiguous else step < heads * dim)):
+        raise PaError(1, f"{who}: {name} has strides {t.stride()}")
+    return step if n > 1 else heads * dim
+
+
+def _array(who, name, t, dtype, device, shape):
+    """Checks a contiguous tensor of a given type, place and shape."""
+    if t.dtype != dtype or t.device != device or t.shape != shape or not t.is_contiguous():
+        raise PaError(1, f"{who}: {name} must be a contiguous {tuple(shape)} of {dtype} on {device}, got "
+                         f"{tuple(t.shape)} of {t.dtype} on {t.device}")
+
+
+def _pools(who, desc, k_cache, v_cache, device):
+    """Checks the pools against the desc (any view of the same bytes is taken)."""
+    need = desc.num_blocks * desc.num_kv_heads * desc.block_size * desc.head_dim * desc.kv_torch_dtype.itemsize
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if t.device != device or not t.is_contiguous() or t.numel() * t.element_size() != need:
+            raise PaError(1, f"{who}: {name} must hold {need} contiguous bytes on {device}")
+    for name, t in (("k_head_scales", desc._keep[0]), ("v_head_scales", desc._keep[1])):
+        if isinstance(t, torch.Tensor):
+            _array(who, name, t, torch.float32, device, (desc.num_kv_heads,))
+
+
+class _On:
+    """Makes a device current for a call (the library launches on the current one)."""
+
+    def __init__(self, who, device, stream):
+        if device.type != "cuda":
+            raise PaError(1, f"{who}: tensors must be on a CUDA device, got {device}")
+        self.stream, self.back = stream, None
+        self.device = device.index
+
+    def __enter__(self):
+        was = torch.cuda.current_device()
+        if was != self.device:
+            torch.cuda.set_device(self.device)
+            self.back = was
+        return _stream(self.stream)
+
+    def __exit__(self, *exc):
+        if self.back is not None:
+            torch.cuda.set_device(self.back)
+
+
+class QkPrep(ctypes.Structure):
+    """pa_qk_prep: norm weights and rotation table of one layer (kept alive by this object)."""
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("cos_sin", ctypes.c_void_p), ("num_positions", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
+
+    @classmethod
+    def make(cls, q_weight=None, k_weight=None, eps=1e-6, cos_sin=None, interleaved=False):
+        """q_weight / k_weight: device [head_dim] in the query dtype, or None (no norm).  cos_sin: device fp32
+        [num_positions][rot_dim], a position's cosines and then its sines, or None (no rotation)."""
+        n, rot = (int(cos_sin.shape[0]), int(cos_sin.shape[1])) if cos_sin is not None else (0, 0)
+        p = cls(_ptr(q_weight), _ptr(k_weight), float(eps), _ptr(cos_sin), n, rot, int(bool(interleaved)))
+        p._keep = (q_weight, k_weight, cos_sin)
+        return p
+
+
+def pa_norm_rope_write(desc, prep, q, k, v, positions, slot_mapping, q_out, k_cache, v_cache, stream=None):
+    """Norm and rotation of q [T][Hq][D] and k [T][Hkv][D], queries to q_out, k and v to the pools through int64
+    slots.  q, k, v may be slices of one projection's output (token stride above a row); positions: int32 [T]
+    (None without a rotation table); q_out contiguous, or q itself."""
+    who, device, dt = "pa_norm_rope_write", q.device, desc.q_torch_dtype
+    n, hkv, d = int(q.shape[0]), desc.num_kv_heads, desc.head_dim
+    qs = _rows(who, "q", q, dt, device, desc.num_q_heads, d, False)
+    ks = _rows(who, "k", k, dt, device, hkv, d, False)
+    vs = _rows(who, "v", v, dt, device, hkv, d, False)
+    _rows(who, "q_out", q_out, dt, device, desc.num_q_heads, d)
+    if k.shape[0] != n or v.shape[0] != n or q_out.shape[0] != n:
+        raise PaError(1, f"{who}: q, k, v and q_out differ in tokens")
+    _array(who, "slot_mapping", slot_mapping, torch.int64, device, (n,))
+    qw, kw, cs = prep._keep
+    if cs is not None:
+        _array(who, "cos_sin", cs, torch.float32, device, (prep.num_positions, prep.rot_dim))
+        if positions is None:
+            raise PaError(1, f"{who}: a rotation needs positions")
+    if positions is not None:
+        _array(who, "positions", positions, torch.int32, device, (n,))
+    for name, w in (("q_weight", qw), ("k_weight", kw)):
+        if w is not None:
+            _array(who, name, w, dt, device, (d,))
+    _pools(who, desc, k_cache, v_cache, device)
+    with _On(who, device, stream) as st:
+        _check(lib().pa_norm_rope_write(ctypes.byref(desc), ctypes.byref(prep), _ptr(q), qs, _ptr(k), ks, _ptr(v), vs,
+                                        _ptr(positions), _ptr(slot_mapping), n, _ptr(q_out), _ptr(k_cache),
+                                        _ptr(v_cache), st), who)
+
+
+def pa_cache_read(desc, slot_mapping, k_cache, v_cache, k_out, v_out, stream=None):
+    """Rows of int64 slots out of the pools into k_out, v_out [T][Hkv][D], dequantised."""
+    who, device, dt = "pa_cache_read", k_out.device, desc.q_torch_dtype
+    n = int(slot_mapping.shape[0])
+    _array(who, "slot_mapping", slot_mapping, torch.int64, device, (n,))
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        _array(who, name, t, dt, device, (n, desc.num_kv_heads, desc.head_dim))
+    _pools(who, desc, k_cache, v_cache, device)
+    with _On(who, device, stream) as st:
+        _check(lib().pa_cache_read(ctypes.byref(desc), _ptr(slot_mapping), n, _ptr(k_cache), _ptr(v_cache),
+                                   _ptr(k_out), _ptr(v_out), st), who)
+
+
 def pa_copy_blocks(desc, src, dst, k_cache, v_cache, stream=None):
     """Copy-on-write's device half: K/V block dst[i] := block src[i] (int32 device tensors)."""
     n = int(src.shape[0])

@@ -15,6 +15,8 @@ SIGNATURES = {
     "pa_version": (ctypes.c_char_p, []),
     "pa_block_bytes": (_SZ, [_P]),
     "pa_cache_write": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P, _P, _P]),
+    "pa_norm_rope_write": (ctypes.c_int, [_P, _P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I32, _P, _P, _P, _P]),
+    "pa_cache_read": (ctypes.c_int, [_P, _P, _I32, _P, _P, _P, _P, _P]),
     "pa_copy_blocks": (ctypes.c_int, [_P, _P, _P, _I32, _P, _P, _P]),
     "pa_decode_workspace_size": (_SZ, [_P, _I32]),
     "pa_decode": (ctypes.c_int, [_P, _P, _P, _P, _P, _I32, _P, _I32, _F, _P, _P, _SZ, _P]),

@@ -423,6 +423,125 @@ int pa_cache_write(const pa_cache_desc* d, const void* k_new, const void* v_new,
                      "pa_cache_write");
 }
 
+int pa_norm_rope_write(const pa_cache_desc* d, const pa_qk_prep* prep, const void* q, int64_t q_stride, const void* k,
+                       int64_t k_stride, const void* v, int64_t v_stride, const int32_t* positions,
+                       const int64_t* slot_mapping, int32_t num_tokens, void* q_out, void* k_cache, void* v_cache,
+                       void* stream) {
+  clear_error();
+  const char* who = "pa_norm_rope_write";
+  int rc = check_desc(d, who);
+  if (rc) return rc;
+  if (!prep) return fail(PA_ERR_INVALID_ARG, "%s: prep is NULL", who);
+  if (num_tokens < 0) return fail(PA_ERR_INVALID_ARG, "%s: num_tokens < 0", who);
+  if ((prep->q_weight || prep->k_weight) && !(std::isfinite(prep->eps) && prep->eps >= 0.f))
+    return fail(PA_ERR_INVALID_ARG, "%s: eps must be finite and >= 0", who);
+  if (prep->cos_sin) {
+    if (prep->num_positions <= 0) return fail(PA_ERR_INVALID_ARG, "%s: num_positions %d", who, prep->num_positions);
+    if (prep->rot_dim <= 0 || prep->rot_dim > d->head_dim || prep->rot_dim % 8)
+      return fail(PA_ERR_INVALID_ARG, "%s: rot_dim %d (a multiple of 8 up to head_dim %d)", who, prep->rot_dim,
+                  d->head_dim);
+    if (prep->interleaved != 0 && prep->interleaved != 1)
+      return fail(PA_ERR_INVALID_ARG, "%s: interleaved is 0 or 1", who);
+  }
+  if (d->kv_dtype != kFP8 && d->kv_dtype != d->q_dtype)
+    return fail(PA_ERR_UNSUPPORTED, "%s: q dtype %d into kv dtype %d", who, d->q_dtype, d->kv_dtype);
+  if (num_tokens == 0) return PA_OK;
+  if (!q || !k || !v || (prep->cos_sin && !positions) || !slot_mapping || !q_out || !k_cache || !v_cache)
+    return fail(PA_ERR_INVALID_ARG, "%s: NULL pointer", who);
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) || !aligned(k_cache, 16) ||
+      !aligned(v_cache, 16) || !aligned(positions, 4) || !aligned(slot_mapping, 8) || !aligned(prep->q_weight, 16) ||
+      !aligned(prep->k_weight, 16) || !aligned(prep->cos_sin, 16))
+    return fail(PA_ERR_INVALID_ARG, "%s: misaligned pointer", who);
+  const int64_t eb = elem_bytes(d->q_dtype);
+  const int64_t q_row = (int64_t)d->num_q_heads * d->head_dim, kv_row = (int64_t)d->num_kv_heads * d->head_dim;
+  const struct {
+    const void* p;
+    int64_t stride, row;
+  } in[3] = {{q, q_stride, q_row}, {k, k_stride, kv_row}, {v, v_stride, kv_row}};
+  const uintptr_t out0 = reinterpret_cast<uintptr_t>(q_out), out1 = out0 + (uintptr_t)(num_tokens * q_row * eb);
+  for (int i = 0; i < 3; ++i) {
+    if (in[i].stride < in[i].row || in[i].stride * eb % 16 || in[i].stride > (int64_t)1 << 28)
+      return fail(PA_ERR_INVALID_ARG, "%s: a token stride of %lld elements for rows of %lld", who,
+                  (long long)in[i].stride, (long long)in[i].row);
+    const uintptr_t a = reinterpret_cast<uintptr_t>(in[i].p);
+    const uintptr_t b = a + (uintptr_t)(((num_tokens - 1) * in[i].stride + in[i].row) * eb);
+    const bool in_place = i == 0 && q_out == q && q_stride == q_row;
+    if (a < out1 && out0 < b && !in_place)
+      return fail(PA_ERR_INVALID_ARG, "%s: q_out overlaps an input", who);
+  }
+  int sms = 0;
+  if ((rc = num_sms(&sms))) return rc;
+  NormRopeParams p = {};
+  p.q = static_cast<const uint8_t*>(q);
+  p.k = static_cast<const uint8_t*>(k);
+  p.v = static_cast<const uint8_t*>(v);
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.q_weight = static_cast<const uint8_t*>(prep->q_weight);
+  p.k_weight = static_cast<const uint8_t*>(prep->k_weight);
+  p.eps = prep->eps;
+  p.cos_sin = prep->cos_sin;
+  p.num_positions = prep->num_positions;
+  p.rot_dim = prep->cos_sin ? prep->rot_dim : 0;
+  p.interleaved = prep->interleaved;
+  p.positions = positions;
+  p.slots = slot_mapping;
+  p.q_out = static_cast<uint8_t*>(q_out);
+  p.k_cache = static_cast<uint8_t*>(k_cache);
+  p.v_cache = static_cast<uint8_t*>(v_cache);
+  p.num_tokens = num_tokens;
+  p.num_q_heads = d->num_q_heads;
+  p.num_kv_heads = d->num_kv_heads;
+  p.head_dim = d->head_dim;
+  p.block_size = d->block_size;
+  p.num_slots = (int64_t)d->num_blocks * d->block_size;
+  p.k_scale = d->k_scale;
+  p.v_scale = d->v_scale;
+  if (d->kv_dtype == kFP8) {
+    p.k_head = d->k_head_scales;
+    p.v_head = d->v_head_scales;
+  }
+  return cuda_status(launch_norm_rope_write(p, d->q_dtype, d->kv_dtype, sms, static_cast<cudaStream_t>(stream)), who);
+}
+
+int pa_cache_read(const pa_cache_desc* d, const int64_t* slot_mapping, int32_t num_tokens, const void* k_cache,
+                  const void* v_cache, void* k_out, void* v_out, void* stream) {
+  clear_error();
+  const char* who = "pa_cache_read";
+  int rc = check_desc(d, who);
+  if (rc) return rc;
+  if (num_tokens < 0) return fail(PA_ERR_INVALID_ARG, "%s: num_tokens < 0", who);
+  if (d->kv_dtype != kFP8 && d->kv_dtype != d->q_dtype)
+    return fail(PA_ERR_UNSUPPORTED, "%s: kv dtype %d into q dtype %d", who, d->kv_dtype, d->q_dtype);
+  if (num_tokens == 0) return PA_OK;
+  if (!slot_mapping || !k_cache || !v_cache || !k_out || !v_out)
+    return fail(PA_ERR_INVALID_ARG, "%s: NULL pointer", who);
+  if (!aligned(slot_mapping, 8) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_out, 16) ||
+      !aligned(v_out, 16))
+    return fail(PA_ERR_INVALID_ARG, "%s: misaligned pointer", who);
+  int sms = 0;
+  if ((rc = num_sms(&sms))) return rc;
+  CacheReadParams p = {};
+  p.slots = slot_mapping;
+  p.k_cache = static_cast<const uint8_t*>(k_cache);
+  p.v_cache = static_cast<const uint8_t*>(v_cache);
+  p.k_out = static_cast<uint8_t*>(k_out);
+  p.v_out = static_cast<uint8_t*>(v_out);
+  p.num_tokens = num_tokens;
+  p.num_kv_heads = d->num_kv_heads;
+  p.head_dim = d->head_dim;
+  p.block_size = d->block_size;
+  p.num_slots = (int64_t)d->num_blocks * d->block_size;
+  p.k_scale = d->k_scale;
+  p.v_scale = d->v_scale;
+  if (d->kv_dtype == kFP8) {
+    p.k_head = d->k_head_scales;
+    p.v_head = d->v_head_scales;
+  }
+  return cuda_status(launch_cache_read(p, d->q_dtype, d->kv_dtype, sms, static_cast<cudaStream_t>(stream)), who);
+}
+
 int pa_copy_blocks(const pa_cache_desc* d, const int32_t* src, const int32_t* dst, int32_t n, void* k_cache,
                    void* v_cache, void* stream) {
   clear_error();

@@ -24,6 +24,46 @@ struct CacheWriteParams {
 };
 cudaError_t launch_cache_write(const CacheWriteParams& p, int in_dtype, int kv_dtype, cudaStream_t stream);
 
+// pa_norm_rope_write: norms, rotation and cache write of a step's new rows.
+struct NormRopeParams {
+  const uint8_t* q;
+  const uint8_t* k;
+  const uint8_t* v;
+  int64_t q_stride, k_stride, v_stride;  // elements between tokens
+  const uint8_t* q_weight;               // [head_dim] or nullptr: no norm of the queries
+  const uint8_t* k_weight;               // [head_dim] or nullptr: no norm of the keys
+  float eps;
+  const float* cos_sin;  // [num_positions][rot_dim] or nullptr: no rotation
+  int32_t num_positions, rot_dim, interleaved;
+  const int32_t* positions;
+  const int64_t* slots;
+  uint8_t* q_out;
+  uint8_t* k_cache;
+  uint8_t* v_cache;
+  int32_t num_tokens, num_q_heads, num_kv_heads, head_dim, block_size;
+  int64_t num_slots;
+  float k_scale, v_scale;
+  const float* k_head;  // per-kv-head scales (device) or nullptr: k_scale / v_scale
+  const float* v_head;
+};
+cudaError_t launch_norm_rope_write(const NormRopeParams& p, int q_dtype, int kv_dtype, int num_sms,
+                                   cudaStream_t stream);
+
+// pa_cache_read: rows of given slots out of the pools.
+struct CacheReadParams {
+  const int64_t* slots;
+  const uint8_t* k_cache;
+  const uint8_t* v_cache;
+  uint8_t* k_out;
+  uint8_t* v_out;
+  int32_t num_tokens, num_kv_heads, head_dim, block_size;
+  int64_t num_slots;
+  float k_scale, v_scale;
+  const float* k_head;  // per-kv-head scales (device) or nullptr: k_scale / v_scale
+  const float* v_head;
+};
+cudaError_t launch_cache_read(const CacheReadParams& p, int q_dtype, int kv_dtype, int num_sms, cudaStream_t stream);
+
 // Whole-block copies inside both pools (copy-on-write): K and V block dst[i]
 // become copies of block src[i]; pairs with an id outside [0, num_blocks)
 // or src == dst are skipped.

@@ -1,0 +1,81 @@
+"""Refusals of the layer-step operators, on the host: bad arguments are turned
+down before anything is launched."""
+import ctypes
+
+import pytest
+import torch
+
+import paged_kv_cache_452_b200 as pa
+
+P = 4096  # an aligned address that is never read: every call here returns first
+
+
+def write(desc, prep, n=1, q=P, qs=1 << 14, k=2 * P, ks=1 << 14, v=3 * P, vs=1 << 14, pos=P, slots=P, out=1 << 30, kc=P,
+          vc=P):
+    return pa.lib().pa_norm_rope_write(ctypes.byref(desc) if desc is not None else None,
+                                       ctypes.byref(prep) if prep is not None else None, q, qs, k, ks, v, vs, pos, slots,
+                                       n, out, kc, vc, None)
+
+
+def prep_of(qw=P, kw=P, eps=1e-6, cs=P, npos=10, rot=64, inter=0):
+    return pa.QkPrep(qw, kw, eps, cs, npos, rot, inter)
+
+
+def test_norm_rope_write_refusals():
+    desc = pa.CacheDesc.make(16, 16, 2, 8, 64, "bf16", "bf16")
+    assert write(None, prep_of()) == 1
+    assert write(desc, None) == 1
+    assert write(desc, prep_of(), n=0) == 0 and write(desc, prep_of(), n=-1) == 1
+    for bad in (prep_of(eps=-1.0), prep_of(eps=float("nan")), prep_of(npos=0), prep_of(rot=0), prep_of(rot=12),
+                prep_of(rot=72), prep_of(inter=2), prep_of(qw=P + 8), prep_of(kw=P + 2), prep_of(cs=P + 4)):
+        assert write(desc, bad) == 1
+    for kw in (dict(q=None), dict(k=None), dict(v=None), dict(pos=None), dict(slots=None), dict(out=None), dict(kc=None),
+               dict(vc=None), dict(q=P + 8), dict(k=P + 2), dict(pos=P + 2), dict(slots=P + 4), dict(out=P + 4),
+               dict(qs=8 * 64 - 8), dict(ks=2 * 64 - 8), dict(vs=129), dict(qs=(1 << 28) + 8)):
+        assert write(desc, prep_of(), n=3, **kw) == 1, kw
+    # q_out over an input: in place only when q's rows lie end to end
+    assert write(desc, prep_of(), n=3, out=P) == 1
+    assert b"overlaps" in pa.lib().pa_last_error()
+    assert write(desc, prep_of(), n=3, out=2 * P + 16) == 1
+    assert write(pa.CacheDesc.make(16, 16, 2, 8, 64, "f32", "bf16"), prep_of()) == 2
+    assert write(pa.CacheDesc.make(16, 16, 2, 8, 96, "bf16", "bf16"), prep_of()) == 2
+
+
+def test_cache_read_refusals():
+    desc = pa.CacheDesc.make(16, 16, 2, 8, 64, "bf16", "bf16")
+
+    def read(d, n=1, slots=P, kc=P, vc=P, ko=P, vo=P):
+        return pa.lib().pa_cache_read(ctypes.byref(d) if d is not None else None, slots, n, kc, vc, ko, vo, None)
+    assert read(None) == 1 and read(desc, n=-1) == 1 and read(desc, n=0) == 0
+    for kw in (dict(slots=None), dict(kc=None), dict(vc=None), dict(ko=None), dict(vo=None), dict(slots=P + 4),
+               dict(ko=P + 8), dict(vc=P + 2)):
+        assert read(desc, **kw) == 1, kw
+    assert read(pa.CacheDesc.make(16, 16, 2, 8, 64, "bf16", "f32")) == 2
+
+
+def test_bindings_refuse_wrong_tensors():
+    desc = pa.CacheDesc.make(4, 16, 2, 8, 64, "bf16", "bf16")
+    bf = torch.bfloat16
+    kc, vc = pa.alloc_cache(desc, "cpu")
+    q, k, v, out = (torch.zeros((3, h, 64), dtype=bf) for h in (8, 2, 2, 8))
+    slots, pos = torch.zeros(3, dtype=torch.int64), torch.zeros(3, dtype=torch.int32)
+    cs, w = torch.zeros((10, 64)), torch.zeros(64, dtype=bf)
+    prep = pa.QkPrep.make(w, w, 1e-6, cs)
+    good = dict(q=q, k=k, v=v, positions=pos, slot_mapping=slots, q_out=out, k_cache=kc, v_cache=vc)
+    with pytest.raises(pa.PaError, match="CUDA device"):  # all well but for the place
+        pa.pa_norm_rope_write(desc, prep, **good)
+    for bad in (dict(q=q.float()), dict(k=k[:2]), dict(v=v[:, :1]), dict(q=q.transpose(1, 2)), dict(slot_mapping=pos),
+                dict(positions=slots), dict(positions=None), dict(q_out=out[:, :, ::2]), dict(k_cache=kc[:3]),
+                dict(v_cache=vc.float()), dict(q_out=torch.zeros((3, 16, 64), dtype=bf)[:, ::2])):
+        with pytest.raises(pa.PaError, match="pa_norm_rope_write"):
+            pa.pa_norm_rope_write(desc, prep, **{**good, **bad})
+        assert "CUDA device" not in str(pytest.raises(pa.PaError, pa.pa_norm_rope_write, desc, prep,
+                                                      **{**good, **bad}).value)
+    with pytest.raises(pa.PaError, match="q_weight"):
+        pa.pa_norm_rope_write(desc, pa.QkPrep.make(w.float(), w, 1e-6, cs), **good)
+    with pytest.raises(pa.PaError, match="cos_sin"):
+        pa.pa_norm_rope_write(desc, pa.QkPrep.make(w, w, 1e-6, cs.double()), **good)
+    with pytest.raises(pa.PaError, match="k_out"):
+        pa.pa_cache_read(desc, slots, kc, vc, k[:2], v)
+    with pytest.raises(pa.PaError, match="CUDA device"):
+        pa.pa_cache_read(desc, slots, kc, vc, k, v)
