@@ -356,6 +356,52 @@ int pa_decode_chunked_prefill(const pa_cache_desc* desc, const void* q, const vo
                               int32_t max_q_len, float scale, void* out, void* workspace,
                               size_t workspace_bytes, void* stream);
 
+/* ---- biased attention -----------------------------------------------------
+ * Attention whose scores are capped, biased by distance, or masked by a
+ * sliding window and an always-visible prefix.  Query head h's row at
+ * position i sees key j (0 <= j < seq_lens[s]) if
+ *     j < prefix_lens[s],  or  j <= i and (window == 0 or i - j < window);
+ * its score is
+ *     softcap * tanh(scale * q_i k_j / softcap) - slopes[h] * |i - j|
+ * (softcap 0: scale * q_i k_j), and the output is the softmax over the visible
+ * keys.  Without prefix and window that is pa_decode's causal attention. */
+typedef struct {
+  float softcap;              /* 0 (none), or positive and finite */
+  int32_t window;             /* 0 (none), or the keys a row sees up to itself, itself included */
+  const float* slopes;        /* NULL (none), or device fp32 [num_q_heads], finite */
+  const int32_t* prefix_lens; /* NULL (none), or device int32 [num_seqs]: keys 0 .. prefix_lens[s] - 1 are
+                                 seen by every row of sequence s, rows before them included (two-way
+                                 attention inside a prompt's prefix) and rows past the window (kept first
+                                 tokens); taken as 0 below 0 and as seq_lens[s] above it */
+} pa_score_mod;
+
+/* Scratch bytes pa_decode_biased and pa_decode_chunked_prefill_biased need. */
+size_t pa_biased_workspace_size(const pa_cache_desc* desc, int32_t num_seqs, int32_t num_tokens);
+
+/* pa_decode_biased: pa_decode under `mod`: sequence s's query row sits at
+ * position seq_lens[s] - 1.  Blocks between a sequence's prefix and its
+ * window are not read, and their table entries may hold anything.
+ * Arguments, errors, the workspace (sized by pa_biased_workspace_size) and its
+ * error word as for pa_decode; `scale` positive and finite.  bf16 queries over
+ * a bf16 or e4m3 pool run on the tensor cores for every group and head_dim,
+ * fp32 queries on CUDA cores.  V rows that no query of the sequence sees may
+ * hold anything, NaN included. */
+int pa_decode_biased(const pa_cache_desc* desc, const pa_score_mod* mod, const void* q, const void* k_cache,
+                     const void* v_cache, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                     const int32_t* seq_lens, int32_t num_seqs, float scale, void* out, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/* pa_decode_chunked_prefill_biased: pa_decode_chunked_prefill under `mod`, for
+ * a mixed step.  A prefix may reach past a row's own position, up to the
+ * sequence's last token (whose K/V are in the pool).  Arguments, errors and
+ * the workspace as for pa_decode_chunked_prefill and pa_decode_biased. */
+int pa_decode_chunked_prefill_biased(const pa_cache_desc* desc, const pa_score_mod* mod, const void* q,
+                                     const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                                     int32_t max_blocks_per_seq, const int32_t* query_start_loc,
+                                     const int32_t* seq_lens, int32_t num_seqs, int32_t num_tokens,
+                                     int32_t max_q_len, float scale, void* out, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
 /* ---- host block pool --------------------------------------------------------
  * The block manager of "PagedAttention：KV cache 即虚拟内存（block manager &
  * 碎片）", section 深入原理: free_block_queue is a doubly linked list in

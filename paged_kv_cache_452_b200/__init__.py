@@ -338,6 +338,75 @@ def pa_decode_prefix(desc, q, k_cache, v_cache, block_tables, seq_lens, groups, 
         int(workspace.numel() * workspace.element_size()), _stream(stream)), "pa_decode_prefix")
 
 
+class ScoreMod(ctypes.Structure):
+    """pa_score_mod: what the biased attention does to the scores (keeps its tensors alive)."""
+    _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int32), ("slopes", ctypes.c_void_p),
+                ("prefix_lens", ctypes.c_void_p)]
+
+    @classmethod
+    def make(cls, softcap=0.0, window=0, slopes=None, prefix_lens=None):
+        """softcap: cap * tanh(score / cap), 0 for none; window: keys a row sees up to itself, 0 for all; slopes:
+        device fp32 [num_q_heads], the score loses slope * distance; prefix_lens: device int32 [num_seqs], leading
+        keys that every row sees."""
+        m = cls(float(softcap), int(window), _ptr(slopes), _ptr(prefix_lens))
+        m._keep = (slopes, prefix_lens)
+        return m
+
+
+def pa_biased_workspace_size(desc, num_seqs, num_tokens) -> int:
+    n = int(lib().pa_biased_workspace_size(ctypes.byref(desc), int(num_seqs), int(num_tokens)))
+    if n == 0:
+        raise PaError(1, "pa_biased_workspace_size: " + lib().pa_last_error().decode())
+    return n
+
+
+def _biased_args(who, desc, mod, q, k_cache, v_cache, block_tables, seq_lens, out, workspace):
+    device, dt = q.device, desc.q_torch_dtype
+    shape = (q.shape[0], desc.num_q_heads, desc.head_dim)
+    _array(who, "q", q, dt, device, shape)
+    _array(who, "out", out, dt, device, shape)
+    n = int(seq_lens.shape[0])
+    _array(who, "seq_lens", seq_lens, torch.int32, device, (n,))
+    if block_tables.dim() != 2:
+        raise PaError(1, f"{who}: block_tables must be [num_seqs][max_blocks]")
+    _array(who, "block_tables", block_tables, torch.int32, device, (n, block_tables.shape[1]))
+    slopes, prefix = mod._keep
+    if slopes is not None:
+        _array(who, "slopes", slopes, torch.float32, device, (desc.num_q_heads,))
+    if prefix is not None:
+        _array(who, "prefix_lens", prefix, torch.int32, device, (n,))
+    if workspace.device != device or not workspace.is_contiguous():
+        raise PaError(1, f"{who}: workspace must be contiguous on {device}")
+    _pools(who, desc, k_cache, v_cache, device)
+    return device, n
+
+
+def pa_decode_biased(desc, mod, q, k_cache, v_cache, block_tables, seq_lens, scale, out, workspace, stream=None):
+    """pa_decode with capped, distance-biased or window- and prefix-masked scores (mod: a ScoreMod)."""
+    who = "pa_decode_biased"
+    device, s = _biased_args(who, desc, mod, q, k_cache, v_cache, block_tables, seq_lens, out, workspace)
+    if q.shape[0] != s:
+        raise PaError(1, f"{who}: {q.shape[0]} query rows for {s} sequences")
+    with _On(who, device, stream) as st:
+        _check(lib().pa_decode_biased(ctypes.byref(desc), ctypes.byref(mod), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                      _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens), s, float(scale),
+                                      _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(), st),
+               who)
+
+
+def pa_decode_chunked_prefill_biased(desc, mod, q, k_cache, v_cache, block_tables, query_start_loc, seq_lens,
+                                     max_q_len, scale, out, workspace, stream=None):
+    """pa_decode_chunked_prefill with capped, distance-biased or window- and prefix-masked scores (mod: a ScoreMod)."""
+    who = "pa_decode_chunked_prefill_biased"
+    device, s = _biased_args(who, desc, mod, q, k_cache, v_cache, block_tables, seq_lens, out, workspace)
+    _array(who, "query_start_loc", query_start_loc, torch.int32, device, (s + 1,))
+    with _On(who, device, stream) as st:
+        _check(lib().pa_decode_chunked_prefill_biased(
+            ctypes.byref(desc), ctypes.byref(mod), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+            block_tables.shape[1], _ptr(query_start_loc), _ptr(seq_lens), s, q.shape[0], int(max_q_len), float(scale),
+            _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(), st), who)
+
+
 def default_scale(head_dim):
     return 1.0 / math.sqrt(head_dim)
 

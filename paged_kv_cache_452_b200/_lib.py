@@ -29,6 +29,10 @@ SIGNATURES = {
                                         _F, _P, _P, _SZ, _P]),
     "pa_decode_chunked_prefill": (ctypes.c_int,
                                   [_P, _P, _P, _P, _P, _I32, _P, _P, _I32, _I32, _I32, _F, _P, _P, _SZ, _P]),
+    "pa_biased_workspace_size": (_SZ, [_P, _I32, _I32]),
+    "pa_decode_biased": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _I32, _P, _I32, _F, _P, _P, _SZ, _P]),
+    "pa_decode_chunked_prefill_biased": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _I32, _P, _P, _I32, _I32, _I32, _F,
+                                                        _P, _P, _SZ, _P]),
     "pa_pool_create": (ctypes.c_int, [_I32, _I32, _P, _P]),
     "pa_pool_destroy": (None, [_P]),
     "pa_pool_add_seq": (ctypes.c_int, [_P, _I64, _P, _I32, _P]),

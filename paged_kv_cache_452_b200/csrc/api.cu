@@ -142,7 +142,8 @@ int encode_kv_map(CUtensorMap* m, const void* base, int dt, const pa_cache_desc*
   const int eb = elem_bytes(dt);
   cuuint64_t dims[2] = {(cuuint64_t)d->head_dim, (cuuint64_t)d->num_blocks * d->num_kv_heads * d->block_size};
   cuuint64_t strides[1] = {(cuuint64_t)d->head_dim * eb};
-  cuuint32_t box[2] = {(cuuint32_t)(128 / eb), (cuuint32_t)d->block_size};
+  const int row = d->head_dim * eb;  // 64-byte rows (e4m3, head_dim 64) take boxes of 64 bytes and their swizzle
+  cuuint32_t box[2] = {(cuuint32_t)((row < 128 ? row : 128) / eb), (cuuint32_t)d->block_size};
   cuuint32_t estr[2] = {1, 1};
   // the row stride must step over a whole row and stay a multiple of 16
   // bytes: a map whose strides overlap or shrink is refused before encoding
@@ -151,8 +152,8 @@ int encode_kv_map(CUtensorMap* m, const void* base, int dt, const pa_cache_desc*
                 (unsigned long long)strides[0], (unsigned long long)(dims[0] * eb));
   CUresult r = enc(m, dt == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
                    const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                   row < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   return PA_OK;
 }
@@ -161,10 +162,9 @@ int encode_kv_map(CUtensorMap* m, const void* base, int dt, const pa_cache_desc*
 // kernel: a box is [128 / G tokens][G heads][64 elements], 128-byte swizzle,
 // so one box fills one 64-column chunk of a unit's Q tile in row order
 // (position-major, group head minor).
-int encode_q_map(CUtensorMap* m, const void* q, int num_tokens, const pa_cache_desc* d) {
+int encode_q_map(CUtensorMap* m, const void* q, int num_tokens, const pa_cache_desc* d, int group) {
   auto enc = encode_fn();
   if (!enc) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
-  const int group = d->num_q_heads / d->num_kv_heads;
   cuuint64_t dims[3] = {(cuuint64_t)d->head_dim, (cuuint64_t)d->num_q_heads, (cuuint64_t)num_tokens};
   // each stride steps over the whole previous dimension: rows do not overlap
   cuuint64_t strides[2] = {(cuuint64_t)d->head_dim * 2, (cuuint64_t)d->num_q_heads * d->head_dim * 2};
@@ -348,6 +348,173 @@ int run_simt(const pa_cache_desc* d, const void* q, const void* k_cache, const v
   cudaError_t e = launch_attn_simt(p, d->q_dtype, d->kv_dtype, stream);
   if (e == cudaErrorNotSupported)
     return fail(PA_ERR_UNSUPPORTED, "%s: q dtype %d with kv dtype %d", who, d->q_dtype, d->kv_dtype);
+  return cuda_status(e, who);
+}
+
+// The biased attention's kernels cut a group that is too large for them into
+// equal parts, each a kernel kv head of its own: the largest divisor up to
+// `most` (8 query columns of the decode kernel, 128 rows of the chunk kernel).
+int cut_group(int group, int most) {
+  int g = group < most ? group : most;
+  while (group % g) --g;
+  return g;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+ScoreMod kernel_mod(const pa_score_mod* m, float scale, float k_scale) {
+  ScoreMod k = {};
+  if (m->softcap > 0.f) {
+    k.cap_in = 2.f * kLog2e * scale * k_scale / m->softcap;
+    k.cap_out = kLog2e * m->softcap;
+  }
+  k.window = m->window;
+  k.slopes = m->slopes;
+  k.prefix = m->prefix_lens;
+  k.sub = 1;
+  return k;
+}
+
+int check_mod(const pa_score_mod* m, float scale, const pa_cache_desc* d, int32_t max_blocks, const char* who) {
+  if (!m) return fail(PA_ERR_INVALID_ARG, "%s: mod is NULL", who);
+  if (!(m->softcap >= 0.f) || !std::isfinite(m->softcap))
+    return fail(PA_ERR_INVALID_ARG, "%s: softcap must be 0 or positive and finite", who);
+  if (m->window < 0) return fail(PA_ERR_INVALID_ARG, "%s: window < 0", who);
+  if (!(scale > 0.f) || !std::isfinite(scale))
+    return fail(PA_ERR_INVALID_ARG, "%s: scale must be positive and finite", who);
+  if (!aligned(m->slopes, 4) || !aligned(m->prefix_lens, 4))
+    return fail(PA_ERR_INVALID_ARG, "%s: misaligned slopes or prefix_lens", who);
+  if ((int64_t)max_blocks * d->block_size >= (int64_t)INT32_MAX)
+    return fail(PA_ERR_UNSUPPORTED, "%s: table rows of 2^31 tokens", who);
+  return PA_OK;
+}
+
+bool biased_tc(const pa_cache_desc* d) { return d->q_dtype == kBF16 && d->kv_dtype != kF32; }
+
+// Single-token rows of a biased step on the tensor-core decode (qsl null:
+// every row).
+int run_decode_biased(const pa_cache_desc* d, const pa_score_mod* mod, const void* q, const void* k_cache,
+                      const void* v_cache, const int32_t* block_tables, int32_t max_blocks, const int32_t* seq_lens,
+                      const int32_t* qsl, int32_t num_seqs, int32_t num_rows, float scale, void* out, void* workspace,
+                      size_t workspace_bytes, cudaStream_t stream, const char* who) {
+  int sms = 0;
+  int rc = num_sms(&sms);
+  if (rc) return rc;
+  const int group = d->num_q_heads / d->num_kv_heads, cut = cut_group(group, 8);
+  const int heads = d->num_q_heads / cut;
+  if ((int64_t)num_seqs * max_blocks * heads >= (int64_t)INT32_MAX)
+    return fail(PA_ERR_UNSUPPORTED, "%s: num_seqs * max_blocks_per_seq * heads reaches 2^31", who);
+  WsCarve c = carve(workspace, num_seqs, heads, cut, d->head_dim, sms);
+  if (workspace_bytes < c.bytes)
+    return fail(PA_ERR_INVALID_ARG, "%s: workspace %zu < %zu bytes", who, workspace_bytes, c.bytes);
+  CUtensorMap tm_k, tm_v;
+  if ((rc = make_kv_map(&tm_k, k_cache, d->kv_dtype, d))) return rc;
+  if (d->kv_dtype == kBF16) {
+    if ((rc = make_kv_map(&tm_v, v_cache, d->kv_dtype, d))) return rc;
+  } else {
+    tm_v = tm_k;  // e4m3 V tiles are contiguous and come by bulk copy
+  }
+  const bool fp8 = d->kv_dtype == kFP8;
+  const float k_scale = fp8 && !d->k_head_scales ? d->k_scale : 1.f;
+  DecodeParams p = {};
+  p.q = static_cast<const uint8_t*>(q);
+  p.out = static_cast<uint8_t*>(out);
+  p.v_cache = static_cast<const uint8_t*>(v_cache);
+  p.block_tables = block_tables;
+  p.max_blocks = max_blocks;
+  p.rows.seq_lens = seq_lens;
+  p.rows.qsl = qsl;
+  p.rows.num_seqs = num_seqs;
+  p.rows.num_rows = num_rows;
+  p.num_q_heads = d->num_q_heads;
+  p.num_kv_heads = heads;
+  p.num_blocks = d->num_blocks;
+  p.group = cut;
+  p.scale_log2 = scale * kLog2e * k_scale;
+  p.out_scale = fp8 && !d->v_head_scales ? d->v_scale : 1.f;
+  p.k_head = fp8 ? d->k_head_scales : nullptr;
+  p.v_head = fp8 ? d->v_head_scales : nullptr;
+  p.mod = kernel_mod(mod, scale, k_scale);
+  p.mod.sub = group / cut;
+  p.ws = c.ws;
+  cudaError_t e = launch_decode_biased(p, tm_k, tm_v, d->kv_dtype, d->head_dim, d->block_size, sms, stream);
+  if (e == cudaErrorNotSupported) return fail(PA_ERR_UNSUPPORTED, "%s: too many sequences for one launch", who);
+  return cuda_status(e, who);
+}
+
+// Chunk rows (more than one per sequence) of a biased step on tcgen05.
+int run_prefill_biased(const pa_cache_desc* d, const pa_score_mod* mod, const void* q, const void* k_cache,
+                       const void* v_cache, const int32_t* block_tables, int32_t max_blocks, const int32_t* qsl,
+                       const int32_t* seq_lens, int32_t num_seqs, int32_t num_tokens, float scale, bool after_decode,
+                       void* out, void* workspace, cudaStream_t stream, const char* who) {
+  int sms = 0;
+  int rc = num_sms(&sms);
+  if (rc) return rc;
+  const int group = d->num_q_heads / d->num_kv_heads, cut = cut_group(group, 128);
+  CUtensorMap tm_k, tm_v, tm_q;
+  if ((rc = make_kv_map(&tm_k, k_cache, d->kv_dtype, d))) return rc;
+  if ((rc = make_kv_map(&tm_v, v_cache, d->kv_dtype, d))) return rc;
+  if ((rc = encode_q_map(&tm_q, q, num_tokens, d, cut))) return rc;
+  PrefillParams p = {};
+  p.q = static_cast<const uint8_t*>(q);
+  p.out = static_cast<uint8_t*>(out);
+  p.block_tables = block_tables;
+  p.max_blocks = max_blocks;
+  p.rows.seq_lens = seq_lens;
+  p.rows.qsl = qsl;
+  p.rows.num_seqs = num_seqs;
+  p.rows.num_rows = num_tokens;
+  p.num_q_heads = d->num_q_heads;
+  p.num_kv_heads = d->num_q_heads / cut;
+  p.group = cut;
+  p.num_blocks = d->num_blocks;
+  p.scale_log2 = scale * kLog2e;
+  p.out_scale = 1.f;
+  p.mod = kernel_mod(mod, scale, 1.f);
+  p.mod.sub = group / cut;
+  p.err = static_cast<int32_t*>(workspace);
+  p.unit_ctr = static_cast<int32_t*>(workspace) + 2;
+  p.unit_exit = static_cast<int32_t*>(workspace) + 3;
+  p.after_decode = after_decode;
+  cudaError_t e = launch_prefill_biased(p, tm_k, tm_v, tm_q, d->kv_dtype, d->head_dim, d->block_size, num_tokens, sms,
+                                        stream);
+  if (e == cudaErrorNotSupported) return fail(PA_ERR_UNSUPPORTED, "%s: too many sequences for one launch", who);
+  return cuda_status(e, who);
+}
+
+int run_biased_simt(const pa_cache_desc* d, const pa_score_mod* mod, const void* q, const void* k_cache,
+                    const void* v_cache, const int32_t* block_tables, int32_t max_blocks, const int32_t* seq_lens,
+                    const int32_t* qsl, int32_t num_seqs, int32_t num_rows, float scale, void* out, void* workspace,
+                    cudaStream_t stream, const char* who) {
+  BiasedSimtParams b = {};
+  SimtParams& p = b.a;
+  p.num_blocks = d->num_blocks;
+  p.err = static_cast<int32_t*>(workspace);
+  p.q = static_cast<const uint8_t*>(q);
+  p.out = static_cast<uint8_t*>(out);
+  p.k_cache = static_cast<const uint8_t*>(k_cache);
+  p.v_cache = static_cast<const uint8_t*>(v_cache);
+  p.block_tables = block_tables;
+  p.max_blocks = max_blocks;
+  p.rows.seq_lens = seq_lens;
+  p.rows.qsl = qsl;
+  p.rows.num_seqs = num_seqs;
+  p.rows.num_rows = num_rows;
+  p.num_q_heads = d->num_q_heads;
+  p.num_kv_heads = d->num_kv_heads;
+  p.head_dim = d->head_dim;
+  p.block_size = d->block_size;
+  p.scale = scale;
+  p.k_scale = d->k_scale;
+  p.v_scale = d->v_scale;
+  if (d->kv_dtype == kFP8) {
+    p.k_head = d->k_head_scales;
+    p.v_head = d->v_head_scales;
+  }
+  b.mod = kernel_mod(mod, scale, 1.f);
+  cudaError_t e = launch_attn_biased_simt(b, d->q_dtype, d->kv_dtype, stream);
+  if (e == cudaErrorNotSupported)
+    return fail(PA_ERR_UNSUPPORTED, "%s: q dtype %d with kv dtype %d, %d rows", who, d->q_dtype, d->kv_dtype, num_rows);
   return cuda_status(e, who);
 }
 
@@ -740,7 +907,7 @@ int pa_decode_chunked_prefill(const pa_cache_desc* d, const void* q, const void*
       if ((rc = num_sms(&sms))) return rc;
       if (umma) {
         CUtensorMap tm_q;
-        if ((rc = encode_q_map(&tm_q, q, num_tokens, d))) return rc;
+        if ((rc = encode_q_map(&tm_q, q, num_tokens, d, group))) return rc;
         e = launch_prefill_umma(pp, tm_k, tm_v, tm_q, d->head_dim, d->block_size, num_tokens, sms, st);
       }
       if (e == cudaErrorNotSupported && prefill_tc_supported(d->kv_dtype, d->q_dtype, d->head_dim, d->block_size, group))
@@ -753,6 +920,77 @@ int pa_decode_chunked_prefill(const pa_cache_desc* d, const void* q, const void*
   if (workspace_bytes < 256) return fail(PA_ERR_INVALID_ARG, "%s: workspace < 256 bytes", who);
   return run_simt(d, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, query_start_loc, num_seqs,
                   num_tokens, 0, scale, out, workspace, st, who);
+}
+
+size_t pa_biased_workspace_size(const pa_cache_desc* d, int32_t num_seqs, int32_t num_tokens) {
+  clear_error();
+  if (check_desc(d, "pa_biased_workspace_size")) return 0;
+  if (num_seqs < 0 || num_tokens < 0) {
+    fail(PA_ERR_INVALID_ARG, "pa_biased_workspace_size: negative size");
+    return 0;
+  }
+  if (!biased_tc(d)) return 256;
+  int sms = 0;
+  if (num_sms(&sms)) return 0;
+  const int cut = cut_group(d->num_q_heads / d->num_kv_heads, 8);
+  return decode_tc_workspace_bytes(num_seqs, d->num_q_heads / cut, cut, d->head_dim, sms);
+}
+
+int pa_decode_biased(const pa_cache_desc* d, const pa_score_mod* mod, const void* q, const void* k_cache,
+                     const void* v_cache, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                     const int32_t* seq_lens, int32_t num_seqs, float scale, void* out, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+  clear_error();
+  const char* who = "pa_decode_biased";
+  int rc = check_attn_args(d, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, num_seqs, out,
+                           workspace, who);
+  if (rc) return rc;
+  if ((rc = check_mod(mod, scale, d, max_blocks_per_seq, who)) || num_seqs == 0) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (biased_tc(d))
+    return run_decode_biased(d, mod, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, nullptr, num_seqs,
+                             num_seqs, scale, out, workspace, workspace_bytes, st, who);
+  if (workspace_bytes < 256) return fail(PA_ERR_INVALID_ARG, "%s: workspace < 256 bytes", who);
+  return run_biased_simt(d, mod, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, nullptr, num_seqs,
+                         num_seqs, scale, out, workspace, st, who);
+}
+
+int pa_decode_chunked_prefill_biased(const pa_cache_desc* d, const pa_score_mod* mod, const void* q,
+                                     const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                                     int32_t max_blocks_per_seq, const int32_t* query_start_loc,
+                                     const int32_t* seq_lens, int32_t num_seqs, int32_t num_tokens,
+                                     int32_t max_q_len, float scale, void* out, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+  clear_error();
+  const char* who = "pa_decode_chunked_prefill_biased";
+  int rc = check_attn_args(d, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, num_seqs, out,
+                           workspace, who);
+  if (rc) return rc;
+  if ((rc = check_mod(mod, scale, d, max_blocks_per_seq, who)) || num_seqs == 0) return rc;
+  if (!query_start_loc || !aligned(query_start_loc, 4)) return fail(PA_ERR_INVALID_ARG, "%s: bad query_start_loc", who);
+  if (num_tokens < 0 || max_q_len < 0) return fail(PA_ERR_INVALID_ARG, "%s: negative size", who);
+  if (num_tokens == 0) return PA_OK;
+  if (max_q_len == 0) return fail(PA_ERR_INVALID_ARG, "%s: max_q_len 0 with %d tokens", who, num_tokens);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (!biased_tc(d) || d->kv_dtype == kFP8) {
+    if (workspace_bytes < 256) return fail(PA_ERR_INVALID_ARG, "%s: workspace < 256 bytes", who);
+    return run_biased_simt(d, mod, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, query_start_loc,
+                           num_seqs, num_tokens, scale, out, workspace, st, who);
+  }
+  // single-token rows on the decode kernel (there are none when the rows fill
+  // every sequence up to max_q_len), the others on the chunk kernel
+  const bool decodes = max_q_len == 1 || (int64_t)num_seqs * max_q_len != num_tokens;
+  const size_t need = pa_biased_workspace_size(d, num_seqs, num_tokens);
+  if (need == 0) return PA_ERR_INVALID_ARG;  // the size query recorded why
+  if (workspace_bytes < need)
+    return fail(PA_ERR_INVALID_ARG, "%s: workspace %zu < %zu bytes", who, workspace_bytes, need);
+  if (decodes) {
+    rc = run_decode_biased(d, mod, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, query_start_loc,
+                           num_seqs, num_tokens, scale, out, workspace, workspace_bytes, st, who);
+    if (rc || max_q_len == 1) return rc;
+  }
+  return run_prefill_biased(d, mod, q, k_cache, v_cache, block_tables, max_blocks_per_seq, query_start_loc, seq_lens,
+                            num_seqs, num_tokens, scale, decodes, out, workspace, st, who);
 }
 
 }  // extern "C"

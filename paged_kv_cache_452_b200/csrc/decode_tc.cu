@@ -66,11 +66,16 @@ struct Cfg {
   static constexpr int ROW = D * ELEM;   // bytes per token row
   static constexpr int TILE = BS * ROW;  // bytes of one K (or V) tile
   static constexpr int KVB = 2 * TILE;   // K and V tiles of a stage
-  static constexpr int NCH = ROW / 128;  // 128-byte chunks per K/V row
+  static constexpr int NCH = (ROW + 127) / 128;  // 128-byte chunks per K/V row
   static constexpr int KM = BS / 16;     // 16-key m-tiles per tile
   static constexpr int DM = D / 16;      // 16-d m-tiles of O^T
   static constexpr int KSTEPS = D / 16;  // k-steps of S^T = K Q^T
-  static_assert(ROW % 128 == 0, "rows must be whole 128-byte swizzle rows");
+  static_assert(ROW % 128 == 0 || (FP8 && ROW == 64), "rows must be whole 128-byte (e4m3: or 64-byte) swizzle rows");
+  // byte offset of 16-byte unit u of key `key` in an e4m3 K tile: 128-byte
+  // swizzle, or for 64-byte rows the 64-byte one
+  static __device__ __forceinline__ int k8(int key, int u) {
+    return ROW == 64 ? key * 64 + ((u ^ ((key >> 1) & 3)) << 4) : key * 128 + ((u ^ (key & 7)) << 4);
+  }
   static_assert(BS % 16 == 0, "block size must be a multiple of 16");
 };
 
@@ -134,6 +139,23 @@ __device__ __forceinline__ int seq_skip(const DecodeParams& p, bool pfx, int s) 
   if (!pfx) return 0;
   const int pf = __ldg(p.pfx_of + s);
   return pf >= 0 ? __ldg(p.pfx_blocks + pf) : 0;
+}
+
+// The biased decode's view of sequence s (its query at position len - 1): a
+// row's blocks [0, np) hold visible prefix keys, blocks [np + gap, end) the
+// window's; the gap between them is not read.
+struct Span {
+  int pfx, lo;  // visible keys: [0, pfx) and [lo, len)
+  int np, gap;  // blocks
+};
+template <int BS>
+__device__ __forceinline__ Span seq_span(const DecodeParams& p, int s, int len) {
+  Span v;
+  v.pfx = p.mod.prefix ? max(0, min(len, __ldg(p.mod.prefix + s))) : 0;
+  v.lo = p.mod.window > 0 ? max(0, len - p.mod.window) : 0;
+  v.np = (v.pfx + BS - 1) / BS;
+  v.gap = max(0, v.lo / BS - v.np);
+  return v;
 }
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -215,7 +237,10 @@ __device__ __forceinline__ void fused_write(const DecodeParams& p, uint8_t* st, 
   }
 }
 
-template <int KV, int D, int BS>
+// MOD: the biased form (pa_decode_biased): p.mod's cap, distance bias, window
+// and prefix; p.num_kv_heads counts cut groups (mod.sub of them share a pool
+// kv head), so that any group takes this kernel.
+template <int KV, int D, int BS, bool MOD>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm<KV>())
     decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const DecodeParams p) {
@@ -227,7 +252,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<KV>())
   const int hkv = p.num_kv_heads, G = p.group, hq = p.num_q_heads;
   const int QA = q_area_bytes(G, D);
   const int STAGE = C::KVB + QA;  // bytes per ring stage
-  const bool pfx = p.pfx_of != nullptr;
+  const bool pfx = !MOD && p.pfx_of != nullptr;
+  const int pool_heads = MOD ? hkv / p.mod.sub : hkv;  // kv heads of the pool
   const SmemLayout L = smem_layout(STAGE, NSW, S);
   int32_t* prefix = reinterpret_cast<int32_t*>(smem + L.prefix);
   __shared__ int32_t warp_tot[kWarps];
@@ -250,6 +276,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<KV>())
     if (nb > p.max_blocks) {  // context longer than its table row: flag, clamp
       atomicCAS(p.ws.err, 0, 3);
       nb = p.max_blocks;
+    }
+    if constexpr (MOD) {
+      if (nb > 0) nb -= seq_span<BS>(p, s, min(len, nb * BS)).gap;
     }
     if (pfx) {
       // a shared prefix's blocks are attended by the prefix kernel: only the
@@ -348,15 +377,22 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<KV>())
       const int local = t - hkv * prefix[s];
       d.h = local / nb;
       const int skip = seq_skip(p, pfx, s);
-      const int i = local - d.h * nb + skip;
+      int i = local - d.h * nb + skip;
+      const bool opens = i == skip || t == wbeg;
+      int end = nb + skip;  // blocks of the row up to its context's end
+      if constexpr (MOD) {
+        const Span sp = seq_span<BS>(p, s, min(__ldg(p.rows.seq_lens + s), p.max_blocks * BS));
+        if (i >= sp.np) i += sp.gap;
+        end += sp.gap;
+      }
       d.blk = __ldg(p.block_tables + (int64_t)s * p.max_blocks + i);
       if (d.blk < 0 || d.blk >= p.num_blocks) {  // bad table entry: flag, read block 0
         atomicCAS(p.ws.err, 0, 2);
         d.blk = 0;
       }
-      if (i == skip || t == wbeg) {  // the tile opens a piece
+      if (opens) {  // the tile opens a piece
         d.row = p.rows.qsl ? __ldg(p.rows.qsl + s) : s;
-        d.len = min(__ldg(p.rows.seq_lens + s), (nb + skip) * BS);
+        d.len = min(__ldg(p.rows.seq_lens + s), end * BS);
       }
     }
     return d;
@@ -387,13 +423,14 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<KV>())
     // one copy per lane, all in the same instructions: lanes 0..NCH-1 take
     // the K tile's 128-byte column boxes, the next lanes the V tile, the
     // next one the query rows
-    const int32_t krow = (blkj * hkv + hj) * BS;
+    const int ph = MOD ? hj / p.mod.sub : hj;  // kv head of the pool
+    const int32_t krow = (blkj * pool_heads + ph) * BS;
     if (lane < C::NCH) {
       dev::tma_load_2d(st + lane * BS * 128, &tm_k, lane * (128 / C::ELEM), krow, &full[st_i], pol);
     } else if (lane < 2 * C::NCH) {
       const int c = lane - C::NCH;
       if constexpr (C::FP8) {
-        dev::bulk_load(st + C::TILE, p.v_cache + ((int64_t)blkj * hkv + hj) * C::TILE, (uint32_t)C::TILE,
+        dev::bulk_load(st + C::TILE, p.v_cache + ((int64_t)blkj * pool_heads + ph) * C::TILE, (uint32_t)C::TILE,
                        &full[st_i], pol);
       } else {
         dev::tma_load_2d(st + C::TILE + c * BS * 128, &tm_v, c * 64, krow, &full[st_i], pol);
@@ -433,8 +470,21 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<KV>())
     const int skip = seq_skip(p, pfx, s);  // tile a holds block `skip` of the row
     int row = 0, len = 0;
     // this kv head's softmax and output scales (e4m3 per-head dequantisation)
-    const float sl2 = p.k_head ? p.scale_log2 * __ldg(p.k_head + h) : p.scale_log2;
-    const float osc = p.v_head ? p.out_scale * __ldg(p.v_head + h) : p.out_scale;
+    const int ph = MOD ? h / p.mod.sub : h;
+    const float khs = p.k_head ? __ldg(p.k_head + ph) : 1.f;
+    const float sl2 = p.k_head ? p.scale_log2 * khs : p.scale_log2;
+    const float osc = p.v_head ? p.out_scale * __ldg(p.v_head + ph) : p.out_scale;
+    Span span{0, 0, 0, 0};
+    float cap_in = 0.f, sp0 = 0.f, sp1 = 0.f;  // the piece's cap factor and this thread's columns' slopes (log2 units)
+    if constexpr (MOD) {
+      span = seq_span<BS>(p, s, min(__ldg(p.rows.seq_lens + s), p.max_blocks * BS));
+      cap_in = p.mod.cap_in * khs;
+      if (p.mod.slopes) {
+        const float log2e = 1.4426950408889634f;
+        if (c0 < G) sp0 = __ldg(p.mod.slopes + h * G + c0) * log2e;
+        if (c1 < G) sp1 = __ldg(p.mod.slopes + h * G + c1) * log2e;
+      }
+    }
     uint32_t qf[C::KSTEPS][2];
 
     float m0 = -1e30f, m1 = -1e30f, l0 = 0.f, l1 = 0.f;
@@ -457,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<KV>())
           ok = false;
           break;
         }
-        if (p.k_new != nullptr && pe == b && lane < 2 * (D * 2 / 128)) {
+        if (!MOD && p.k_new != nullptr && pe == b && lane < 2 * (D * 2 / 128)) {
           // pa_decode_fused: this piece ends the sequence, whose new K/V rows
           // its last tile stores; pull them into L2 now so that the write
           // does not wait on a cold load
@@ -489,8 +539,26 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<KV>())
       }
       const uint32_t kbase = ring_u32 + stage * STAGE;
       const uint32_t vbase = kbase + C::TILE;
-      const int key0 = (tile - a + skip) * BS;
-      if (p.k_new != nullptr && tile == b - 1) {
+      int key0 = (tile - a + skip) * BS;
+      if constexpr (MOD) {
+        if (tile - a >= span.np) key0 += span.gap * BS;
+        // keys of the tile outside the prefix and the window: their weights are
+        // 0, but 0 * NaN would poison P V, so their V rows are zeroed
+        const int z0 = max(span.pfx, key0) - key0, z1 = min(span.lo, key0 + BS) - key0;
+        if (z0 < z1) {
+          uint8_t* vt = ring + (size_t)stage * STAGE + C::TILE;
+          if constexpr (!C::FP8) {
+            for (int i = lane; i < (z1 - z0) * C::NCH * 8; i += 32) {
+              const int key = z0 + i / (C::NCH * 8), rest = i % (C::NCH * 8);
+              *reinterpret_cast<uint4*>(vt + (rest >> 3) * (BS * 128) + key * 128 + (rest & 7) * 16) =
+                  make_uint4(0, 0, 0, 0);
+            }
+          } else {
+            for (int i = lane; i < D * (z1 - z0); i += 32) vt[(i / (z1 - z0)) * BS + z0 + i % (z1 - z0)] = 0;
+          }
+          __syncwarp();
+        }
+      } else if (p.k_new != nullptr && tile == b - 1) {
         // pa_decode_fused: the sequence's last tile holds its new token at
         // position len - 1; store the token's K/V rows into the pool and
         // over the landed tile, so the attention below uses them
@@ -540,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<KV>())
 #pragma unroll
           for (int uu = 0; uu < C::KSTEPS / 2; ++uu) {
             const int unit = 2 * uu + (li >> 1);
-            const uint32_t addr = kbase + key * 128 + ((unit ^ (key & 7)) << 4);
+            const uint32_t addr = kbase + C::k8(key, unit);
             uint32_t w0, w1, w2, w3;
             dev::ldsm_x4(addr, w0, w1, w2, w3);
             uint32_t l0w, h0w, l1w, h1w, l2w, h2w, l3w, h3w;
@@ -555,10 +623,27 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<KV>())
         // rows of this thread: keys r0 (row g) and r1 (row g+8)
         const int r0 = key0 + 16 * km + (C::FP8 ? kperm(g) : g);
         const int r1 = key0 + 16 * km + (C::FP8 ? kperm(g + 8) : g + 8);
-        sc[km][0] = r0 < len ? (acc0[0] + acc1[0]) * sl2 : -INFINITY;
-        sc[km][1] = r0 < len ? (acc0[1] + acc1[1]) * sl2 : -INFINITY;
-        sc[km][2] = r1 < len ? (acc0[2] + acc1[2]) * sl2 : -INFINITY;
-        sc[km][3] = r1 < len ? (acc0[3] + acc1[3]) * sl2 : -INFINITY;
+        if constexpr (MOD) {
+          const bool v0 = r0 < len && (r0 >= span.lo || r0 < span.pfx), v1 = r1 < len && (r1 >= span.lo || r1 < span.pfx);
+          const float d0 = (float)(len - 1 - r0), d1 = (float)(len - 1 - r1);  // distances
+          float x[4] = {acc0[0] + acc1[0], acc0[1] + acc1[1], acc0[2] + acc1[2], acc0[3] + acc1[3]};
+          if (p.mod.cap_out > 0.f) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = dev::capped(x[i], cap_in, p.mod.cap_out);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] *= sl2;
+          }
+          sc[km][0] = v0 ? fmaf(-sp0, d0, x[0]) : -INFINITY;
+          sc[km][1] = v0 ? fmaf(-sp1, d0, x[1]) : -INFINITY;
+          sc[km][2] = v1 ? fmaf(-sp0, d1, x[2]) : -INFINITY;
+          sc[km][3] = v1 ? fmaf(-sp1, d1, x[3]) : -INFINITY;
+        } else {
+          sc[km][0] = r0 < len ? (acc0[0] + acc1[0]) * sl2 : -INFINITY;
+          sc[km][1] = r0 < len ? (acc0[1] + acc1[1]) * sl2 : -INFINITY;
+          sc[km][2] = r1 < len ? (acc0[2] + acc1[2]) * sl2 : -INFINITY;
+          sc[km][3] = r1 < len ? (acc0[3] + acc1[3]) * sl2 : -INFINITY;
+        }
       }
 
       // ---- online softmax per query column (columns 2tq, 2tq+1) ----
@@ -806,12 +891,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<KV>())
 // shared memory and registers, times the SMs.  (Two decode grids must not
 // run at the same time on one GPU: each could hold the SMs the other's later
 // CTAs wait for; the bounded wait would then end both with error word 1.)
-template <int KV, int D, int BS>
+template <int KV, int D, int BS, bool MOD = false>
 cudaError_t launch_instance(DecodeParams p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, int num_sms,
                             cudaStream_t stream) {
   using C = Cfg<KV, D, BS>;
   const SmemLayout L = smem_layout(C::KVB + q_area_bytes(p.group, D), p.nstages, p.rows.num_seqs);
-  auto kern = decode_tc_kernel<KV, D, BS>;
+  auto kern = decode_tc_kernel<KV, D, BS, MOD>;
   // raise the kernel's dynamic shared memory limit once per device
   static int set_for[64] = {0};
   int dev = 0;
@@ -880,9 +965,8 @@ size_t decode_tc_workspace_bytes(int num_seqs, int num_kv_heads, int group, int 
   return off;
 }
 
-cudaError_t launch_decode_tc(const DecodeParams& p_in, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
-                             int kv, int head_dim, int block_size, int num_sms, cudaStream_t stream) {
-  DecodeParams p = p_in;
+// Ring stages and grid of a launch.
+static bool shape_launch(DecodeParams& p, int kv, int head_dim, int block_size, int num_sms) {
   // the dtype's CTAs per SM while each warp still gets a double-buffered
   // ring, else fewer CTAs with deeper rings (large blocks)
   int ctas = kv == kFP8 ? ctas_per_sm<kFP8>() : ctas_per_sm<kBF16>();
@@ -890,8 +974,15 @@ cudaError_t launch_decode_tc(const DecodeParams& p_in, const CUtensorMap& tm_k, 
     p.nstages = pick_stages(kv, head_dim, block_size, p.group, p.rows.num_seqs, ctas);
     if (p.nstages >= 2 || ctas == 1) break;
   }
-  if (p.nstages < 2) return cudaErrorNotSupported;
+  if (p.nstages < 2) return false;
   p.grid = ctas * num_sms;
+  return true;
+}
+
+cudaError_t launch_decode_tc(const DecodeParams& p_in, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                             int kv, int head_dim, int block_size, int num_sms, cudaStream_t stream) {
+  DecodeParams p = p_in;
+  if (!shape_launch(p, kv, head_dim, block_size, num_sms)) return cudaErrorNotSupported;
   if (kv == kBF16) {
     if (head_dim == 128 && block_size == 16) return launch_instance<kBF16, 128, 16>(p, tm_k, tm_v, num_sms, stream);
     if (head_dim == 128 && block_size == 32) return launch_instance<kBF16, 128, 32>(p, tm_k, tm_v, num_sms, stream);
@@ -902,6 +993,24 @@ cudaError_t launch_decode_tc(const DecodeParams& p_in, const CUtensorMap& tm_k, 
     if (head_dim == 128 && block_size == 32) return launch_instance<kFP8, 128, 32>(p, tm_k, tm_v, num_sms, stream);
   }
   return cudaErrorNotSupported;
+}
+
+template <int KV, int D>
+static cudaError_t launch_biased_bs(const DecodeParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                    int block_size, int num_sms, cudaStream_t stream) {
+  return block_size == 16 ? launch_instance<KV, D, 16, true>(p, tm_k, tm_v, num_sms, stream)
+                          : launch_instance<KV, D, 32, true>(p, tm_k, tm_v, num_sms, stream);
+}
+
+cudaError_t launch_decode_biased(const DecodeParams& p_in, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                 int kv, int head_dim, int block_size, int num_sms, cudaStream_t stream) {
+  DecodeParams p = p_in;
+  if (!shape_launch(p, kv, head_dim, block_size, num_sms)) return cudaErrorNotSupported;
+  if (kv == kBF16)
+    return head_dim == 128 ? launch_biased_bs<kBF16, 128>(p, tm_k, tm_v, block_size, num_sms, stream)
+                           : launch_biased_bs<kBF16, 64>(p, tm_k, tm_v, block_size, num_sms, stream);
+  return head_dim == 128 ? launch_biased_bs<kFP8, 128>(p, tm_k, tm_v, block_size, num_sms, stream)
+                         : launch_biased_bs<kFP8, 64>(p, tm_k, tm_v, block_size, num_sms, stream);
 }
 
 }  // namespace pa

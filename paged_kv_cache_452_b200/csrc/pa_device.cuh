@@ -304,6 +304,19 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// The capped score c * tanh(s / c) in log2 units, for a raw product x with
+// s = x * scale: tanh(y) = 1 - 2 / (1 + e^(2y)), so with in = 2 log2(e) scale
+// / c and out = log2(e) c it is out - 2 out / (1 + 2^(x in)).  The
+// subtraction cancels for small y, which leaves an absolute error of about
+// out * 2^-23 (1e-5 for c = 50): what counts for an exponent.
+__device__ __forceinline__ float capped(float x, float in, float out) {
+  return fmaf(-2.f * out, rcp(1.f + ex2(x * in)), out);
+}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);

@@ -88,6 +88,18 @@ struct AttnRows {
   int32_t num_rows;
 };
 
+// What the biased attention (pa_decode_biased and the mixed step's form) does
+// to the scores of a row at position i: s = cap * tanh(scale q k / cap), minus
+// slope * |i - j|; key j is visible if j < prefix, or j <= i and, with a
+// window, i - j < window.
+struct ScoreMod {
+  float cap_in, cap_out;  // 2 log2(e) scale / cap and log2(e) cap: see capped(); cap_out 0: no cap
+  int32_t window;         // 0: none
+  const float* slopes;    // [num_q_heads] (device) or nullptr
+  const int32_t* prefix;  // [num_seqs] (device) or nullptr
+  int32_t sub;            // kernel kv heads per pool kv head (a group too large for the kernel is cut)
+};
+
 // Workspace carve-up of the split-K decode kernel.
 struct DecodeWorkspace {
   int32_t* err;             // error word (first 4 bytes of the caller's buffer)
@@ -128,12 +140,17 @@ struct DecodeParams {
   const float* pfx_o;   // [chunks][num_members][Hq][D]
   int32_t pfx_members;
   int32_t pfx_chunk_blocks;  // blocks per prefix chunk (prefix_chunk_keys / block_size)
+  ScoreMod mod;              // the biased kernel's
   DecodeWorkspace ws;
 };
 
 // kv: kBF16 or kFP8; returns cudaErrorNotSupported for unsupported shapes.
 cudaError_t launch_decode_tc(const DecodeParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                              int kv, int head_dim, int block_size, int num_sms, cudaStream_t stream);
+// The same with p.mod applied; groups 1..8, head_dim 64 and 128 for both
+// pools.  p.num_kv_heads counts kernel kv heads (mod.sub per pool kv head).
+cudaError_t launch_decode_biased(const DecodeParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                 int kv, int head_dim, int block_size, int num_sms, cudaStream_t stream);
 size_t decode_tc_smem_bytes(int kv, int head_dim, int block_size, int group, int num_seqs, int nstages);
 int decode_tc_workers(int num_sms);  // the most worker warps a launch can have (workspace sizing)
 size_t decode_tc_workspace_bytes(int num_seqs, int num_kv_heads, int group, int head_dim, int num_sms);
@@ -166,6 +183,10 @@ struct PrefillParams {
   int32_t chunk_keys;          // prefix keys per unit, a multiple of 128
   float* pfx_ml;               // [chunks][M][Hq][2] (max reference, sum), log2 domain
   float* pfx_o;                // [chunks][M][Hq][D]
+  ScoreMod mod;                // the biased kernel's
+  float out_scale;             // the biased kernel's: 1, or an e4m3 pool's V scale
+  const float* k_head;         // e4m3 per-kv-head scales (device) or nullptr
+  const float* v_head;
 };
 
 // The split of a prefix into chunks of keys that pa_decode_prefix uses: a
@@ -200,6 +221,11 @@ bool prefill_umma_supported(int kv, int q, int head_dim, int block_size, int gro
 cudaError_t launch_prefill_umma(const PrefillParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                 const CUtensorMap& tm_q, int head_dim, int block_size, int num_tokens, int num_sms,
                                 cudaStream_t stream);
+// The same rows with p.mod applied, any group up to 128 (a unit's rows are
+// 128 / G whole positions).
+cudaError_t launch_prefill_biased(const PrefillParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                  const CUtensorMap& tm_q, int kv, int head_dim, int block_size, int num_tokens,
+                                  int num_sms, cudaStream_t stream);
 cudaError_t launch_prefill_tc(const PrefillParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                               int head_dim, int block_size, int num_tokens, cudaStream_t stream);
 
@@ -220,6 +246,12 @@ struct SimtParams {
   int32_t num_blocks;      // table entries outside [0, num_blocks) are flagged and read as block 0
   int32_t* err;            // error word of the caller's workspace
 };
+// Biased attention of every row of a step on CUDA cores (fp32 queries).
+struct BiasedSimtParams {
+  SimtParams a;
+  ScoreMod mod;
+};
+cudaError_t launch_attn_biased_simt(const BiasedSimtParams& p, int q_dtype, int kv_dtype, cudaStream_t stream);
 cudaError_t launch_attn_simt(const SimtParams& p, int q_dtype, int kv_dtype, cudaStream_t stream);
 
 }  // namespace pa

@@ -79,3 +79,65 @@ def test_bindings_refuse_wrong_tensors():
         pa.pa_cache_read(desc, slots, kc, vc, k[:2], v)
     with pytest.raises(pa.PaError, match="CUDA device"):
         pa.pa_cache_read(desc, slots, kc, vc, k, v)
+
+
+def test_biased_attention_refusals():
+    desc = pa.CacheDesc.make(16, 16, 2, 8, 64, "bf16", "bf16")
+    f32 = pa.CacheDesc.make(16, 16, 2, 8, 64, "f32", "f32")
+    L = pa.lib()
+    mod = pa.ScoreMod(30.0, 10, P, P)
+
+    def decode(d, m, q=P, kc=P, vc=P, bt=P, mb=4, sl=P, n=2, scale=0.125, out=P, ws=P, wb=1 << 30):
+        return L.pa_decode_biased(ctypes.byref(d) if d is not None else None, ctypes.byref(m) if m is not None else None,
+                                  q, kc, vc, bt, mb, sl, n, scale, out, ws, wb, None)
+
+    def chunk(d, m, q=P, kc=P, vc=P, bt=P, mb=4, qsl=P, sl=P, n=2, t=5, mq=4, scale=0.125, out=P, ws=P, wb=1 << 30):
+        return L.pa_decode_chunked_prefill_biased(
+            ctypes.byref(d) if d is not None else None, ctypes.byref(m) if m is not None else None, q, kc, vc, bt, mb,
+            qsl, sl, n, t, mq, scale, out, ws, wb, None)
+    bad_mods = [pa.ScoreMod(-1.0, 0, None, None), pa.ScoreMod(float("nan"), 0, None, None),
+                pa.ScoreMod(float("inf"), 0, None, None), pa.ScoreMod(0.0, -1, None, None),
+                pa.ScoreMod(0.0, 0, P + 2, None), pa.ScoreMod(0.0, 0, None, P + 1)]
+    for call in (decode, chunk):
+        assert call(None, mod) == 1 and call(desc, None) == 1
+        for m in bad_mods:
+            assert call(desc, m) == 1
+        for kw in (dict(q=None), dict(kc=None), dict(vc=None), dict(bt=None), dict(sl=None), dict(out=None), dict(ws=None),
+                   dict(q=P + 8), dict(out=P + 2), dict(ws=P + 16), dict(n=-1), dict(mb=-1), dict(scale=0.0),
+                   dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf"))):
+            assert call(desc, mod, **kw) == 1, kw
+        assert call(f32, mod, wb=255) == 1  # workspace too small, fp32 path
+        assert call(desc, mod, n=20000) == 2
+        assert call(desc, mod, n=1, mb=1 << 27) == 2  # a table row of 2^31 tokens
+        assert call(desc, mod, n=0) == 0
+    for kw in (dict(qsl=None), dict(qsl=P + 2), dict(t=-1), dict(mq=-1), dict(mq=0)):
+        assert chunk(desc, mod, **kw) == 1, kw
+    assert chunk(desc, mod, t=0) == 0
+    assert L.pa_biased_workspace_size(ctypes.byref(desc), -1, 1) == 0
+    assert L.pa_biased_workspace_size(None, 1, 1) == 0
+    assert pa.pa_biased_workspace_size(f32, 4, 4) == 256
+
+
+def test_biased_bindings_refuse_wrong_tensors():
+    bf, i32 = torch.bfloat16, torch.int32
+    desc = pa.CacheDesc.make(4, 16, 2, 8, 64, "bf16", "bf16")
+    kc, vc = pa.alloc_cache(desc, "cpu")
+    good = dict(q=torch.zeros((2, 8, 64), dtype=bf), k_cache=kc, v_cache=vc, block_tables=torch.zeros((2, 3), dtype=i32),
+                seq_lens=torch.zeros(2, dtype=i32), scale=0.125, out=torch.zeros((2, 8, 64), dtype=bf),
+                workspace=torch.zeros(1024, dtype=torch.uint8))
+    mod = pa.ScoreMod.make(30.0, 0, torch.zeros(8), torch.zeros(2, dtype=i32))
+    bad = [dict(q=good["q"].float()), dict(q=good["q"][:1]), dict(out=good["out"][:, :4]), dict(k_cache=kc[:2]),
+           dict(block_tables=good["block_tables"].long()), dict(block_tables=good["block_tables"][0]),
+           dict(seq_lens=good["seq_lens"].long())]
+    bad_mods = [pa.ScoreMod.make(slopes=torch.zeros(4)), pa.ScoreMod.make(slopes=torch.zeros(8).double()),
+                pa.ScoreMod.make(prefix_lens=torch.zeros(3, dtype=i32)), pa.ScoreMod.make(prefix_lens=torch.zeros(2))]
+    chunk = dict(query_start_loc=torch.zeros(3, dtype=i32), max_q_len=1)
+    for f, more in ((pa.pa_decode_biased, {}), (pa.pa_decode_chunked_prefill_biased, chunk)):
+        with pytest.raises(pa.PaError, match="CUDA device"):
+            f(desc, mod, **good, **more)
+        for kw in bad:
+            assert "CUDA device" not in str(pytest.raises(pa.PaError, f, desc, mod, **{**good, **more, **kw}).value)
+        for m in bad_mods:
+            assert "CUDA device" not in str(pytest.raises(pa.PaError, f, desc, m, **good, **more).value)
+    with pytest.raises(pa.PaError, match="query_start_loc"):
+        pa.pa_decode_chunked_prefill_biased(desc, mod, **good, query_start_loc=torch.zeros(2, dtype=i32), max_q_len=1)
