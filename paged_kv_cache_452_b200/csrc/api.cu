@@ -451,11 +451,21 @@ int run_prefill_biased(const pa_cache_desc* d, const pa_score_mod* mod, const vo
   int rc = num_sms(&sms);
   if (rc) return rc;
   const int group = d->num_q_heads / d->num_kv_heads, cut = cut_group(group, 128);
+  const bool fp8 = d->kv_dtype == kFP8;
+  const float k_scale = fp8 && !d->k_head_scales ? d->k_scale : 1.f;
   CUtensorMap tm_k, tm_v, tm_q;
-  if ((rc = make_kv_map(&tm_k, k_cache, d->kv_dtype, d))) return rc;
-  if ((rc = make_kv_map(&tm_v, v_cache, d->kv_dtype, d))) return rc;
   if ((rc = encode_q_map(&tm_q, q, num_tokens, d, cut))) return rc;
+  if (fp8) {
+    tm_k = tm_v = tm_q;  // e4m3 blocks come by bulk copies
+  } else {
+    if ((rc = make_kv_map(&tm_k, k_cache, d->kv_dtype, d))) return rc;
+    if ((rc = make_kv_map(&tm_v, v_cache, d->kv_dtype, d))) return rc;
+  }
   PrefillParams p = {};
+  p.k_raw = static_cast<const uint8_t*>(k_cache);
+  p.v_raw = static_cast<const uint8_t*>(v_cache);
+  p.k_head = fp8 ? d->k_head_scales : nullptr;
+  p.v_head = fp8 ? d->v_head_scales : nullptr;
   p.q = static_cast<const uint8_t*>(q);
   p.out = static_cast<uint8_t*>(out);
   p.block_tables = block_tables;
@@ -468,16 +478,16 @@ int run_prefill_biased(const pa_cache_desc* d, const pa_score_mod* mod, const vo
   p.num_kv_heads = d->num_q_heads / cut;
   p.group = cut;
   p.num_blocks = d->num_blocks;
-  p.scale_log2 = scale * kLog2e;
-  p.out_scale = 1.f;
-  p.mod = kernel_mod(mod, scale, 1.f);
+  p.scale_log2 = scale * kLog2e * k_scale;
+  p.out_scale = fp8 && !d->v_head_scales ? d->v_scale : 1.f;
+  p.mod = kernel_mod(mod, scale, k_scale);
   p.mod.sub = group / cut;
   p.err = static_cast<int32_t*>(workspace);
   p.unit_ctr = static_cast<int32_t*>(workspace) + 2;
   p.unit_exit = static_cast<int32_t*>(workspace) + 3;
   p.after_decode = after_decode;
-  cudaError_t e = launch_prefill_biased(p, tm_k, tm_v, tm_q, d->kv_dtype, d->head_dim, d->block_size, num_tokens, sms,
-                                        stream);
+  cudaError_t e = launch_chunk_biased(p, tm_k, tm_v, tm_q, d->kv_dtype, d->head_dim, d->block_size, num_tokens, sms,
+                                      stream);
   if (e == cudaErrorNotSupported) return fail(PA_ERR_UNSUPPORTED, "%s: too many sequences for one launch", who);
   return cuda_status(e, who);
 }
@@ -512,7 +522,7 @@ int run_biased_simt(const pa_cache_desc* d, const pa_score_mod* mod, const void*
     p.v_head = d->v_head_scales;
   }
   b.mod = kernel_mod(mod, scale, 1.f);
-  cudaError_t e = launch_attn_biased_simt(b, d->q_dtype, d->kv_dtype, stream);
+  cudaError_t e = launch_attn_biased_simt(b, d->kv_dtype, stream);
   if (e == cudaErrorNotSupported)
     return fail(PA_ERR_UNSUPPORTED, "%s: q dtype %d with kv dtype %d, %d rows", who, d->q_dtype, d->kv_dtype, num_rows);
   return cuda_status(e, who);
@@ -972,7 +982,7 @@ int pa_decode_chunked_prefill_biased(const pa_cache_desc* d, const pa_score_mod*
   if (num_tokens == 0) return PA_OK;
   if (max_q_len == 0) return fail(PA_ERR_INVALID_ARG, "%s: max_q_len 0 with %d tokens", who, num_tokens);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (!biased_tc(d) || d->kv_dtype == kFP8) {
+  if (!biased_tc(d)) {
     if (workspace_bytes < 256) return fail(PA_ERR_INVALID_ARG, "%s: workspace < 256 bytes", who);
     return run_biased_simt(d, mod, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, query_start_loc,
                            num_seqs, num_tokens, scale, out, workspace, st, who);

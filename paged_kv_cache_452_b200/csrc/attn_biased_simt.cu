@@ -29,18 +29,6 @@ __device__ __forceinline__ void load_elems(const uint8_t* base, int64_t idx, flo
       const float4 v = __ldg(p + i);
       x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
     }
-  } else if constexpr (sizeof(T) == 2) {
-    const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(base) + idx);
-#pragma unroll
-    for (int i = 0; i < E / 8; ++i) {
-      const uint4 v = __ldg(p + i);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        x[8 * i + 2 * k] = dev::bf16_bits_to_f32(w[k] & 0xFFFFu);
-        x[8 * i + 2 * k + 1] = dev::bf16_bits_to_f32(w[k] >> 16);
-      }
-    }
   } else {
     const uint2* p = reinterpret_cast<const uint2*>(base + idx);
 #pragma unroll
@@ -55,13 +43,10 @@ __device__ __forceinline__ void load_elems(const uint8_t* base, int64_t idx, flo
   }
 }
 
-template <int QT> struct QElem { using T = float; };
-template <> struct QElem<kBF16> { using T = __nv_bfloat16; };
 template <int KV> struct KElem { using T = float; };
-template <> struct KElem<kBF16> { using T = __nv_bfloat16; };
 template <> struct KElem<kFP8> { using T = uint8_t; };
 
-template <int QT, int KV, int D, int NP>
+template <int KV, int D, int NP>
 __global__ void __launch_bounds__(kWarps * 32) attn_biased_simt_kernel(const BiasedSimtParams bp) {
   dev::grid_dep_wait();
   const SimtParams& p = bp.a;
@@ -104,7 +89,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_biased_simt_kernel(const Bia
     const int row = (int)(pr / G), h = kvh * G + (int)(pr % G);
     pos[n] = at0 + row;
     slope[n] = bp.mod.slopes ? __ldg(bp.mod.slopes + h) * kLog2e : 0.f;
-    load_elems<typename QElem<QT>::T, E>(p.q, ((int64_t)(first + row) * hq + h) * D + sub * E, q[n]);
+    load_elems<float, E>(p.q, ((int64_t)(first + row) * hq + h) * D + sub * E, q[n]);
     m[n] = -1e30f;
     l[n] = 0.f;
 #pragma unroll
@@ -173,20 +158,11 @@ __global__ void __launch_bounds__(kWarps * 32) attn_biased_simt_kernel(const Bia
         if (!any) continue;
         float vx[DV];
         const int64_t vb = kb + (int64_t)k * D + lane * DV;
-        if constexpr (KV == kF32) {
 #pragma unroll
-          for (int e = 0; e < DV; e += 2) {
-            const float2 v = __ldg(reinterpret_cast<const float2*>(reinterpret_cast<const float*>(p.v_cache) + vb + e));
-            vx[e] = v.x;
-            vx[e + 1] = v.y;
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < DV; e += 2) {
-            const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint16_t*>(p.v_cache) + vb + e));
-            vx[e] = dev::bf16_bits_to_f32(v & 0xFFFFu);
-            vx[e + 1] = dev::bf16_bits_to_f32(v >> 16);
-          }
+        for (int e = 0; e < DV; e += 2) {
+          const float2 v = __ldg(reinterpret_cast<const float2*>(reinterpret_cast<const float*>(p.v_cache) + vb + e));
+          vx[e] = v.x;
+          vx[e + 1] = v.y;
         }
 #pragma unroll
         for (int n = 0; n < NP; ++n) {
@@ -248,37 +224,35 @@ __global__ void __launch_bounds__(kWarps * 32) attn_biased_simt_kernel(const Bia
     const int64_t pr = pair0 + n;
     const int64_t at = ((int64_t)(first + pr / G) * hq + kvh * G + pr % G) * D + d;
     const float x = L > 0.f ? o / L * (KV == kFP8 ? vs : 1.f) : 0.f;  // an empty context: a zero row
-    if constexpr (QT == kF32) reinterpret_cast<float*>(p.out)[at] = x;
-    else reinterpret_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(x);
+    reinterpret_cast<float*>(p.out)[at] = x;
   }
 }
 
-template <int QT, int KV, int D, int NP>
+template <int KV, int D, int NP>
 cudaError_t launch(const BiasedSimtParams& p, cudaStream_t stream) {
   const int G = p.a.num_q_heads / p.a.num_kv_heads;
   const int64_t blocks = (int64_t)p.a.rows.num_rows * G / NP + p.a.rows.num_seqs;
   if (blocks > INT32_MAX || p.a.num_kv_heads > 65535) return cudaErrorNotSupported;
-  attn_biased_simt_kernel<QT, KV, D, NP><<<dim3((unsigned)blocks, (unsigned)p.a.num_kv_heads), kWarps * 32, 0, stream>>>(p);
+  attn_biased_simt_kernel<KV, D, NP><<<dim3((unsigned)blocks, (unsigned)p.a.num_kv_heads), kWarps * 32, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
 // Pairs per CTA: one where there are few (a decode batch: short chains per
 // warp count), else four.
-template <int QT, int KV>
+template <int KV>
 cudaError_t launch_d(const BiasedSimtParams& p, cudaStream_t stream) {
   const int64_t pairs = (int64_t)p.a.rows.num_rows * p.a.num_q_heads;
   const bool few = pairs <= 1024 || (p.a.num_q_heads == p.a.num_kv_heads && !p.a.rows.qsl);
-  if (p.a.head_dim == 64) return few ? launch<QT, KV, 64, 1>(p, stream) : launch<QT, KV, 64, 4>(p, stream);
-  if (p.a.head_dim == 128) return few ? launch<QT, KV, 128, 1>(p, stream) : launch<QT, KV, 128, 4>(p, stream);
+  if (p.a.head_dim == 64) return few ? launch<KV, 64, 1>(p, stream) : launch<KV, 64, 4>(p, stream);
+  if (p.a.head_dim == 128) return few ? launch<KV, 128, 1>(p, stream) : launch<KV, 128, 4>(p, stream);
   return cudaErrorNotSupported;
 }
 
 }  // namespace
 
-cudaError_t launch_attn_biased_simt(const BiasedSimtParams& p, int q_dtype, int kv_dtype, cudaStream_t stream) {
-  if (q_dtype == kBF16 && kv_dtype == kFP8) return launch_d<kBF16, kFP8>(p, stream);
-  if (q_dtype == kF32 && kv_dtype == kF32) return launch_d<kF32, kF32>(p, stream);
-  if (q_dtype == kF32 && kv_dtype == kFP8) return launch_d<kF32, kFP8>(p, stream);
+cudaError_t launch_attn_biased_simt(const BiasedSimtParams& p, int kv_dtype, cudaStream_t stream) {
+  if (kv_dtype == kF32) return launch_d<kF32>(p, stream);
+  if (kv_dtype == kFP8) return launch_d<kFP8>(p, stream);
   return cudaErrorNotSupported;
 }
 

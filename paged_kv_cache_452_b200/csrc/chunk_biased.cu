@@ -1,0 +1,942 @@
+// Chunks of new tokens under a biased score, over a paged bf16 or e4m3 pool,
+// on the 5th-generation tensor cores (pa_decode_chunked_prefill_biased's rows
+// of more than one per sequence).
+//
+// What it computes: row i of a sequence sees key j if j < prefix, or j <= i
+// and (window) i - j < window; s = cap tanh(scale q k / cap) - slope |i - j|
+// (or scale q k - slope |i - j|), out = softmax(s) V over the visible keys.
+//
+// Unit = (sequence, kv head, 2 x (128 / G) query positions): two query tiles A
+// and B of 128 rows (positions x the group's heads), one warpgroup of softmax
+// warps each, a thread per row.  While A's softmax runs, the tensor core does
+// B's products and the other way round, and both tiles use every K/V tile that
+// is brought in.  One persistent CTA per SM claims units from a counter.
+//  * TMEM (512 columns): S_A, S_B (128 each), O_A, O_B (head_dim each).  A
+//    tile's weights P (16 bit) go over the first 64 columns of its own S.
+//    One thread issues every MMA, in the order PV_A(k) S_A(k+1) PV_B(k)
+//    S_B(k+1): MMAs of one thread run in order, so S_A(k+1) finds P_A(k)
+//    consumed, and S_A(k+1) being complete says that O_A is at rest.
+//  * key tiles (128 keys) run from the last to the first: with a distance
+//    bias the nearest keys carry the largest weights, so the reference that a
+//    row's exponents get from its first tile serves the others.  A later tile
+//    skips the row max: its weights 2^(s - ref) only have to stay finite, and
+//    a sum above kBig sends the warp to a slow path that moves the reference
+//    and rescales O.  Tiles between the prefix and the window are skipped.
+//  * the cap's tanh is an odd polynomial of degree 9 on |y| <= 0.8 (minimax,
+//    3.5e-7 absolute), which leaves one special-function operation per score,
+//    the exponential; a tile with a larger |y| takes the exact form, which
+//    needs three.  Special-function throughput (16 lanes a clock an SM) is the
+//    bound: 128 x 128 exponentials take 1024 clocks, the tile's two MMAs 512.
+//  * e4m3 pools: blocks land raw (bulk copies), four converter warps write them
+//    as f16 (exact) into the swizzled K and V tiles, V transposed to key-major
+//    order by its d-major blocks, and the queries are rounded to f16; P is f16.
+// Every wait is bounded (2 s, then the error word); TMEM is freed on every path.
+#include <cuda_runtime.h>
+
+#include "pa_device.cuh"
+#include "pa_kernels.h"
+
+namespace pa {
+namespace {
+
+constexpr int kRows = 128;   // rows of a query tile: the MMA's M
+constexpr int kKeys = 128;   // keys of a K/V tile
+constexpr int kTileRow = 128 * 128;  // bytes of a 64-element-wide chunk of a 128-row tile
+constexpr int kUQ = 4;       // unit queue entries
+constexpr int kGroup = 64;   // sequences of a group in the unit search
+constexpr int kMaxGroups = 256;  // groups: 16384 sequences
+constexpr int kKWarp = 8, kVWarp = 9, kMmaWarp = 10, kConvWarp = 12;  // warps 0..7: softmax of A, of B
+constexpr uint32_t kTmemCols = 512;
+constexpr int kSmemOptIn = 232448;  // 227 KB per block
+constexpr int kMask = 0, kSlope = 1, kCap = 2, kCapSlope = 3;
+
+// tanh(y) = y P(y^2) on |y| <= kCapFast: minimax in the absolute error (3.5e-7),
+// fitted by an exchange iteration in fp64
+constexpr float kCapFast = 0.8f;
+constexpr float kTanh[5] = {0.999995135f, -0.333174266f, 0.131862197f, -0.0482613155f, 0.0114646552f};
+
+template <int KV, int D, int BS>
+struct C {
+  static constexpr bool FP8 = KV == kFP8;
+  static constexpr int NCH = D / 64;                // 64-element chunks of a row
+  static constexpr int TILE = NCH * kTileRow;       // bytes of a 16-bit Q, K or V tile
+  static constexpr int RAW = kKeys * D;             // bytes of a raw e4m3 tile
+  static constexpr int BPT = kKeys / BS;            // blocks per tile
+  static constexpr int NK = FP8 ? 2 : D == 64 ? 4 : 3, NV = FP8 || D == 128 ? 2 : 4;  // K and V tiles in shared memory
+  static constexpr int NR = FP8 ? 2 : 0;            // raw tiles
+  static constexpr int THREADS = FP8 ? 512 : 384;
+  static constexpr int READERS = FP8 ? 14 : 10;     // roles that read a queue entry
+  // weights stay at most this in a tile's sum before the reference moves:
+  // bf16 has fp32's range, f16 ends at 65504
+  static constexpr float BIG = FP8 ? 16384.f : 18446744073709551616.f;
+  // shared memory
+  static constexpr int Q = 0, K = 2 * TILE, V = K + NK * TILE, R = V + NV * TILE, BARS = R + NR * RAW;
+  static constexpr int NBARS = 2 * NK + 2 * NV + 2 * NR + 8 + 4 + 2 * kUQ;
+  static constexpr int UQ = BARS + NBARS * 8, TSLOT = UQ + kUQ * 32, GROUPS = TSLOT + 16;
+  static constexpr int TOTAL = GROUPS + (kMaxGroups + 1) * 4 + 1024;
+  static_assert(TOTAL <= kSmemOptIn, "shared memory");
+  static_assert(256 + 2 * D <= (int)kTmemCols, "TMEM columns");
+};
+
+// One unit, published in shared memory by the claiming warp.
+struct __align__(16) Unit {
+  int s, h;        // sequence (-1: no more units), kernel kv head
+  int row0, qn;    // first query row, positions (at most two tiles' worth)
+  int p0;          // position of the first query
+  int len, pfx;    // context, visible prefix
+  int pad;
+};
+static_assert(sizeof(Unit) == 32, "queue entry");
+
+// A unit's key tiles: [0, npt) and [npt + gap, npt + gap + ...), nt in all,
+// visited from the last.
+template <int BS>
+struct Tiles {
+  int kend, lo, nb, nt, npt, gap, window, pfx;
+  __device__ __forceinline__ Tiles(const Unit& u, const PrefillParams& p) {
+    window = p.mod.window;
+    pfx = u.pfx;
+    kend = max(min(u.len, u.p0 + u.qn), u.pfx);
+    lo = window > 0 ? max(0, u.p0 - window + 1) : 0;
+    nb = min((max(kend, 0) + BS - 1) / BS, p.max_blocks);
+    const int all = (nb * BS + kKeys - 1) / kKeys;
+    npt = min((pfx + kKeys - 1) / kKeys, all);
+    gap = max(0, min(lo / kKeys, all) - npt);
+    nt = all - gap;
+  }
+  __device__ __forceinline__ int tile(int k) const {
+    const int t = nt - 1 - k;
+    return t < npt ? t : t + gap;
+  }
+  // whether rows at positions [a, a + n) see a key of tile t
+  __device__ __forceinline__ bool active(int t, int a, int n) const {
+    if (n <= 0) return false;
+    if (t < npt) return true;
+    const int first = window > 0 ? max(0, a - window + 1) : 0;
+    return t * kKeys < a + n && t >= first / kKeys;
+  }
+};
+
+__device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 168;"); }
+__device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 80;"); }
+
+template <int KV, int D, int BS, int MOD>
+__global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
+    chunk_biased_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                        const __grid_constant__ CUtensorMap tm_q, const PrefillParams p) {
+  using T = C<KV, D, BS>;
+  constexpr bool CAPS = MOD >= kCap, SLOPES = MOD == kSlope || MOD == kCapSlope;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + T::BARS);
+  uint64_t* kempty = kfull + T::NK;
+  uint64_t* vfull = kempty + T::NK;
+  uint64_t* vempty = vfull + T::NV;
+  uint64_t* rfull = vempty + T::NV;
+  uint64_t* rempty = rfull + T::NR;
+  uint64_t* s_full = rempty + T::NR;  // [2] S of a tile is complete (and the tile's earlier PV)
+  uint64_t* p_full = s_full + 2;      // [2] P is written
+  uint64_t* o_done = p_full + 2;      // [2] a unit's last PV is complete
+  uint64_t* o_free = o_done + 2;      // [2] O has been read out
+  uint64_t* q_full = o_free + 2;      // the Q tiles are in place
+  uint64_t* q_raw = q_full + 1;       // e4m3: ... as bf16, before their conversion
+  uint64_t* q_free = q_raw + 1;       // the unit's last S MMA is complete
+  uint64_t* done = q_free + 1;        // every MMA issued is complete
+  uint64_t* uq_full = done + 1;
+  uint64_t* uq_empty = uq_full + kUQ;
+  Unit* uq = reinterpret_cast<Unit*>(smem + T::UQ);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + T::TSLOT);
+  int32_t* gsum = reinterpret_cast<int32_t*>(smem + T::GROUPS);  // unit blocks before each group of sequences
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = p.group, hq = p.num_q_heads, hkv = p.num_kv_heads, S = p.rows.num_seqs;
+  const int QB = kRows / G, QB2 = 2 * QB;
+
+  if (!p.after_decode) dev::grid_dep_wait();
+  // ---- unit blocks of each group of sequences, exclusive prefix --------------
+  auto blocks_of = [&](int s) {
+    const int q = s < S ? p.rows.qsl[s + 1] - p.rows.qsl[s] : 0;
+    return q > 1 ? (q + QB2 - 1) / QB2 : 0;  // single rows are the decode kernel's
+  };
+  const int groups = (S + kGroup - 1) / kGroup;
+  for (int g = warp; g < groups; g += T::THREADS / 32) {
+    int n = blocks_of(kGroup * g + 2 * lane) + blocks_of(kGroup * g + 2 * lane + 1);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+    if (lane == 0) gsum[g] = n;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < T::NK; ++i) {
+      dev::mbar_init(&kfull[i], T::FP8 ? 4 : 1);
+      dev::mbar_init(&kempty[i], 1);
+    }
+    for (int i = 0; i < T::NV; ++i) {
+      dev::mbar_init(&vfull[i], T::FP8 ? 4 : 1);
+      dev::mbar_init(&vempty[i], 1);
+    }
+    for (int i = 0; i < T::NR; ++i) {
+      dev::mbar_init(&rfull[i], 1);
+      dev::mbar_init(&rempty[i], 4);
+    }
+    for (int x = 0; x < 2; ++x) {
+      dev::mbar_init(&s_full[x], 1);
+      dev::mbar_init(&p_full[x], 4);
+      dev::mbar_init(&o_done[x], 1);
+      dev::mbar_init(&o_free[x], 4);
+    }
+    dev::mbar_init(q_full, T::FP8 ? 8 : 1);
+    dev::mbar_init(q_raw, 1);
+    dev::mbar_init(q_free, 1);
+    dev::mbar_init(done, 1);
+    for (int i = 0; i < kUQ; ++i) {
+      dev::mbar_init(&uq_full[i], 1);
+      dev::mbar_init(&uq_empty[i], T::READERS);
+    }
+    dev::fence_barrier_init();
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int run = 0;
+    for (int g0 = 0; g0 < groups; g0 += 32) {
+      const int n = g0 + lane < groups ? gsum[g0 + lane] : 0;
+      int x = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (g0 + lane < groups) gsum[g0 + lane] = run + x - n;
+      run += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) gsum[groups] = run;
+  }
+  __syncthreads();
+  dev::grid_dep_launch();
+  const int nunits = gsum[groups] * hkv;
+  auto finish_queue = [&]() {  // the last CTA puts the claim counter back to zero
+    if (tid == 0) {
+      __threadfence();
+      if (atomicAdd(p.unit_exit, 1) == (int)gridDim.x - 1) {
+        atomicExch(p.unit_ctr, 0);
+        atomicExch(p.unit_exit, 0);
+      }
+    }
+    // this grid does not wait for the step's decode grid before it works, and
+    // a later grid of the stream may wait for this one alone
+    if (p.after_decode) dev::grid_dep_wait();
+  };
+  if ((int)blockIdx.x >= nunits) {
+    finish_queue();
+    return;
+  }
+  if (warp == kMmaWarp) {
+    dev::tmem_alloc(tmem_slot, kTmemCols);
+    dev::tmem_relinquish();
+  }
+  dev::tc_fence_before();
+  __syncthreads();
+  dev::tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
+
+  // queue entry n, as one warp's (or thread's) copy; ok false: none
+  auto read_unit = [&](int n, Unit& u, bool& ok) {
+    const int slot = n % kUQ;
+    if (ok) ok = dev::mbar_wait(&uq_full[slot], (uint32_t)((n / kUQ) & 1), p.err);
+    if (ok) u = uq[slot];
+    else u.s = -1;
+  };
+
+  if (warp == kKWarp || warp == kVWarp) {
+    // ================= claims, and the loads of K / V and Q ======================
+    if constexpr (T::FP8) reg_dec();
+    const bool is_v = warp == kVWarp;
+    const uint64_t pol = dev::policy_evict_last();  // the sequence's other units read the same tiles
+    const uint64_t qpol = dev::policy_evict_first();
+    const int ph_div = p.mod.sub;
+    bool ok = true;
+    int st = 0, g = 0, qlast = -1;
+    uint32_t ph = 0;
+    for (int n = 0;; ++n) {
+      Unit u;
+      u.s = -1;
+      if (!is_v) {
+        // claim the next unit and publish it
+        int idx = 0;
+        if (ok && lane == 0) idx = atomicAdd(p.unit_ctr, 1);
+        idx = __shfl_sync(0xffffffffu, idx, 0);
+        if (ok && idx < nunits) {
+          const int x = idx / hkv;
+          int lo = 0, hi = groups - 1;  // the last group with gsum <= x
+          while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (gsum[mid] <= x) lo = mid; else hi = mid - 1;
+          }
+          const int s0 = kGroup * lo + 2 * lane;  // this lane's two sequences
+          const int nb0 = blocks_of(s0), nb = nb0 + blocks_of(s0 + 1);
+          int inc = nb;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+          }
+          const int local = x - gsum[lo];
+          const uint32_t hit = __ballot_sync(0xffffffffu, local >= inc - nb && local < inc);
+          const int who = hit ? __ffs(hit) - 1 : 0;
+          const int pair0 = __shfl_sync(0xffffffffu, inc - nb, who);
+          const int n0 = __shfl_sync(0xffffffffu, nb0, who), n1 = __shfl_sync(0xffffffffu, nb, who) - n0;
+          if (hit) {
+            const int second = local - pair0 >= n0;
+            const int before = pair0 + (second ? n0 : 0), mine = second ? n1 : n0;
+            u.s = kGroup * lo + 2 * who + second;
+            u.h = idx % hkv;
+            const int first = p.rows.qsl[u.s], qlen = p.rows.qsl[u.s + 1] - first;
+            const int qb = mine - 1 - (local - before);  // a sequence's last (longest) rows first
+            int len = p.rows.seq_lens[u.s];
+            u.p0 = len - qlen + qb * QB2;
+            u.row0 = first + qb * QB2;
+            u.qn = min(QB2, qlen - qb * QB2);
+            if (len > p.max_blocks * BS) {  // longer than its table row: flag, clamp
+              if (lane == 0) atomicCAS(p.err, 0, 3);
+              len = p.max_blocks * BS;
+            }
+            u.len = len;
+            u.pfx = p.mod.prefix ? max(0, min(len, __ldg(p.mod.prefix + u.s))) : 0;
+            u.pad = 0;
+          }
+        }
+        const int slot = n % kUQ;
+        if (n >= kUQ && ok)
+          ok = __all_sync(0xffffffffu, dev::mbar_wait(&uq_empty[slot], (uint32_t)(((n / kUQ) - 1) & 1), p.err));
+        if (!ok) u.s = -1;
+        if (lane == 0) {
+          uq[slot] = u;
+          dev::mbar_arrive(&uq_full[slot]);
+        }
+        __syncwarp();
+      } else {
+        read_unit(n, u, ok);
+        ok = __all_sync(0xffffffffu, ok);
+        __syncwarp();
+        if (lane == 0) dev::mbar_arrive(&uq_empty[n % kUQ]);
+      }
+      if (u.s < 0) break;
+      const Tiles<BS> tl(u, p);
+      if (is_v) {
+        // the unit's queries, once the previous unit's S MMAs are done with
+        // them: two boxes of 128 / G positions (rows past the unit are other
+        // rows or zeros: computed, not kept)
+        if (n > 0 && ok) ok = __all_sync(0xffffffffu, dev::mbar_wait(q_free, (uint32_t)((n - 1) & 1), p.err));
+        if (!ok) continue;
+        if (lane == 0) {
+          uint64_t* bar = T::FP8 ? q_raw : q_full;
+          dev::mbar_arrive_expect_tx(bar, (uint32_t)(2 * T::NCH * QB * G * 128));
+#pragma unroll
+          for (int i = 0; i < 2 * T::NCH; ++i)
+            dev::tma_load_3d(smem + T::Q + (i / T::NCH) * T::TILE + (i % T::NCH) * kTileRow, &tm_q, (i % T::NCH) * 64,
+                             u.h * G, u.row0 + (i / T::NCH) * QB, bar, qpol);
+        }
+        qlast = n;
+        __syncwarp();
+        if constexpr (T::FP8) continue;  // K and V both come raw, by the K warp
+      }
+      const int32_t* table = p.block_tables + (int64_t)u.s * p.max_blocks;
+      const int head = u.h / ph_div, pool_heads = hkv / ph_div;
+      // a block is read if a row of the unit may see one of its keys
+      auto entry = [&](int k, int j) -> int32_t {
+        const int b = tl.tile(k) * T::BPT + j;
+        return k < tl.nt && b < tl.nb && (b * BS < u.pfx || b >= tl.lo / BS) ? __ldg(table + b) : -2;
+      };
+      auto checked = [&](int32_t blk) {
+        if (blk < 0 || blk >= p.num_blocks) {  // bad table entry: flag, read block 0
+          atomicCAS(p.err, 0, 2);
+          blk = 0;
+        }
+        return blk;
+      };
+      if constexpr (!T::FP8) {
+        uint64_t* fullb = is_v ? vfull : kfull;
+        uint64_t* emptyb = is_v ? vempty : kempty;
+        uint8_t* ring = smem + (is_v ? T::V : T::K);
+        const int nst = is_v ? T::NV : T::NK;
+        const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
+        const int c = lane / T::BPT, j = lane % T::BPT;
+        const bool mine = lane < T::NCH * T::BPT;
+        int32_t next = mine ? entry(0, j) : -2;
+        for (int k = 0; k < tl.nt && ok; ++k, ++g) {
+          if (g >= nst) ok = __all_sync(0xffffffffu, dev::mbar_wait(&emptyb[st], ph ^ 1u, p.err));
+          if (!ok) break;
+          const int32_t blk = next;
+          if (mine) next = entry(k + 1, j);
+          int32_t y = p.num_blocks * pool_heads * BS;  // past the pool: zeros
+          if (blk != -2) y = (checked(blk) * pool_heads + head) * BS;
+          if (lane == 0) dev::mbar_arrive_expect_tx(&fullb[st], (uint32_t)T::TILE);
+          __syncwarp();
+          if (mine) dev::tma_load_2d(ring + st * T::TILE + c * kTileRow + j * BS * 128, tm, c * 64, y, &fullb[st], pol);
+          if (++st == nst) {
+            st = 0;
+            ph ^= 1u;
+          }
+        }
+      } else {
+        // raw K, then raw V of each tile, a bulk copy per block
+        const int j = lane % T::BPT;
+        int32_t next = lane < T::BPT ? entry(0, j) : -2;
+        for (int k = 0; k < tl.nt && ok; ++k) {
+          int32_t blk = next;
+          if (lane < T::BPT) next = entry(k + 1, j);
+          const bool mine = blk != -2;
+          if (mine) blk = checked(blk);
+          const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(0xffffffffu, mine)) * BS * D);
+          for (int side = 0; side < 2 && ok; ++side, ++g) {
+            if (g >= T::NR) ok = __all_sync(0xffffffffu, dev::mbar_wait(&rempty[st], ph ^ 1u, p.err));
+            if (!ok) break;
+            if (lane == 0) dev::mbar_arrive_expect_tx(&rfull[st], bytes);
+            __syncwarp();
+            if (mine)
+              dev::bulk_load(smem + T::R + st * T::RAW + j * BS * D,
+                             (side ? p.v_raw : p.k_raw) + ((int64_t)blk * pool_heads + head) * BS * D,
+                             (uint32_t)(BS * D), &rfull[st], pol);
+            if (++st == T::NR) {
+              st = 0;
+              ph ^= 1u;
+            }
+          }
+        }
+      }
+    }
+    // drain: what is still in flight must land before the CTA may exit
+    if (lane == 0) {
+      uint64_t* fullb = T::FP8 ? rfull : is_v ? vfull : kfull;
+      const int nst = T::FP8 ? T::NR : is_v ? T::NV : T::NK;
+      for (int d = max(0, g - nst); d < g; ++d)
+        dev::mbar_wait(&fullb[d % nst], (uint32_t)((d / nst) & 1), nullptr, 100000000ull);
+      if (qlast >= 0) dev::mbar_wait(T::FP8 ? q_raw : q_full, (uint32_t)(qlast & 1), nullptr, 100000000ull);
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    // ============================ MMA issue (one thread) =============================
+    if constexpr (T::FP8) reg_dec();
+    if (lane == 0) {
+      const uint32_t idesc_s = T::FP8 ? dev::umma_idesc_f16(kKeys, false) : dev::umma_idesc_bf16(kKeys, false);
+      const uint32_t idesc_o = T::FP8 ? dev::umma_idesc_f16(D, false) : dev::umma_idesc_bf16(D, true);
+      const uint64_t dq = dev::umma_desc_sw128(dev::smem_u32(smem + T::Q), 16, 1024);
+      const uint64_t dk = dev::umma_desc_sw128(dev::smem_u32(smem + T::K), 16, 1024);
+      // V: bf16 MN-major (d contiguous, 64-wide chunks kTileRow apart); e4m3's
+      // converted tile K-major (keys contiguous, 64-key chunks of D rows)
+      const uint64_t dv = dev::umma_desc_sw128(dev::smem_u32(smem + T::V), T::FP8 ? 16 : kTileRow, 1024);
+      int kst = 0, vst = 0;
+      uint32_t kph = 0, vph = 0;
+      uint32_t pcount[2] = {0, 0}, units[2] = {0, 0};
+      bool ok = true;
+      auto issue_s = [&](int x) {
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint64_t off = (uint64_t)(((ks >> 2) * kTileRow + (ks & 3) * 32) >> 4);
+          dev::umma_ss(tbase + x * kKeys, dq + (uint64_t)(x * (T::TILE >> 4)) + off,
+                       dk + (uint64_t)(kst * (T::TILE >> 4)) + off, idesc_s, ks > 0 ? 1u : 0u);
+        }
+        dev::umma_commit(&s_full[x]);
+      };
+      for (int n = 0;; ++n) {
+        Unit u;
+        read_unit(n, u, ok);
+        dev::mbar_arrive(&uq_empty[n % kUQ]);
+        if (u.s < 0) break;
+        const Tiles<BS> tl(u, p);
+        const int na = min(u.qn, QB);  // positions of tile A; B has the rest
+        auto act = [&](int x, int k) {
+          return k < tl.nt && tl.active(tl.tile(k), u.p0 + x * QB, x ? u.qn - na : na);
+        };
+        ok = ok && dev::mbar_wait(q_full, (uint32_t)(n & 1), p.err);
+        bool begun[2] = {false, false};
+        // step k: the PVs of tile k and the S's of tile k + 1
+        for (int k = -1; k < tl.nt && ok; ++k) {
+          if (k >= 0) {
+            ok = dev::mbar_wait(&vfull[vst], vph, p.err);
+          }
+          if (k + 1 < tl.nt && k < 0) ok = ok && dev::mbar_wait(&kfull[kst], kph, p.err);
+          bool kready = k < 0;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (!ok) break;
+            if (k >= 0 && act(x, k)) {
+              ok = dev::mbar_wait(&p_full[x], pcount[x] & 1, p.err);
+              ++pcount[x];
+              if (ok && !begun[x] && units[x] > 0) ok = dev::mbar_wait(&o_free[x], (units[x] - 1) & 1, p.err);
+              if (!ok) break;
+              dev::tc_fence_after();
+#pragma unroll
+              for (int ks = 0; ks < kKeys / 16; ++ks) {
+                const uint64_t off = T::FP8 ? (uint64_t)(((ks >> 2) * (D * 128) + (ks & 3) * 32) >> 4)
+                                            : (uint64_t)((ks * 16 * 128) >> 4);
+                dev::umma_ts(tbase + 2 * kKeys + x * D, tbase + x * kKeys + 8 * ks,
+                             dv + (uint64_t)(vst * (T::TILE >> 4)) + off, idesc_o, (begun[x] || ks > 0) ? 1u : 0u);
+              }
+              begun[x] = true;
+              bool more = false;  // a later tile of this unit for x
+              for (int j = k + 1; j < tl.nt && !more; ++j) more = act(x, j);
+              if (!more) {
+                dev::umma_commit(&o_done[x]);
+                ++units[x];
+              }
+            }
+            if (k + 1 < tl.nt) {
+              if (!kready) {
+                ok = dev::mbar_wait(&kfull[kst], kph, p.err);
+                kready = true;
+                if (!ok) break;
+              }
+              if (act(x, k + 1)) {
+                dev::tc_fence_after();
+                issue_s(x);
+              }
+            }
+          }
+          if (!ok) break;
+          if (k >= 0) {
+            dev::umma_commit(&vempty[vst]);
+            if (++vst == T::NV) {
+              vst = 0;
+              vph ^= 1u;
+            }
+          }
+          if (k + 1 < tl.nt) {
+            dev::umma_commit(&kempty[kst]);
+            if (++kst == T::NK) {
+              kst = 0;
+              kph ^= 1u;
+            }
+          }
+          if (k + 1 == max(0, tl.nt - 1)) dev::umma_commit(q_free);
+        }
+      }
+      // every MMA issued has completed before TMEM may be freed
+      dev::umma_commit(done);
+      dev::mbar_wait(done, 0, nullptr, 100000000ull);
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    // ============================ softmax rows =================================
+    if constexpr (T::FP8) reg_inc();
+    const int x = warp >> 2, quarter = warp & 3;
+    const int r = 32 * quarter + lane;  // this thread's row of tile x: its TMEM lane
+    const uint32_t lane_addr = (uint32_t)(32 * quarter) << 16;
+    const uint32_t ts = tbase + x * kKeys + lane_addr, to = tbase + 2 * kKeys + x * D + lane_addr;
+    uint8_t* qs = smem + T::Q + x * T::TILE;
+    uint32_t scount = 0, ucount = 0;
+    int gv = 0;  // key tiles before this unit (the V ring's position)
+    bool ok = true;
+    auto wait_ok = [&](uint64_t* bar, uint32_t parity) {
+      if (ok) ok = __all_sync(0xffffffffu, dev::mbar_wait(bar, parity, p.err));
+    };
+    for (int n = 0;; ++n) {
+      Unit u;
+      read_unit(n, u, ok);
+      ok = __all_sync(0xffffffffu, ok);
+      __syncwarp();
+      if (lane == 0) dev::mbar_arrive(&uq_empty[n % kUQ]);
+      if (!ok || u.s < 0) break;
+      const Tiles<BS> tl(u, p);
+      const int na = min(u.qn, QB);
+      const int px = u.p0 + x * QB, nx = x ? u.qn - na : na;  // this tile's positions
+      const bool valid = r < nx * G;
+      const int pos = px + r / G;
+      const int qh = u.h * G + r % G;
+      float scale = p.scale_log2, cap_in = p.mod.cap_in, osc = p.out_scale, slope = 0.f;
+      if constexpr (T::FP8) {
+        const int head = u.h / p.mod.sub;
+        if (p.k_head) {
+          const float ks = __ldg(p.k_head + head);
+          scale *= ks;
+          cap_in *= ks;
+        }
+        if (p.v_head) osc *= __ldg(p.v_head + head);
+        // the queries as f16, in place
+        wait_ok(q_raw, (uint32_t)(n & 1));
+#pragma unroll
+        for (int v = 0; v < T::NCH * 8; ++v) {
+          uint4* w = reinterpret_cast<uint4*>(qs + (v >> 3) * kTileRow + r * 128 + (v & 7) * 16);
+          uint4 b = *w;
+          uint32_t* e = &b.x;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            e[i] = dev::pack_f16(dev::bf16_bits_to_f32(e[i] & 0xFFFFu), dev::bf16_bits_to_f32(e[i] >> 16));
+          *w = b;
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) dev::mbar_arrive(q_full);
+      }
+      if constexpr (SLOPES) {
+        if (valid) slope = __ldg(p.mod.slopes + qh) * 1.4426950408889634f;
+      }
+      // y = x * y_in is what the cap's tanh takes (a row past the unit holds
+      // anything and must not ask for the exact form)
+      const float y_in = valid ? cap_in * (0.5f / 1.4426950408889634f) : 0.f;
+      float ref = -1e30f, lsum = 0.f;
+      bool first = true;
+      for (int k = 0; k < tl.nt; ++k) {
+        const int t = tl.tile(k);
+        if (!tl.active(t, px, nx)) continue;
+        wait_ok(&s_full[x], scount & 1);
+        ++scount;
+        dev::tc_fence_after();
+        const int key0 = t * kKeys;
+        // the row sees keys [wlo, hi) and [0, pl) of the tile
+        const int hi = valid ? min(pos + 1, u.len) - key0 : 0;
+        const int wlo = tl.window > 0 ? pos - tl.window + 1 - key0 : 0;
+        const int pl = valid ? u.pfx - key0 : 0;
+        const bool whole = (hi >= kKeys && wlo <= 0) || pl >= kKeys;
+        const bool edge = !__all_sync(0xffffffffu, whole);
+        const bool ahead = SLOPES && __any_sync(0xffffffffu, slope != 0.f && pl > pos + 1 - key0);
+        const float dist = (float)(pos - key0);
+        // arguments of 32 scores: s - rf in log2 units; exact: the cap's exact
+        // form; zmax: the largest y^2 of the polynomial form
+        auto args = [&](int c, float (&a)[32], float rf, bool exact, float& zmax) {
+          uint32_t w[32];
+          dev::tmem_ld32(ts + 32 * c, w);
+          if (CAPS && edge) {  // what a hidden key holds must not choose the cap's form
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int key = 32 * c + i;
+              w[i] = (key < pl || (key < hi && key >= wlo)) ? w[i] : 0u;
+            }
+          }
+          const float base = SLOPES ? fmaf(-slope, dist - (float)(32 * c), -rf) : -rf;
+          if (CAPS && exact) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              a[i] = dev::capped(__uint_as_float(w[i]), cap_in, p.mod.cap_out) + (SLOPES ? fmaf(slope, (float)i, base) : base);
+          } else if constexpr (CAPS) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float y = __uint_as_float(w[i]) * y_in, z = y * y;
+              zmax = fmaxf(zmax, z);
+              float q = fmaf(z, p.mod.poly[4], p.mod.poly[3]);
+              q = fmaf(z, q, p.mod.poly[2]);
+              q = fmaf(z, q, p.mod.poly[1]);
+              q = fmaf(z, q, p.mod.poly[0]);
+              a[i] = fmaf(y, q, SLOPES ? fmaf(slope, (float)i, base) : base);
+            }
+          } else if constexpr (MOD == kSlope) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) a[i] = fmaf(__uint_as_float(w[i]), scale, fmaf(slope, (float)i, base));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) a[i] = fmaf(__uint_as_float(w[i]), scale, base);
+          }
+          if (SLOPES && ahead) {  // keys past the row's position: their distance has the other sign
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float over = fmaxf(0.f, (float)(32 * c + i) - dist);
+              a[i] = fmaf(-2.f * slope, over, a[i]);
+            }
+          }
+          if (edge) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int key = 32 * c + i;
+              a[i] = (key < pl || (key < hi && key >= wlo)) ? a[i] : -INFINITY;
+            }
+          }
+        };
+        auto row_max = [&](bool exact, float& zmax) {
+          float m = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            float a[32];
+            args(c, a, 0.f, exact, zmax);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) m = dev::max3(m, a[i], a[i + 1]);
+          }
+          return m;
+        };
+        uint32_t pk[kKeys / 2];
+        auto weights = [&](float rf, bool exact, float& zmax) {
+          float sum = 0.f;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float a[32], s4[4] = {0.f, 0.f, 0.f, 0.f};
+            args(c, a, rf, exact, zmax);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float e0 = dev::ex2(a[2 * i]), e1 = dev::ex2(a[2 * i + 1]);
+              s4[i & 3] += e0 + e1;
+              pk[16 * c + i] = T::FP8 ? dev::pack_f16(e0, e1) : dev::pack_bf16(e0, e1);
+            }
+            sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+          }
+          return sum;
+        };
+        float zmax = 0.f;
+        bool exact = false;
+        if (first) {
+          float m = row_max(false, zmax);
+          if (CAPS && __any_sync(0xffffffffu, !(zmax <= kCapFast * kCapFast))) {
+            exact = true;
+            m = row_max(true, zmax);
+          }
+          ref = fmaxf(ref, m);
+        }
+        float sum = weights(ref, exact, zmax);
+        if (CAPS && !exact && __any_sync(0xffffffffu, !(zmax <= kCapFast * kCapFast))) {
+          exact = true;
+          sum = weights(ref, true, zmax);
+        }
+        if (!first && __any_sync(0xffffffffu, !(sum <= T::BIG))) {
+          // the reference moves (rare).  O is at rest: S of this tile was
+          // issued behind the previous PV
+          const float m = row_max(exact, zmax);
+          const bool move = m > ref;
+          const float alpha = move ? dev::ex2(ref - m) : 1.f;
+          if (move) ref = m;
+          lsum *= alpha;
+          sum = weights(ref, exact, zmax);
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t w[32];
+            dev::tmem_ld32(to + 32 * c, w);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * alpha);
+            dev::tmem_st32(to + 32 * c, w);
+          }
+        }
+        first = false;
+        lsum += sum;
+        dev::tmem_st64(ts, pk);
+        if constexpr (!T::FP8) {
+          // V rows that no row of the unit sees may hold anything (0 * NaN):
+          // zeroed by the first tile of the unit that uses them
+          const bool mine = x == 0 || !tl.active(t, u.p0, na);
+          auto zero_v = [&](int z0, int z1) {
+            if (z0 >= z1 || !mine) return;
+            const int gg = gv + k;
+            wait_ok(&vfull[gg % T::NV], (uint32_t)((gg / T::NV) & 1));
+            uint8_t* vt = smem + T::V + (gg % T::NV) * T::TILE;
+            for (int i = tid & 127; i < (z1 - z0) * T::NCH * 8; i += 128) {
+              const int key = z0 + i / (T::NCH * 8), rest = i % (T::NCH * 8);
+              *reinterpret_cast<uint4*>(vt + (rest >> 3) * kTileRow + key * 128 + (rest & 7) * 16) =
+                  make_uint4(0, 0, 0, 0);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          };
+          zero_v(max(0, max(u.len, u.pfx) - key0), min(kKeys, tl.nb * BS - key0));
+          zero_v(max(u.pfx, key0) - key0, min(tl.lo, key0 + kKeys) - key0);
+        }
+        dev::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) dev::mbar_arrive(&p_full[x]);
+      }
+      gv += tl.nt;
+      // ---- O / sum -> the output row; then O is free ----
+      const int64_t at = ((int64_t)(u.row0 + x * QB + r / G) * hq + qh) * D;
+      uint4* dst = reinterpret_cast<uint4*>(p.out + at * 2);
+      if (!first) {
+        wait_ok(&o_done[x], ucount & 1);
+        ++ucount;
+        dev::tc_fence_after();
+        const float inv = lsum > 0.f ? osc / lsum : (lsum == 0.f ? 0.f : lsum);  // nothing visible: 0; NaN stays
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t w[32];
+          dev::tmem_ld32(to + 32 * c, w);
+          if (valid && ok) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t o[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                o[e] = dev::pack_bf16(__uint_as_float(w[8 * i + 2 * e]) * inv, __uint_as_float(w[8 * i + 2 * e + 1]) * inv);
+              dst[4 * c + i] = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+          }
+        }
+        dev::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) dev::mbar_arrive(&o_free[x]);
+      } else if (valid && ok) {  // no tile at all
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) dst[i] = make_uint4(0, 0, 0, 0);
+      }
+    }
+  } else if (T::FP8 && warp >= kConvWarp) {
+    // ==================== e4m3 -> f16 tiles ====================================
+    if constexpr (T::FP8) {
+      reg_dec();
+      const int ct = tid - 32 * kConvWarp;  // 0..127
+      bool ok = true;
+      int g = 0;   // tiles of K (and of V) converted
+      int rst = 0;
+      uint32_t rph = 0;
+      auto wait_ok = [&](uint64_t* bar, uint32_t parity) {
+        if (ok) ok = __all_sync(0xffffffffu, dev::mbar_wait(bar, parity, p.err));
+      };
+      auto to_f16 = [&](const uint4& b, uint4& lo, uint4& hi) {
+        dev::e4m3x4_to_f16x2(b.x, lo.x, lo.y);
+        dev::e4m3x4_to_f16x2(b.y, lo.z, lo.w);
+        dev::e4m3x4_to_f16x2(b.z, hi.x, hi.y);
+        dev::e4m3x4_to_f16x2(b.w, hi.z, hi.w);
+      };
+      for (int n = 0;; ++n) {
+        Unit u;
+        read_unit(n, u, ok);
+        ok = __all_sync(0xffffffffu, ok);
+        __syncwarp();
+        if (lane == 0) dev::mbar_arrive(&uq_empty[n % kUQ]);
+        if (!ok || u.s < 0) break;
+        const Tiles<BS> tl(u, p);
+        for (int k = 0; k < tl.nt; ++k, ++g) {
+          const int key0 = tl.tile(k) * kKeys;
+          const int ring = g % 2;
+          const uint32_t par = (uint32_t)((g / 2) & 1);
+          static_assert(T::NK == 2 && T::NV == 2, "rings of two");
+          // ---- K: rows of D bytes -> rows of D f16, 64-element chunks
+          wait_ok(&rfull[rst], rph);
+          if (g >= 2) wait_ok(&kempty[ring], par ^ 1u);
+          {
+            const uint8_t* raw = smem + T::R + rst * T::RAW;
+            uint8_t* out = smem + T::K + ring * T::TILE;
+#pragma unroll
+            for (int i = 0; i < T::RAW / 16 / 128; ++i) {
+              const int idx = i * 128 + ct, key = idx / (D / 16), pc = idx % (D / 16);
+              uint4 a, b;
+              to_f16(*reinterpret_cast<const uint4*>(raw + idx * 16), a, b);
+              uint8_t* row = out + (pc >> 2) * kTileRow + key * 128;
+              *reinterpret_cast<uint4*>(row + (((2 * (pc & 3)) ^ (key & 7)) << 4)) = a;
+              *reinterpret_cast<uint4*>(row + (((2 * (pc & 3) + 1) ^ (key & 7)) << 4)) = b;
+            }
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            dev::mbar_arrive(&kfull[ring]);
+            dev::mbar_arrive(&rempty[rst]);
+          }
+          if (++rst == T::NR) {
+            rst = 0;
+            rph ^= 1u;
+          }
+          // ---- V: blocks [D][BS] -> rows of d, keys contiguous, 64-key chunks;
+          // keys that no row of the unit sees become 0 (0 * NaN)
+          wait_ok(&rfull[rst], rph);
+          if (g >= 2) wait_ok(&vempty[ring], par ^ 1u);
+          {
+            const uint8_t* raw = smem + T::R + rst * T::RAW;
+            uint8_t* out = smem + T::V + ring * T::TILE;
+            const int d = ct % D;
+            // keys [0, za) and [zb, ze) of the tile are seen
+            const int za = u.pfx - key0, zb = tl.lo - key0, ze = min(tl.kend, tl.nb * BS) - key0;
+#pragma unroll
+            for (int i = 0; i < 8 * D / 128; ++i) {
+              const int kg = i * (128 / D) + ct / D;  // 16 keys
+              const int jb = kg * 16 / BS, off = kg * 16 % BS;
+              uint4 a, b;
+              to_f16(*reinterpret_cast<const uint4*>(raw + jb * BS * D + d * BS + off), a, b);
+              const int f = kg * 16;
+              if (!((f + 16 <= za) || (f >= zb && f + 16 <= ze))) {
+                uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const int k0 = f + 2 * e, k1 = k0 + 1;
+                  if (!(k0 < za || (k0 >= zb && k0 < ze))) w[e] &= 0xFFFF0000u;
+                  if (!(k1 < za || (k1 >= zb && k1 < ze))) w[e] &= 0x0000FFFFu;
+                }
+                a = make_uint4(w[0], w[1], w[2], w[3]);
+                b = make_uint4(w[4], w[5], w[6], w[7]);
+              }
+              uint8_t* row = out + (kg >> 2) * (D * 128) + d * 128;
+              *reinterpret_cast<uint4*>(row + (((2 * (kg & 3)) ^ (d & 7)) << 4)) = a;
+              *reinterpret_cast<uint4*>(row + (((2 * (kg & 3) + 1) ^ (d & 7)) << 4)) = b;
+            }
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            dev::mbar_arrive(&vfull[ring]);
+            dev::mbar_arrive(&rempty[rst]);
+          }
+          if (++rst == T::NR) {
+            rst = 0;
+            rph ^= 1u;
+          }
+        }
+      }
+    }
+  } else {
+    if constexpr (T::FP8) reg_dec();  // the idle warp of the loaders' warpgroup
+  }
+
+  // ---- free TMEM once every warp is past its last tcgen05 access ----
+  dev::tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    dev::tc_fence_after();
+    dev::tmem_dealloc(tbase, kTmemCols);
+  }
+  finish_queue();
+}
+
+template <int KV, int D, int BS, int MOD>
+cudaError_t launch(const PrefillParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const CUtensorMap& tm_q,
+                   int grid, cudaStream_t stream) {
+  using T = C<KV, D, BS>;
+  auto kern = chunk_biased_kernel<KV, D, BS, MOD>;
+  static int set_for[64] = {0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !set_for[dev]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::TOTAL);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) set_for[dev] = 1;
+  }
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(T::THREADS);
+  cfg.dynamicSmemBytes = T::TOTAL;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, tm_k, tm_v, tm_q, p);
+}
+
+template <int KV, int D, int BS>
+cudaError_t launch_mod(const PrefillParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                       const CUtensorMap& tm_q, int grid, cudaStream_t stream) {
+  if (p.mod.cap_out > 0.f)
+    return p.mod.slopes ? launch<KV, D, BS, kCapSlope>(p, tm_k, tm_v, tm_q, grid, stream)
+                        : launch<KV, D, BS, kCap>(p, tm_k, tm_v, tm_q, grid, stream);
+  if (p.mod.slopes) return launch<KV, D, BS, kSlope>(p, tm_k, tm_v, tm_q, grid, stream);
+  return launch<KV, D, BS, kMask>(p, tm_k, tm_v, tm_q, grid, stream);
+}
+
+template <int KV>
+cudaError_t launch_kv(const PrefillParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const CUtensorMap& tm_q,
+                      int head_dim, int block_size, int grid, cudaStream_t stream) {
+  if (head_dim == 128)
+    return block_size == 16 ? launch_mod<KV, 128, 16>(p, tm_k, tm_v, tm_q, grid, stream)
+                            : launch_mod<KV, 128, 32>(p, tm_k, tm_v, tm_q, grid, stream);
+  return block_size == 16 ? launch_mod<KV, 64, 16>(p, tm_k, tm_v, tm_q, grid, stream)
+                          : launch_mod<KV, 64, 32>(p, tm_k, tm_v, tm_q, grid, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_biased(const PrefillParams& p_in, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                const CUtensorMap& tm_q, int kv, int head_dim, int block_size, int num_tokens,
+                                int num_sms, cudaStream_t stream) {
+  PrefillParams p = p_in;
+  if (p.group < 1 || p.group > kRows || p.rows.num_seqs > kGroup * kMaxGroups) return cudaErrorNotSupported;
+  for (int i = 0; i < 5; ++i) p.mod.poly[i] = kTanh[i] * p.mod.cap_out;
+  const int qb2 = 2 * (kRows / p.group);
+  const int64_t bound = ((int64_t)num_tokens / qb2 + p.rows.num_seqs) * p.num_kv_heads;  // units, at most
+  if (bound <= 0) return cudaSuccess;
+  if (bound >= INT32_MAX) return cudaErrorNotSupported;
+  const int grid = (int)(bound < num_sms ? bound : num_sms);
+  return kv == kBF16 ? launch_kv<kBF16>(p, tm_k, tm_v, tm_q, head_dim, block_size, grid, stream)
+                     : launch_kv<kFP8>(p, tm_k, tm_v, tm_q, head_dim, block_size, grid, stream);
+}
+
+}  // namespace pa

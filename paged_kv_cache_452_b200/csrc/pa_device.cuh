@@ -186,6 +186,10 @@ __host__ __device__ constexpr uint32_t umma_idesc_bf16(int n, bool b_mn_major) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
          ((uint32_t)(128 >> 4) << 24);
 }
+// The same with f16 A and B.
+__host__ __device__ constexpr uint32_t umma_idesc_f16(int n, bool b_mn_major) {
+  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
 // D[tmem] = A * B (+ D if `accumulate`), both operands from shared memory;
 // issued by one thread.
 __device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,

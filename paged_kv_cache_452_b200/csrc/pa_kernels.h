@@ -97,6 +97,7 @@ struct ScoreMod {
   int32_t window;         // 0: none
   const float* slopes;    // [num_q_heads] (device) or nullptr
   const int32_t* prefix;  // [num_seqs] (device) or nullptr
+  float poly[5];          // the chunk kernel's: cap_out times its tanh polynomial
   int32_t sub;            // kernel kv heads per pool kv head (a group too large for the kernel is cut)
 };
 
@@ -184,6 +185,8 @@ struct PrefillParams {
   float* pfx_ml;               // [chunks][M][Hq][2] (max reference, sum), log2 domain
   float* pfx_o;                // [chunks][M][Hq][D]
   ScoreMod mod;                // the biased kernel's
+  const uint8_t* k_raw;        // an e4m3 pool
+  const uint8_t* v_raw;
   float out_scale;             // the biased kernel's: 1, or an e4m3 pool's V scale
   const float* k_head;         // e4m3 per-kv-head scales (device) or nullptr
   const float* v_head;
@@ -221,11 +224,11 @@ bool prefill_umma_supported(int kv, int q, int head_dim, int block_size, int gro
 cudaError_t launch_prefill_umma(const PrefillParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                 const CUtensorMap& tm_q, int head_dim, int block_size, int num_tokens, int num_sms,
                                 cudaStream_t stream);
-// The same rows with p.mod applied, any group up to 128 (a unit's rows are
-// 128 / G whole positions).
-cudaError_t launch_prefill_biased(const PrefillParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
-                                  const CUtensorMap& tm_q, int kv, int head_dim, int block_size, int num_tokens,
-                                  int num_sms, cudaStream_t stream);
+// Rows of more than one per sequence with p.mod applied, any group up to 128;
+// an e4m3 pool comes through k_raw and v_raw, a bf16 one through the maps.
+cudaError_t launch_chunk_biased(const PrefillParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                const CUtensorMap& tm_q, int kv, int head_dim, int block_size, int num_tokens,
+                                int num_sms, cudaStream_t stream);
 cudaError_t launch_prefill_tc(const PrefillParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                               int head_dim, int block_size, int num_tokens, cudaStream_t stream);
 
@@ -251,7 +254,7 @@ struct BiasedSimtParams {
   SimtParams a;
   ScoreMod mod;
 };
-cudaError_t launch_attn_biased_simt(const BiasedSimtParams& p, int q_dtype, int kv_dtype, cudaStream_t stream);
+cudaError_t launch_attn_biased_simt(const BiasedSimtParams& p, int kv_dtype, cudaStream_t stream);
 cudaError_t launch_attn_simt(const SimtParams& p, int q_dtype, int kv_dtype, cudaStream_t stream);
 
 }  // namespace pa

@@ -139,16 +139,7 @@ __device__ __forceinline__ uint32_t swz(int r, int u) { return (uint32_t)(r * 12
 // head, 128 / G member sequences, one chunk of the prefix's keys); its rows
 // are the members' decode queries, every prefix key is visible to every row,
 // and it writes partial (max reference, sum, unnormalised O) rows.
-// MOD: the biased form (pa_decode_chunked_prefill_biased; kPlain: none): the
-// scores take p.mod's cap and distance bias, a row sees its window and the
-// prefix, and the group may be any up to 128 (a unit is then 128 / G whole
-// positions; rows past them compute nothing that is kept).  Its tiles run from
-// the last to the first: with a distance bias the nearest keys carry a row's
-// largest weights, so the first tile's reference serves the others.  Tiles
-// between the prefix and the unit's window are not visited.
-constexpr int kPlain = 0, kMask = 1, kSlope = 2, kCap = 3;
-
-template <int D, int BS, bool PFX, int MOD>
+template <int D, int BS, bool PFX>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_umma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const __grid_constant__ CUtensorMap tm_q, const PrefillParams p) {
@@ -172,7 +163,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = p.group, hq = p.num_q_heads, hkv = p.num_kv_heads;
   const int QB = kRows / G;  // query positions per unit
-  const int pool_heads = MOD ? hkv / p.mod.sub : hkv;  // kv heads of the pool
 
   // Launched right behind the decode kernel of the same step, this grid starts
   // only once every decode CTA has passed its own wait for the step's cache
@@ -231,7 +221,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   if ((int)blockIdx.x >= nunits) {  // nothing allocated yet
     finish_queue();
-    if (MOD && p.after_decode) dev::grid_dep_wait();
     return;
   }
 
@@ -242,14 +231,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   // blk0 .. blk0 + nbneed - 1 of sequence s's table row.
   struct Unit {
     int s, h, first, q0, qn, pos0, seq_len, nbneed, ntiles, blk0, chunk;
-    // biased form: prefix keys, the unit's first window key, prefix tiles, tiles skipped after them
-    int pfx, lo, npt, gap;
-    // the k-th tile visited
-    __device__ __forceinline__ int tile(int k) const {
-      if constexpr (!MOD) return k;
-      const int t = ntiles - 1 - k;
-      return t < npt ? t : t + gap;
-    }
   };
   auto unit_of = [&](int idx) {
     Unit u;
@@ -294,23 +275,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     u.pos0 = u.seq_len - qlen;  // position of the sequence's first query row
     u.q0 = qb * QB;             // first query (local index) of the unit
     u.qn = min(QB, qlen - u.q0);
-    int kend = min(u.seq_len, u.pos0 + u.q0 + u.qn);  // keys the unit needs: [0, kend)
-    if constexpr (MOD) {
-      u.pfx = p.mod.prefix ? max(0, min(u.seq_len, __ldg(p.mod.prefix + lo))) : 0;
-      u.lo = p.mod.window > 0 ? max(0, u.pos0 + u.q0 - p.mod.window + 1) : 0;
-      kend = max(kend, u.pfx);
-    }
+    const int kend = min(u.seq_len, u.pos0 + u.q0 + u.qn);  // keys the unit needs: [0, kend)
     u.nbneed = (kend + BS - 1) / BS;
     if (u.nbneed > p.max_blocks) {
       if (warp == 2 && lane == 0) atomicCAS(p.err, 0, 3);  // (one reporter)
       u.nbneed = p.max_blocks;
     }
     u.ntiles = (u.nbneed * BS + kKeys - 1) / kKeys;
-    if constexpr (MOD) {
-      u.npt = min((u.pfx + kKeys - 1) / kKeys, u.ntiles);
-      u.gap = max(0, min(u.lo / kKeys, u.ntiles) - u.npt);
-      u.ntiles -= u.gap;
-    }
     return u;
   };
 
@@ -361,18 +332,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* ringb = is_v ? vring : kring;
     const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
     const uint64_t pol = dev::policy_evict_last();  // the sequence's other units read the same tiles
-    const int32_t oob_row = p.num_blocks * pool_heads * BS;  // past the pool: TMA fills zeros
+    const int32_t oob_row = p.num_blocks * hkv * BS;  // past the pool: TMA fills zeros
     const int c = lane / C::BPT, j = lane % C::BPT;   // this lane's box: 128-byte chunk, block in tile
     // this lane's table entry for tile k of unit u (-2: past the needed
     // blocks); the check waits until the entry is used, so the load overlaps
     // a tile
     auto entry = [&](const Unit& u, int k) -> int32_t {
-      const int b = u.tile(k) * C::BPT + j;
-      bool need = lane < C::BOXES && b < u.nbneed;
-      // blocks with no key that a row of the unit sees are not read: their
-      // table entries may be stale
-      if constexpr (MOD) need = need && (b * BS < u.pfx || b >= u.lo / BS);
-      return need ? __ldg(p.block_tables + (int64_t)u.s * p.max_blocks + u.blk0 + b)
+      const int b = k * C::BPT + j;
+      return (lane < C::BOXES && b < u.nbneed) ? __ldg(p.block_tables + (int64_t)u.s * p.max_blocks + u.blk0 + b)
                                                 : -2;
     };
     bool ok = true;
@@ -413,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // unit are other rows or zeros, masked by the row warps)
           if (n > 0 && ok) ok = __all_sync(0xffffffffu, dev::mbar_wait(B.q_free, (uint32_t)((n - 1) & 1), p.err));
           if (ok && lane == 0) {
-            dev::mbar_arrive_expect_tx(B.q_full, MOD ? (uint32_t)(C::NCH * QB * G * 128) : (uint32_t)C::QBYTES);
+            dev::mbar_arrive_expect_tx(B.q_full, (uint32_t)C::QBYTES);
 #pragma unroll
             for (int cq = 0; cq < C::NCH; ++cq)
               dev::tma_load_3d(qs + cq * kChunk, &tm_q, cq * 64, u.h * G, u.first + u.q0, B.q_full, qpol);
@@ -435,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             atomicCAS(p.err, 0, 2);
             blk = 0;
           }
-          y = (blk * pool_heads + (MOD ? u.h / p.mod.sub : u.h)) * BS;
+          y = (blk * hkv + u.h) * BS;
         }
         if (lane == 0) dev::mbar_arrive_expect_tx(&fullb[st], (uint32_t)C::KVT);
         __syncwarp();
@@ -583,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 8; i < kKeys; i += 2) mp[(i >> 1) & 7] = dev::max3(mp[(i >> 1) & 7], sv[i], sv[i + 1]);
       return dev::max3(dev::max3(mp[0], mp[1], mp[2]), dev::max3(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7])) *
-             (MOD ? 1.f : p.scale_log2);
+             p.scale_log2;
     };
     // P = 2^(s * scale - ref) as bf16 pairs, and the tile's fp32 sum of them
     auto weights = [&](const float (&sv)[kKeys], float ref, uint32_t (&pk)[kKeys / 2]) {
@@ -592,31 +559,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < 8; ++i) sp[i] = 0.f;
 #pragma unroll
       for (int i = 0; i < kKeys / 2; ++i) {
-        const float a = dev::ex2(MOD ? sv[2 * i] - ref : fmaf(sv[2 * i], p.scale_log2, -ref));
-        const float b = dev::ex2(MOD ? sv[2 * i + 1] - ref : fmaf(sv[2 * i + 1], p.scale_log2, -ref));
+        const float a = dev::ex2(fmaf(sv[2 * i], p.scale_log2, -ref));
+        const float b = dev::ex2(fmaf(sv[2 * i + 1], p.scale_log2, -ref));
         sp[i & 7] += a + b;
         pk[i] = dev::pack_bf16(a, b);
       }
       return ((sp[0] + sp[1]) + (sp[2] + sp[3])) + ((sp[4] + sp[5]) + (sp[6] + sp[7]));
-    };
-    // the biased form: a tile's scores (log2 units) with cap, bias and masks
-    // applied; `hi`, `wlo`, `pl`: the row sees keys [wlo, hi) and [0, pl) of
-    // the tile; `dist`: its distance from the tile's first key
-    auto load_biased = [&](uint32_t ts, float (&sv)[kKeys], bool whole, int hi, int wlo, int pl, float dist, float slope) {
-      uint32_t w[kKeys];
-      dev::tmem_ld(ts, w);
-#pragma unroll
-      for (int i = 0; i < kKeys; ++i) {
-        float x = __uint_as_float(w[i]);
-        if constexpr (MOD == kCap) x = dev::capped(x, p.mod.cap_in, p.mod.cap_out);
-        else x *= p.scale_log2;
-        if constexpr (MOD != kMask) x = fmaf(-slope, fabsf(dist - (float)i), x);
-        sv[i] = x;
-      }
-      if (!whole) {
-#pragma unroll
-        for (int i = 0; i < kKeys; ++i) sv[i] = (i < pl || (i < hi && i >= wlo)) ? sv[i] : -INFINITY;
-      }
     };
     int g0 = 0;
     for (int n = 0;; ++n) {
@@ -637,10 +585,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       // member slot first + r / G
       const int qrow = !PFX ? u.first + u.q0 + r / G : (valid ? __ldg(p.pfx_members + u.first + r / G) : 0);
       const int64_t grow = ((int64_t)qrow * hq + (int64_t)u.h * G + r % G) * D;
-      float slope = 0.f;
-      if constexpr (MOD >= kSlope) {
-        if (p.mod.slopes && valid) slope = __ldg(p.mod.slopes + u.h * G + r % G) * 1.4426950408889634f;
-      }
       // ---- shared-prefix mode: the member's Q row into the swizzled Q tile
       // (zero for rows past the unit); the previous unit's MMAs have all
       // completed (its output was read after them)
@@ -661,31 +605,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait_ok(&B.s_full[g & 1], (uint32_t)((g >> 1) & 1));
         dev::tc_fence_after();
         const uint32_t ts = t_s0 + (uint32_t)((g & 1) * kKeys) + lane_addr;
-        const int key0 = u.tile(k) * kKeys;
-        const int lim = min(pos + 1, u.seq_len) - key0;  // keys [0, lim) of the tile are visible
-        bool whole = valid && lim >= kKeys;
-        int wlo = 0, pl = 0;
-        if constexpr (MOD) {  // ... those from wlo on, and [0, pl)
-          wlo = p.mod.window > 0 ? pos - p.mod.window + 1 - key0 : 0;
-          pl = u.pfx - key0;
-          whole = valid && ((lim >= kKeys && wlo <= 0) || pl >= kKeys);
-          if (!valid) {  // sees nothing
-            wlo = kKeys;
-            pl = 0;
-          }
-        }
+        const int lim = min(pos + 1, u.seq_len) - k * kKeys;  // keys [0, lim) of the tile are visible
+        const bool whole = valid && lim >= kKeys;
         float sv[kKeys];
-        auto load = [&]() {
-          if constexpr (MOD) load_biased(ts, sv, whole, lim, wlo, pl, (float)(pos - key0), slope);
-          else load_s(ts, sv, whole, lim, valid);
-        };
-        load();
+        load_s(ts, sv, whole, lim, valid);
         if (k == 0) ref = fmaxf(ref, row_max(sv));
         uint32_t pk[kKeys / 2];
         float tsum = weights(sv, ref, pk);
         if (k > 0 && __any_sync(0xffffffffu, !(tsum <= kBig))) {
           // slow path (the S buffer is still this tile's: it is released below)
-          load();
+          load_s(ts, sv, whole, lim, valid);
           const float mx = row_max(sv);
           const bool move = mx > ref;
           const float alpha = move ? dev::ex2(ref - mx) : 1.f;
@@ -719,8 +648,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         dev::tmem_st(t_p + (uint32_t)((g & 1) * (kKeys / 2)) + lane_addr, pk);
         // the tile holding the context's end: slots past it hold stale pool
         // bytes (masked scores, but 0 * NaN would poison P V): zero their V rows
-        auto zero_v = [&](int stale0, int stale1) {
-          if (stale0 >= stale1) return;
+        const int key0 = k * kKeys;
+        const int stale0 = u.seq_len - key0, stale1 = min(kKeys, u.nbneed * BS - key0);
+        if (stale0 < stale1) {
           wait_ok(&B.vfull[g % NSV], (uint32_t)((g / NSV) & 1));
           uint8_t* vt = vring + (size_t)(g % NSV) * C::KVT;
           const int units = (stale1 - stale0) * C::NCH * 8;
@@ -730,11 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 make_uint4(0, 0, 0, 0);
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        };
-        zero_v(u.seq_len - key0, min(kKeys, u.nbneed * BS - key0));
-        // and the keys between the prefix and the unit's window, which none
-        // of its rows see
-        if constexpr (MOD) zero_v(max(u.pfx, key0) - key0, min(u.lo, key0 + kKeys) - key0);
+        }
         dev::tc_fence_before();
         __syncwarp();
         if (lane == 0) dev::mbar_arrive(&B.p_full[g & 1]);
@@ -759,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     __uint_as_float(w[4 * uu + 2]), __uint_as_float(w[4 * uu + 3]));
           }
         } else {
-          const float inv = valid ? (MOD ? p.out_scale : 1.f) / lsum : 0.f;
+          const float inv = valid ? 1.f / lsum : 0.f;
           uint4* dst = reinterpret_cast<uint4*>(p.out + grow * 2);
           if (valid && ok) {
 #pragma unroll
@@ -789,18 +715,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     dev::tmem_dealloc(tbase, kTmemCols);
   }
   finish_queue();
-  // this grid did not wait for the step's decode grid to finish, and a later
-  // grid of the stream may wait for this one alone
-  if (MOD && p.after_decode) dev::grid_dep_wait();
 }
 
-template <int D, int BS, bool PFX = false, int MOD = kPlain>
+template <int D, int BS, bool PFX = false>
 cudaError_t launch_u(const PrefillParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const CUtensorMap& tm_q,
                      int grid,
                      cudaStream_t stream) {
   using C = U<D, BS>;
   const ULayout L = u_layout(C::QBYTES, C::KVT, p.nstages, p.nstages_v, p.rows.num_seqs);
-  auto kern = prefill_umma_kernel<D, BS, PFX, MOD>;
+  auto kern = prefill_umma_kernel<D, BS, PFX>;
   static int set_for[64] = {0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -874,38 +797,6 @@ cudaError_t launch_prefix_umma(const PrefillParams& p_in, const CUtensorMap& tm_
   if (head_dim == 128 && block_size == 32) return launch_u<128, 32, true>(p, tm_k, tm_v, tm_k, (int)grid, stream);
   if (head_dim == 64 && block_size == 16) return launch_u<64, 16, true>(p, tm_k, tm_v, tm_k, (int)grid, stream);
   if (head_dim == 64 && block_size == 32) return launch_u<64, 32, true>(p, tm_k, tm_v, tm_k, (int)grid, stream);
-  return cudaErrorNotSupported;
-}
-
-template <int D, int BS>
-static cudaError_t launch_biased_mod(const PrefillParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
-                                     const CUtensorMap& tm_q, int grid, cudaStream_t stream) {
-  if (p.mod.cap_out > 0.f) return launch_u<D, BS, false, kCap>(p, tm_k, tm_v, tm_q, grid, stream);
-  if (p.mod.slopes) return launch_u<D, BS, false, kSlope>(p, tm_k, tm_v, tm_q, grid, stream);
-  return launch_u<D, BS, false, kMask>(p, tm_k, tm_v, tm_q, grid, stream);
-}
-
-cudaError_t launch_prefill_biased(const PrefillParams& p_in, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
-                                  const CUtensorMap& tm_q, int kv, int head_dim, int block_size, int num_tokens,
-                                  int num_sms, cudaStream_t stream) {
-  PrefillParams p = p_in;
-  if (kv != kBF16 || p.group < 1 || p.group > kRows) return cudaErrorNotSupported;
-  const int nch = head_dim / 64;
-  const int qbytes = nch * kChunk, kvt = nch * kChunk;
-  const int fixed = (int)u_layout(qbytes, kvt, 0, 0, p.rows.num_seqs).total;
-  const int nbuf = (kSmemOptIn - kStaticSmem - fixed) / (kvt + 16);
-  const int nsk = min(4, nbuf / 2), nsv = min(4, nbuf - nbuf / 2);
-  if (nsk < 2 || nsv < 2) return cudaErrorNotSupported;
-  p.nstages = nsk;
-  p.nstages_v = nsv;
-  const int qb = kRows / p.group;
-  const int64_t bound = ((int64_t)num_tokens / qb + p.rows.num_seqs) * p.num_kv_heads;  // units, at most
-  if (bound <= 0) return cudaSuccess;
-  const int grid = (int)(bound < num_sms ? bound : num_sms);
-  if (head_dim == 128 && block_size == 16) return launch_biased_mod<128, 16>(p, tm_k, tm_v, tm_q, grid, stream);
-  if (head_dim == 128 && block_size == 32) return launch_biased_mod<128, 32>(p, tm_k, tm_v, tm_q, grid, stream);
-  if (head_dim == 64 && block_size == 16) return launch_biased_mod<64, 16>(p, tm_k, tm_v, tm_q, grid, stream);
-  if (head_dim == 64 && block_size == 32) return launch_biased_mod<64, 32>(p, tm_k, tm_v, tm_q, grid, stream);
   return cudaErrorNotSupported;
 }
 
