@@ -589,120 +589,129 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
         const bool edge = !__all_sync(0xffffffffu, whole);
         const bool ahead = SLOPES && __any_sync(0xffffffffu, slope != 0.f && pl > pos + 1 - key0);
         const float dist = (float)(pos - key0);
-        // arguments of 32 scores: s - rf in log2 units; exact: the cap's exact
-        // form; zmax: the largest y^2 of the polynomial form
-        auto args = [&](int c, float (&a)[32], float rf, bool exact, float& zmax) {
+        // 32 scores of the row's tile -> exponents s - rf in log2 units, every
+        // key of the chunk visible and none past the row's position
+        auto plain_args = [&](int c, float (&a)[32], float rf, float& zmax) {
           uint32_t w[32];
           dev::tmem_ld32(ts + 32 * c, w);
-          if (CAPS && edge) {  // what a hidden key holds must not choose the cap's form
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int key = 32 * c + i;
-              w[i] = (key < pl || (key < hi && key >= wlo)) ? w[i] : 0u;
-            }
-          }
           const float base = SLOPES ? fmaf(-slope, dist - (float)(32 * c), -rf) : -rf;
-          if (CAPS && exact) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              a[i] = dev::capped(__uint_as_float(w[i]), cap_in, p.mod.cap_out) + (SLOPES ? fmaf(slope, (float)i, base) : base);
-          } else if constexpr (CAPS) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
+          for (int i = 0; i < 32; ++i) {
+            const float b = SLOPES ? fmaf(slope, (float)i, base) : base;
+            if constexpr (CAPS) {
               const float y = __uint_as_float(w[i]) * y_in, z = y * y;
               zmax = fmaxf(zmax, z);
               float q = fmaf(z, p.mod.poly[4], p.mod.poly[3]);
               q = fmaf(z, q, p.mod.poly[2]);
               q = fmaf(z, q, p.mod.poly[1]);
               q = fmaf(z, q, p.mod.poly[0]);
-              a[i] = fmaf(y, q, SLOPES ? fmaf(slope, (float)i, base) : base);
-            }
-          } else if constexpr (MOD == kSlope) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) a[i] = fmaf(__uint_as_float(w[i]), scale, fmaf(slope, (float)i, base));
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) a[i] = fmaf(__uint_as_float(w[i]), scale, base);
-          }
-          if (SLOPES && ahead) {  // keys past the row's position: their distance has the other sign
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float over = fmaxf(0.f, (float)(32 * c + i) - dist);
-              a[i] = fmaf(-2.f * slope, over, a[i]);
-            }
-          }
-          if (edge) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int key = 32 * c + i;
-              a[i] = (key < pl || (key < hi && key >= wlo)) ? a[i] : -INFINITY;
+              a[i] = fmaf(y, q, b);
+            } else {
+              a[i] = fmaf(__uint_as_float(w[i]), scale, b);
             }
           }
         };
-        auto row_max = [&](bool exact, float& zmax) {
-          float m = -INFINITY;
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            float a[32];
-            args(c, a, 0.f, exact, zmax);
+        // the same for any tile: masks, keys past the row's position (their
+        // distance has the other sign), and with `exact` the cap's exact form
+        auto any_args = [&](int c, float (&a)[32], float rf, bool exact, float& zmax) {
+          uint32_t w[32];
+          dev::tmem_ld32(ts + 32 * c, w);
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) m = dev::max3(m, a[i], a[i + 1]);
+          for (int i = 0; i < 32; ++i) {
+            const int key = 32 * c + i;
+            const bool see = key < pl || (key < hi && key >= wlo);
+            const float d = dist - (float)key;
+            float x = see ? __uint_as_float(w[i]) : 0.f;  // what a hidden key holds must not choose the cap's form
+            if constexpr (CAPS) {
+              if (exact) {
+                x = dev::capped(x, cap_in, p.mod.cap_out);
+              } else {
+                const float y = x * y_in, z = y * y;
+                zmax = fmaxf(zmax, z);
+                float q = fmaf(z, p.mod.poly[4], p.mod.poly[3]);
+                q = fmaf(z, q, p.mod.poly[2]);
+                q = fmaf(z, q, p.mod.poly[1]);
+                x = y * fmaf(z, q, p.mod.poly[0]);
+              }
+            } else {
+              x *= scale;
+            }
+            if (SLOPES) x = fmaf(-slope, fabsf(d), x);
+            a[i] = see ? x - rf : -INFINITY;
           }
-          return m;
         };
-        uint32_t pk[kKeys / 2];
-        auto weights = [&](float rf, bool exact, float& zmax) {
+        auto chunk_sum = [&](const float (&a)[32], uint32_t* out) {
+          float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float e0 = dev::ex2(a[2 * i]), e1 = dev::ex2(a[2 * i + 1]);
+            s4[i & 3] += e0 + e1;
+            out[i] = T::FP8 ? dev::pack_f16(e0, e1) : dev::pack_bf16(e0, e1);
+          }
+          return (s4[0] + s4[1]) + (s4[2] + s4[3]);
+        };
+        bool slow = first || edge || ahead;
+        float zmax = 0.f;
+        if (!slow) {
+          // weights over the reference in hand, kept in registers until they
+          // are known to be in range (S is needed again if not)
+          uint32_t pk[kKeys / 2];
           float sum = 0.f;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            float a[32], s4[4] = {0.f, 0.f, 0.f, 0.f};
-            args(c, a, rf, exact, zmax);
+            float a[32];
+            plain_args(c, a, ref, zmax);
+            sum += chunk_sum(a, pk + 16 * c);
+          }
+          slow = __any_sync(0xffffffffu, !(sum <= T::BIG) || (CAPS && !(zmax <= kCapFast * kCapFast)));
+          if (!slow) {
+            lsum += sum;
+            dev::tmem_st64(ts, pk);
+          }
+        }
+        if (slow) {
+          // the row max first, then the weights, chunk by chunk over S
+          bool exact = false;
+          float m;
+          for (;;) {
+            m = -INFINITY;
+            zmax = 0.f;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              float a[32];
+              any_args(c, a, 0.f, exact, zmax);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float e0 = dev::ex2(a[2 * i]), e1 = dev::ex2(a[2 * i + 1]);
-              s4[i & 3] += e0 + e1;
-              pk[16 * c + i] = T::FP8 ? dev::pack_f16(e0, e1) : dev::pack_bf16(e0, e1);
+              for (int i = 0; i < 32; i += 2) m = dev::max3(m, a[i], a[i + 1]);
             }
-            sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
-          }
-          return sum;
-        };
-        float zmax = 0.f;
-        bool exact = false;
-        if (first) {
-          float m = row_max(false, zmax);
-          if (CAPS && __any_sync(0xffffffffu, !(zmax <= kCapFast * kCapFast))) {
+            if (!CAPS || exact || !__any_sync(0xffffffffu, !(zmax <= kCapFast * kCapFast))) break;
             exact = true;
-            m = row_max(true, zmax);
           }
-          ref = fmaxf(ref, m);
-        }
-        float sum = weights(ref, exact, zmax);
-        if (CAPS && !exact && __any_sync(0xffffffffu, !(zmax <= kCapFast * kCapFast))) {
-          exact = true;
-          sum = weights(ref, true, zmax);
-        }
-        if (!first && __any_sync(0xffffffffu, !(sum <= T::BIG))) {
-          // the reference moves (rare).  O is at rest: S of this tile was
-          // issued behind the previous PV
-          const float m = row_max(exact, zmax);
-          const bool move = m > ref;
+          // the reference moves where the weights would grow past 2^8.  O is
+          // at rest: this tile's S was issued behind the previous PV
+          const bool move = m > ref + 8.f;
           const float alpha = move ? dev::ex2(ref - m) : 1.f;
           if (move) ref = m;
           lsum *= alpha;
-          sum = weights(ref, exact, zmax);
+          if (!first && __any_sync(0xffffffffu, move)) {
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t w[32];
-            dev::tmem_ld32(to + 32 * c, w);
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t w[32];
+              dev::tmem_ld32(to + 32 * c, w);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * alpha);
-            dev::tmem_st32(to + 32 * c, w);
+              for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * alpha);
+              dev::tmem_st32(to + 32 * c, w);
+            }
+          }
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            float a[32];
+            any_args(c, a, ref, exact, zmax);
+            uint32_t pk[16];
+            lsum += chunk_sum(a, pk);
+            dev::tmem_st16(ts + 16 * c, pk);  // over scores already read
           }
         }
         first = false;
-        lsum += sum;
-        dev::tmem_st64(ts, pk);
         if constexpr (!T::FP8) {
           // V rows that no row of the unit sees may hold anything (0 * NaN):
           // zeroed by the first tile of the unit that uses them
