@@ -13,9 +13,9 @@
 // is brought in.  One persistent CTA per SM claims units from a counter.
 //  * TMEM (512 columns): S_A, S_B (128 each), O_A, O_B (head_dim each).  A
 //    tile's weights P (16 bit) go over the first 64 columns of its own S.
-//    One thread issues every MMA, in the order PV_A(k) S_A(k+1) PV_B(k)
-//    S_B(k+1): MMAs of one thread run in order, so S_A(k+1) finds P_A(k)
-//    consumed, and S_A(k+1) being complete says that O_A is at rest.
+//    One thread per query tile issues its MMAs, PV(k) then S(k+1): MMAs of one
+//    thread run in order, so S(k+1) finds P(k) consumed, and S(k+1) being
+//    complete says that O is at rest.
 //  * key tiles (128 keys) run from the last to the first: with a distance
 //    bias the nearest keys carry the largest weights, so the reference that a
 //    row's exponents get from its first tile serves the others.  A later tile
@@ -108,17 +108,36 @@ struct Tiles {
     const int t = nt - 1 - k;
     return t < npt ? t : t + gap;
   }
-  // whether rows at positions [a, a + n) see a key of tile t
-  __device__ __forceinline__ bool active(int t, int a, int n) const {
-    if (n <= 0) return false;
-    if (t < npt) return true;
+  // the steps k at which rows at positions [a, a + n) see a key of the tile
+  // visited: k0 <= k < k1, or k >= kp
+  __device__ __forceinline__ void steps(int a, int n, int& k0, int& k1, int& kp) const {
+    k0 = k1 = nt;
+    kp = nt;
+    if (n <= 0) return;
+    kp = nt - min(npt, nt);
     const int first = window > 0 ? max(0, a - window + 1) : 0;
-    return t * kKeys < a + n && t >= first / kKeys;
+    // tiles [first / kKeys, ceil((a + n) / kKeys)) past the prefix: tile t is step nt - 1 - (t - gap)
+    const int t0 = max(first / kKeys, npt + gap), t1 = min((max(a + n, 0) + kKeys - 1) / kKeys, nt + gap);
+    if (t1 > t0) {
+      k0 = nt + gap - t1;
+      k1 = nt + gap - t0;
+    }
   }
 };
 
-__device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 168;"); }
-__device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 80;"); }
+// Registers move from the loaders', the MMA's and the converters' warpgroups
+// to the two softmax warpgroups: 2 x 128 x 208 + 128 x 88 of the 384 x 168 at
+// launch, and with the converters 2 x 128 x 176 + 2 x 128 x 80 of 512 x 128.
+template <bool FP8>
+__device__ __forceinline__ void reg_inc() {
+  if constexpr (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+  else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+}
+template <bool FP8>
+__device__ __forceinline__ void reg_dec() {
+  if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+}
 
 template <int KV, int D, int BS, int MOD>
 __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
@@ -167,11 +186,11 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
   if (tid == 0) {
     for (int i = 0; i < T::NK; ++i) {
       dev::mbar_init(&kfull[i], T::FP8 ? 4 : 1);
-      dev::mbar_init(&kempty[i], 1);
+      dev::mbar_init(&kempty[i], 2);  // both query tiles' MMAs
     }
     for (int i = 0; i < T::NV; ++i) {
       dev::mbar_init(&vfull[i], T::FP8 ? 4 : 1);
-      dev::mbar_init(&vempty[i], 1);
+      dev::mbar_init(&vempty[i], 2);
     }
     for (int i = 0; i < T::NR; ++i) {
       dev::mbar_init(&rfull[i], 1);
@@ -185,8 +204,8 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
     }
     dev::mbar_init(q_full, T::FP8 ? 8 : 1);
     dev::mbar_init(q_raw, 1);
-    dev::mbar_init(q_free, 1);
-    dev::mbar_init(done, 1);
+    dev::mbar_init(q_free, 2);
+    dev::mbar_init(done, 2);
     for (int i = 0; i < kUQ; ++i) {
       dev::mbar_init(&uq_full[i], 1);
       dev::mbar_init(&uq_empty[i], T::READERS);
@@ -247,7 +266,7 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
 
   if (warp == kKWarp || warp == kVWarp) {
     // ================= claims, and the loads of K / V and Q ======================
-    if constexpr (T::FP8) reg_dec();
+    reg_dec<T::FP8>();
     const bool is_v = warp == kVWarp;
     const uint64_t pol = dev::policy_evict_last();  // the sequence's other units read the same tiles
     const uint64_t qpol = dev::policy_evict_first();
@@ -412,30 +431,24 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
       if (qlast >= 0) dev::mbar_wait(T::FP8 ? q_raw : q_full, (uint32_t)(qlast & 1), nullptr, 100000000ull);
     }
     __syncwarp();
-  } else if (warp == kMmaWarp) {
-    // ============================ MMA issue (one thread) =============================
-    if constexpr (T::FP8) reg_dec();
+  } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+    // ==================== MMA issue: one thread per query tile ====================
+    reg_dec<T::FP8>();
     if (lane == 0) {
+      const int x = warp - kMmaWarp;
       const uint32_t idesc_s = T::FP8 ? dev::umma_idesc_f16(kKeys, false) : dev::umma_idesc_bf16(kKeys, false);
       const uint32_t idesc_o = T::FP8 ? dev::umma_idesc_f16(D, false) : dev::umma_idesc_bf16(D, true);
-      const uint64_t dq = dev::umma_desc_sw128(dev::smem_u32(smem + T::Q), 16, 1024);
+      const uint64_t dq = dev::umma_desc_sw128(dev::smem_u32(smem + T::Q + x * T::TILE), 16, 1024);
       const uint64_t dk = dev::umma_desc_sw128(dev::smem_u32(smem + T::K), 16, 1024);
       // V: bf16 MN-major (d contiguous, 64-wide chunks kTileRow apart); e4m3's
       // converted tile K-major (keys contiguous, 64-key chunks of D rows)
       const uint64_t dv = dev::umma_desc_sw128(dev::smem_u32(smem + T::V), T::FP8 ? 16 : kTileRow, 1024);
+      const uint32_t ts = tbase + x * kKeys, to = tbase + 2 * kKeys + x * D;
+      // ring positions and barrier phases by counters: every instruction here
+      // delays the tensor core's next tile
       int kst = 0, vst = 0;
-      uint32_t kph = 0, vph = 0;
-      uint32_t pcount[2] = {0, 0}, units[2] = {0, 0};
-      bool ok = true;
-      auto issue_s = [&](int x) {
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint64_t off = (uint64_t)(((ks >> 2) * kTileRow + (ks & 3) * 32) >> 4);
-          dev::umma_ss(tbase + x * kKeys, dq + (uint64_t)(x * (T::TILE >> 4)) + off,
-                       dk + (uint64_t)(kst * (T::TILE >> 4)) + off, idesc_s, ks > 0 ? 1u : 0u);
-        }
-        dev::umma_commit(&s_full[x]);
-      };
+      uint32_t kph = 0, vph = 0, pph = 0, oph = 1;
+      bool ok = true, used = false;
       for (int n = 0;; ++n) {
         Unit u;
         read_unit(n, u, ok);
@@ -443,70 +456,68 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
         if (u.s < 0) break;
         const Tiles<BS> tl(u, p);
         const int na = min(u.qn, QB);  // positions of tile A; B has the rest
-        auto act = [&](int x, int k) {
-          return k < tl.nt && tl.active(tl.tile(k), u.p0 + x * QB, x ? u.qn - na : na);
-        };
+        int k0, k1, kp;
+        tl.steps(u.p0 + x * QB, x ? u.qn - na : na, k0, k1, kp);
         ok = ok && dev::mbar_wait(q_full, (uint32_t)(n & 1), p.err);
-        bool begun[2] = {false, false};
-        // step k: the PVs of tile k and the S's of tile k + 1
-        for (int k = -1; k < tl.nt && ok; ++k) {
+        const int nt = tl.nt;
+        bool begun = false;
+        // step k: the PV of tile k and the S of tile k + 1
+        bool now = false;  // this query tile takes key tile k
+        for (int k = -1; k < nt && ok; ++k) {
+          const bool next = k + 1 < nt && ((k + 1 >= k0 && k + 1 < k1) || k + 1 >= kp);
+          // a stage is given back by both threads, also by one whose query tile
+          // does not take the key tile, and only once it has landed (so
+          // neither can give it back twice in a row)
           if (k >= 0) {
             ok = dev::mbar_wait(&vfull[vst], vph, p.err);
-          }
-          if (k + 1 < tl.nt && k < 0) ok = ok && dev::mbar_wait(&kfull[kst], kph, p.err);
-          bool kready = k < 0;
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (!ok) break;
-            if (k >= 0 && act(x, k)) {
-              ok = dev::mbar_wait(&p_full[x], pcount[x] & 1, p.err);
-              ++pcount[x];
-              if (ok && !begun[x] && units[x] > 0) ok = dev::mbar_wait(&o_free[x], (units[x] - 1) & 1, p.err);
+            if (now) {
+              ok = ok && dev::mbar_wait(&p_full[x], pph, p.err);
+              pph ^= 1u;
+              if (!begun && used) ok = ok && dev::mbar_wait(&o_free[x], oph, p.err);
               if (!ok) break;
               dev::tc_fence_after();
+              const uint64_t vb = dv + (uint64_t)(vst * (T::TILE >> 4));
 #pragma unroll
               for (int ks = 0; ks < kKeys / 16; ++ks) {
                 const uint64_t off = T::FP8 ? (uint64_t)(((ks >> 2) * (D * 128) + (ks & 3) * 32) >> 4)
                                             : (uint64_t)((ks * 16 * 128) >> 4);
-                dev::umma_ts(tbase + 2 * kKeys + x * D, tbase + x * kKeys + 8 * ks,
-                             dv + (uint64_t)(vst * (T::TILE >> 4)) + off, idesc_o, (begun[x] || ks > 0) ? 1u : 0u);
+                dev::umma_ts(to, ts + 8 * ks, vb + off, idesc_o, (begun || ks > 0) ? 1u : 0u);
               }
-              begun[x] = true;
-              bool more = false;  // a later tile of this unit for x
-              for (int j = k + 1; j < tl.nt && !more; ++j) more = act(x, j);
-              if (!more) {
-                dev::umma_commit(&o_done[x]);
-                ++units[x];
-              }
+              begun = true;
             }
-            if (k + 1 < tl.nt) {
-              if (!kready) {
-                ok = dev::mbar_wait(&kfull[kst], kph, p.err);
-                kready = true;
-                if (!ok) break;
-              }
-              if (act(x, k + 1)) {
-                dev::tc_fence_after();
-                issue_s(x);
-              }
-            }
-          }
-          if (!ok) break;
-          if (k >= 0) {
+            if (!ok) break;
             dev::umma_commit(&vempty[vst]);
             if (++vst == T::NV) {
               vst = 0;
               vph ^= 1u;
             }
           }
-          if (k + 1 < tl.nt) {
+          if (k + 1 < nt) {
+            ok = dev::mbar_wait(&kfull[kst], kph, p.err);
+            if (!ok) break;
+            if (next) {
+              dev::tc_fence_after();
+              const uint64_t kb = dk + (uint64_t)(kst * (T::TILE >> 4));
+#pragma unroll
+              for (int ks = 0; ks < D / 16; ++ks) {
+                const uint64_t off = (uint64_t)(((ks >> 2) * kTileRow + (ks & 3) * 32) >> 4);
+                dev::umma_ss(ts, dq + off, kb + off, idesc_s, ks > 0 ? 1u : 0u);
+              }
+              dev::umma_commit(&s_full[x]);
+            }
             dev::umma_commit(&kempty[kst]);
             if (++kst == T::NK) {
               kst = 0;
               kph ^= 1u;
             }
           }
-          if (k + 1 == max(0, tl.nt - 1)) dev::umma_commit(q_free);
+          if (k + 1 == max(0, nt - 1)) dev::umma_commit(q_free);
+          now = next;
+        }
+        if (begun) {
+          dev::umma_commit(&o_done[x]);
+          used = true;
+          oph ^= 1u;
         }
       }
       // every MMA issued has completed before TMEM may be freed
@@ -516,13 +527,16 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
     __syncwarp();
   } else if (warp < 8) {
     // ============================ softmax rows =================================
-    if constexpr (T::FP8) reg_inc();
+    reg_inc<T::FP8>();
     const int x = warp >> 2, quarter = warp & 3;
     const int r = 32 * quarter + lane;  // this thread's row of tile x: its TMEM lane
     const uint32_t lane_addr = (uint32_t)(32 * quarter) << 16;
     const uint32_t ts = tbase + x * kKeys + lane_addr, to = tbase + 2 * kKeys + x * D + lane_addr;
     uint8_t* qs = smem + T::Q + x * T::TILE;
     uint32_t scount = 0, ucount = 0;
+    uint64_t poly2[5];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) poly2[i] = dev::f2(p.mod.poly[i], p.mod.poly[i]);
     int gv = 0;  // key tiles before this unit (the V ring's position)
     bool ok = true;
     auto wait_ok = [&](uint64_t* bar, uint32_t parity) {
@@ -538,6 +552,8 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
       const Tiles<BS> tl(u, p);
       const int na = min(u.qn, QB);
       const int px = u.p0 + x * QB, nx = x ? u.qn - na : na;  // this tile's positions
+      int k0, k1, kp;
+      tl.steps(px, nx, k0, k1, kp);
       const bool valid = r < nx * G;
       const int pos = px + r / G;
       const int qh = u.h * G + r % G;
@@ -576,7 +592,7 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
       bool first = true;
       for (int k = 0; k < tl.nt; ++k) {
         const int t = tl.tile(k);
-        if (!tl.active(t, px, nx)) continue;
+        if (!((k >= k0 && k < k1) || k >= kp)) continue;
         wait_ok(&s_full[x], scount & 1);
         ++scount;
         dev::tc_fence_after();
@@ -589,55 +605,82 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
         const bool edge = !__all_sync(0xffffffffu, whole);
         const bool ahead = SLOPES && __any_sync(0xffffffffu, slope != 0.f && pl > pos + 1 - key0);
         const float dist = (float)(pos - key0);
-        // 32 scores of the row's tile -> exponents s - rf in log2 units, every
-        // key of the chunk visible and none past the row's position
-        auto plain_args = [&](int c, float (&a)[32], float rf, float& zmax) {
-          uint32_t w[32];
-          dev::tmem_ld32(ts + 32 * c, w);
-          const float base = SLOPES ? fmaf(-slope, dist - (float)(32 * c), -rf) : -rf;
+        // 32 scores of the row's tile (in w) -> weights over the reference, as
+        // packed pairs; every key of the chunk is visible and none lies past the
+        // row's position.  Arithmetic on pairs: issue slots count.
+        uint64_t sum2 = 0;
+        float zm0 = 0.f, zm1 = 0.f;
+        auto plain_chunk = [&](int c, const uint32_t (&w)[32], uint32_t* out) {
+          const float base = SLOPES ? fmaf(-slope, dist - (float)(32 * c), -ref) : -ref;
+          uint64_t b = SLOPES ? dev::f2(base, base + slope) : dev::f2(base, base);
+          const uint64_t step = dev::f2(2.f * slope, 2.f * slope);
+          const uint64_t in = CAPS ? dev::f2(y_in, y_in) : dev::f2(scale, scale);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float b = SLOPES ? fmaf(slope, (float)i, base) : base;
+          for (int i = 0; i < 16; ++i) {
+            const uint64_t x = dev::f2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+            uint64_t a;
             if constexpr (CAPS) {
-              const float y = __uint_as_float(w[i]) * y_in, z = y * y;
-              zmax = fmaxf(zmax, z);
-              float q = fmaf(z, p.mod.poly[4], p.mod.poly[3]);
-              q = fmaf(z, q, p.mod.poly[2]);
-              q = fmaf(z, q, p.mod.poly[1]);
-              q = fmaf(z, q, p.mod.poly[0]);
-              a[i] = fmaf(y, q, b);
+              const uint64_t y = dev::mul2(x, in), z = dev::mul2(y, y);
+              float z0, z1;
+              dev::f2_split(z, z0, z1);
+              if (i & 1) zm1 = dev::max3(zm1, z0, z1);
+              else zm0 = dev::max3(zm0, z0, z1);
+              uint64_t q = dev::fma2(z, poly2[4], poly2[3]);
+              q = dev::fma2(z, q, poly2[2]);
+              q = dev::fma2(z, q, poly2[1]);
+              q = dev::fma2(z, q, poly2[0]);
+              a = dev::fma2(y, q, b);
             } else {
-              a[i] = fmaf(__uint_as_float(w[i]), scale, b);
+              a = dev::fma2(x, in, b);
             }
+            if (SLOPES) b = dev::add2(b, step);
+            float e0, e1;
+            dev::f2_split(a, e0, e1);
+            e0 = dev::ex2(e0);
+            e1 = dev::ex2(e1);
+            sum2 = dev::add2(sum2, dev::f2(e0, e1));
+            out[i] = T::FP8 ? dev::pack_f16(e0, e1) : dev::pack_bf16(e0, e1);
           }
         };
-        // the same for any tile: masks, keys past the row's position (their
-        // distance has the other sign), and with `exact` the cap's exact form
+        // 32 scores of any tile -> exponents s - rf in log2 units: masks, keys
+        // past the row's position (their distance has the other sign), and with
+        // `exact` the cap's exact form
         auto any_args = [&](int c, float (&a)[32], float rf, bool exact, float& zmax) {
           uint32_t w[32];
           dev::tmem_ld32(ts + 32 * c, w);
+          // the chunk's visible keys, a bit each: [0, pl) and [wlo, hi)
+          auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
+          const uint32_t vis = below(pl - 32 * c) | (below(hi - 32 * c) & ~below(wlo - 32 * c));
+          // what a hidden key holds must not choose the cap's form
+#pragma unroll
+          for (int i = 0; i < 32; ++i) a[i] = (vis & (1u << i)) ? __uint_as_float(w[i]) : 0.f;
+          if constexpr (CAPS) {
+            if (exact) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) a[i] = dev::capped(a[i], cap_in, p.mod.cap_out);
+            } else {
+              float z0 = 0.f, z1 = 0.f;
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const uint64_t y = dev::mul2(dev::f2(a[i], a[i + 1]), dev::f2(y_in, y_in)), z = dev::mul2(y, y);
+                float u0, u1;
+                dev::f2_split(z, u0, u1);
+                if (i & 2) z1 = dev::max3(z1, u0, u1);
+                else z0 = dev::max3(z0, u0, u1);
+                uint64_t q = dev::fma2(z, poly2[4], poly2[3]);
+                q = dev::fma2(z, q, poly2[2]);
+                q = dev::fma2(z, q, poly2[1]);
+                q = dev::fma2(z, q, poly2[0]);
+                dev::f2_split(dev::mul2(y, q), a[i], a[i + 1]);
+              }
+              zmax = dev::max3(zmax, z0, z1);
+            }
+          }
+          const float mul = CAPS ? 1.f : scale;
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const int key = 32 * c + i;
-            const bool see = key < pl || (key < hi && key >= wlo);
-            const float d = dist - (float)key;
-            float x = see ? __uint_as_float(w[i]) : 0.f;  // what a hidden key holds must not choose the cap's form
-            if constexpr (CAPS) {
-              if (exact) {
-                x = dev::capped(x, cap_in, p.mod.cap_out);
-              } else {
-                const float y = x * y_in, z = y * y;
-                zmax = fmaxf(zmax, z);
-                float q = fmaf(z, p.mod.poly[4], p.mod.poly[3]);
-                q = fmaf(z, q, p.mod.poly[2]);
-                q = fmaf(z, q, p.mod.poly[1]);
-                x = y * fmaf(z, q, p.mod.poly[0]);
-              }
-            } else {
-              x *= scale;
-            }
-            if (SLOPES) x = fmaf(-slope, fabsf(d), x);
-            a[i] = see ? x - rf : -INFINITY;
+            const float off = SLOPES ? fmaf(-slope, fabsf(dist - (float)(32 * c + i)), -rf) : -rf;
+            a[i] = (vis & (1u << i)) ? fmaf(a[i], mul, off) : -INFINITY;
           }
         };
         auto chunk_sum = [&](const float (&a)[32], uint32_t* out) {
@@ -651,19 +694,21 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
           return (s4[0] + s4[1]) + (s4[2] + s4[3]);
         };
         bool slow = first || edge || ahead;
-        float zmax = 0.f;
         if (!slow) {
           // weights over the reference in hand, kept in registers until they
           // are known to be in range (S is needed again if not)
-          uint32_t pk[kKeys / 2];
-          float sum = 0.f;
+          uint32_t pk[kKeys / 2], w[2][32];
+          dev::tmem_ld32_start(ts, w[0]);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            float a[32];
-            plain_args(c, a, ref, zmax);
-            sum += chunk_sum(a, pk + 16 * c);
+            dev::tmem_wait32(w[c & 1]);
+            if (c < 3) dev::tmem_ld32_start(ts + 32 * (c + 1), w[(c + 1) & 1]);
+            plain_chunk(c, w[c & 1], pk + 16 * c);
           }
-          slow = __any_sync(0xffffffffu, !(sum <= T::BIG) || (CAPS && !(zmax <= kCapFast * kCapFast)));
+          float s0, s1;
+          dev::f2_split(sum2, s0, s1);
+          const float sum = s0 + s1;
+          slow = __any_sync(0xffffffffu, !(sum <= T::BIG) || (CAPS && !(fmaxf(zm0, zm1) <= kCapFast * kCapFast)));
           if (!slow) {
             lsum += sum;
             dev::tmem_st64(ts, pk);
@@ -672,7 +717,7 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
         if (slow) {
           // the row max first, then the weights, chunk by chunk over S
           bool exact = false;
-          float m;
+          float m, zmax;
           for (;;) {
             m = -INFINITY;
             zmax = 0.f;
@@ -714,10 +759,10 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
         first = false;
         if constexpr (!T::FP8) {
           // V rows that no row of the unit sees may hold anything (0 * NaN):
-          // zeroed by the first tile of the unit that uses them
-          const bool mine = x == 0 || !tl.active(t, u.p0, na);
+          // each query tile zeroes them before its own PV (neither waits for
+          // the other's)
           auto zero_v = [&](int z0, int z1) {
-            if (z0 >= z1 || !mine) return;
+            if (z0 >= z1) return;
             const int gg = gv + k;
             wait_ok(&vfull[gg % T::NV], (uint32_t)((gg / T::NV) & 1));
             uint8_t* vt = smem + T::V + (gg % T::NV) * T::TILE;
@@ -770,7 +815,7 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
   } else if (T::FP8 && warp >= kConvWarp) {
     // ==================== e4m3 -> f16 tiles ====================================
     if constexpr (T::FP8) {
-      reg_dec();
+      reg_dec<true>();
       const int ct = tid - 32 * kConvWarp;  // 0..127
       bool ok = true;
       int g = 0;   // tiles of K (and of V) converted
@@ -870,8 +915,6 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
         }
       }
     }
-  } else {
-    if constexpr (T::FP8) reg_dec();  // the idle warp of the loaders' warpgroup
   }
 
   // ---- free TMEM once every warp is past its last tcgen05 access ----
