@@ -41,6 +41,7 @@ namespace {
 
 constexpr int kRows = 128;   // rows of a query tile: the MMA's M
 constexpr int kKeys = 128;   // keys of a K/V tile
+constexpr int kHalf = 64;    // keys of a step: half a tile
 constexpr int kTileRow = 128 * 128;  // bytes of a 64-element-wide chunk of a 128-row tile
 constexpr int kUQ = 4;       // unit queue entries
 constexpr int kGroup = 64;   // sequences of a group in the unit search
@@ -71,7 +72,7 @@ struct C {
   static constexpr float BIG = FP8 ? 16384.f : 18446744073709551616.f;
   // shared memory
   static constexpr int Q = 0, K = 2 * TILE, V = K + NK * TILE, R = V + NV * TILE, BARS = R + NR * RAW;
-  static constexpr int NBARS = 2 * NK + 2 * NV + 2 * NR + 8 + 4 + 2 * kUQ;
+  static constexpr int NBARS = 2 * NK + 2 * NV + 2 * NR + 14 + 4 + 2 * kUQ;
   static constexpr int UQ = BARS + NBARS * 8, TSLOT = UQ + kUQ * 32, GROUPS = TSLOT + 16;
   static constexpr int TOTAL = GROUPS + (kMaxGroups + 1) * 4 + 1024;
   static_assert(TOTAL <= kSmemOptIn, "shared memory");
@@ -108,21 +109,23 @@ struct Tiles {
     const int t = nt - 1 - k;
     return t < npt ? t : t + gap;
   }
-  // the steps k at which rows at positions [a, a + n) see a key of the tile
-  // visited: k0 <= k < k1, or k >= kp
-  __device__ __forceinline__ void steps(int a, int n, int& k0, int& k1, int& kp) const {
-    k0 = k1 = nt;
-    kp = nt;
-    if (n <= 0) return;
-    kp = nt - min(npt, nt);
-    const int first = window > 0 ? max(0, a - window + 1) : 0;
-    // tiles [first / kKeys, ceil((a + n) / kKeys)) past the prefix: tile t is step nt - 1 - (t - gap)
-    const int t0 = max(first / kKeys, npt + gap), t1 = min((max(a + n, 0) + kKeys - 1) / kKeys, nt + gap);
-    if (t1 > t0) {
-      k0 = nt + gap - t1;
-      k1 = nt + gap - t0;
-    }
+  // Half tiles, 64 keys each, in the order of the visits: step j is half 1 - j
+  // % 2 of tile(j / 2).  first() is step 0's half (64-key index), next() the one after.
+  __device__ __forceinline__ int first_half() const { return nt > 0 ? 2 * tile(0) + 1 : 0; }
+  __device__ __forceinline__ int next_half(int h) const {
+    return gap > 0 && h == 2 * (npt + gap) ? 2 * npt - 1 : h - 1;
   }
+};
+// Whether rows at positions [a, a + n) see a key of half h.
+struct Seen {
+  int hp, f, e;
+  template <int BS>
+  __device__ __forceinline__ Seen(const Tiles<BS>& t, int a, int n) {
+    hp = n > 0 ? (t.pfx + kHalf - 1) / kHalf : 0;
+    f = (t.window > 0 ? max(0, a - t.window + 1) : 0) / kHalf;
+    e = n > 0 ? (max(a + n, 0) + kHalf - 1) / kHalf : 0;
+  }
+  __device__ __forceinline__ bool operator()(int h) const { return h < hp || (h >= f && h < e); }
 };
 
 // Registers move from the loaders', the MMA's and the converters' warpgroups
@@ -153,10 +156,11 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
   uint64_t* vempty = vfull + T::NV;
   uint64_t* rfull = vempty + T::NV;
   uint64_t* rempty = rfull + T::NR;
-  uint64_t* s_full = rempty + T::NR;  // [2] S of a tile is complete (and the tile's earlier PV)
-  uint64_t* p_full = s_full + 2;      // [2] P is written
-  uint64_t* o_done = p_full + 2;      // [2] a unit's last PV is complete
-  uint64_t* o_free = o_done + 2;      // [2] O has been read out
+  // per query tile x and S buffer b, at 2 x + b
+  uint64_t* s_full = rempty + T::NR;  // [4] S is complete
+  uint64_t* p_full = s_full + 4;      // [4] P is written
+  uint64_t* pv_done = p_full + 4;     // [4] its PV is complete
+  uint64_t* o_free = pv_done + 4;     // [2] a unit's O has been read out
   uint64_t* q_full = o_free + 2;      // the Q tiles are in place
   uint64_t* q_raw = q_full + 1;       // e4m3: ... as bf16, before their conversion
   uint64_t* q_free = q_raw + 1;       // the unit's last S MMA is complete
@@ -196,12 +200,12 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
       dev::mbar_init(&rfull[i], 1);
       dev::mbar_init(&rempty[i], 4);
     }
-    for (int x = 0; x < 2; ++x) {
-      dev::mbar_init(&s_full[x], 1);
-      dev::mbar_init(&p_full[x], 4);
-      dev::mbar_init(&o_done[x], 1);
-      dev::mbar_init(&o_free[x], 4);
+    for (int i = 0; i < 4; ++i) {
+      dev::mbar_init(&s_full[i], 1);
+      dev::mbar_init(&p_full[i], 4);
+      dev::mbar_init(&pv_done[i], 1);
     }
+    for (int x = 0; x < 2; ++x) dev::mbar_init(&o_free[x], 4);
     dev::mbar_init(q_full, T::FP8 ? 8 : 1);
     dev::mbar_init(q_raw, 1);
     dev::mbar_init(q_free, 2);
@@ -259,7 +263,7 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
   // queue entry n, as one warp's (or thread's) copy; ok false: none
   auto read_unit = [&](int n, Unit& u, bool& ok) {
     const int slot = n % kUQ;
-    if (ok) ok = dev::mbar_wait(&uq_full[slot], (uint32_t)((n / kUQ) & 1), p.err);
+    if (ok) ok = dev::mbar_wait_clk(&uq_full[slot], (uint32_t)((n / kUQ) & 1), p.err);
     if (ok) u = uq[slot];
     else u.s = -1;
   };
@@ -324,7 +328,7 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
         }
         const int slot = n % kUQ;
         if (n >= kUQ && ok)
-          ok = __all_sync(0xffffffffu, dev::mbar_wait(&uq_empty[slot], (uint32_t)(((n / kUQ) - 1) & 1), p.err));
+          ok = __all_sync(0xffffffffu, dev::mbar_wait_clk(&uq_empty[slot], (uint32_t)(((n / kUQ) - 1) & 1), p.err));
         if (!ok) u.s = -1;
         if (lane == 0) {
           uq[slot] = u;
@@ -343,7 +347,7 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
         // the unit's queries, once the previous unit's S MMAs are done with
         // them: two boxes of 128 / G positions (rows past the unit are other
         // rows or zeros: computed, not kept)
-        if (n > 0 && ok) ok = __all_sync(0xffffffffu, dev::mbar_wait(q_free, (uint32_t)((n - 1) & 1), p.err));
+        if (n > 0 && ok) ok = __all_sync(0xffffffffu, dev::mbar_wait_clk(q_free, (uint32_t)((n - 1) & 1), p.err));
         if (!ok) continue;
         if (lane == 0) {
           uint64_t* bar = T::FP8 ? q_raw : q_full;
@@ -381,7 +385,7 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
         const bool mine = lane < T::NCH * T::BPT;
         int32_t next = mine ? entry(0, j) : -2;
         for (int k = 0; k < tl.nt && ok; ++k, ++g) {
-          if (g >= nst) ok = __all_sync(0xffffffffu, dev::mbar_wait(&emptyb[st], ph ^ 1u, p.err));
+          if (g >= nst) ok = __all_sync(0xffffffffu, dev::mbar_wait_clk(&emptyb[st], ph ^ 1u, p.err));
           if (!ok) break;
           const int32_t blk = next;
           if (mine) next = entry(k + 1, j);
@@ -406,7 +410,7 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
           if (mine) blk = checked(blk);
           const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(0xffffffffu, mine)) * BS * D);
           for (int side = 0; side < 2 && ok; ++side, ++g) {
-            if (g >= T::NR) ok = __all_sync(0xffffffffu, dev::mbar_wait(&rempty[st], ph ^ 1u, p.err));
+            if (g >= T::NR) ok = __all_sync(0xffffffffu, dev::mbar_wait_clk(&rempty[st], ph ^ 1u, p.err));
             if (!ok) break;
             if (lane == 0) dev::mbar_arrive_expect_tx(&rfull[st], bytes);
             __syncwarp();
@@ -427,8 +431,8 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
       uint64_t* fullb = T::FP8 ? rfull : is_v ? vfull : kfull;
       const int nst = T::FP8 ? T::NR : is_v ? T::NV : T::NK;
       for (int d = max(0, g - nst); d < g; ++d)
-        dev::mbar_wait(&fullb[d % nst], (uint32_t)((d / nst) & 1), nullptr, 100000000ull);
-      if (qlast >= 0) dev::mbar_wait(T::FP8 ? q_raw : q_full, (uint32_t)(qlast & 1), nullptr, 100000000ull);
+        dev::mbar_wait_clk(&fullb[d % nst], (uint32_t)((d / nst) & 1), nullptr, 1ll << 28);
+      if (qlast >= 0) dev::mbar_wait_clk(T::FP8 ? q_raw : q_full, (uint32_t)(qlast & 1), nullptr, 1ll << 28);
     }
     __syncwarp();
   } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
@@ -436,18 +440,19 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
     reg_dec<T::FP8>();
     if (lane == 0) {
       const int x = warp - kMmaWarp;
-      const uint32_t idesc_s = T::FP8 ? dev::umma_idesc_f16(kKeys, false) : dev::umma_idesc_bf16(kKeys, false);
+      const uint32_t idesc_s = T::FP8 ? dev::umma_idesc_f16(kHalf, false) : dev::umma_idesc_bf16(kHalf, false);
       const uint32_t idesc_o = T::FP8 ? dev::umma_idesc_f16(D, false) : dev::umma_idesc_bf16(D, true);
       const uint64_t dq = dev::umma_desc_sw128(dev::smem_u32(smem + T::Q + x * T::TILE), 16, 1024);
       const uint64_t dk = dev::umma_desc_sw128(dev::smem_u32(smem + T::K), 16, 1024);
       // V: bf16 MN-major (d contiguous, 64-wide chunks kTileRow apart); e4m3's
       // converted tile K-major (keys contiguous, 64-key chunks of D rows)
       const uint64_t dv = dev::umma_desc_sw128(dev::smem_u32(smem + T::V), T::FP8 ? 16 : kTileRow, 1024);
-      const uint32_t ts = tbase + x * kKeys, to = tbase + 2 * kKeys + x * D;
+      const uint32_t ts = tbase + x * 2 * kHalf, to = tbase + 4 * kHalf + x * D;
       // ring positions and barrier phases by counters: every instruction here
       // delays the tensor core's next tile
       int kst = 0, vst = 0;
-      uint32_t kph = 0, vph = 0, pph = 0, oph = 1;
+      uint32_t kph = 0, vph = 0, oph = 1;
+      uint32_t cs = 0, cp = 0;  // S's and PV's issued
       bool ok = true, used = false;
       for (int n = 0;; ++n) {
         Unit u;
@@ -456,73 +461,81 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
         if (u.s < 0) break;
         const Tiles<BS> tl(u, p);
         const int na = min(u.qn, QB);  // positions of tile A; B has the rest
-        int k0, k1, kp;
-        tl.steps(u.p0 + x * QB, x ? u.qn - na : na, k0, k1, kp);
-        ok = ok && dev::mbar_wait(q_full, (uint32_t)(n & 1), p.err);
-        const int nt = tl.nt;
+        const Seen seen(tl, u.p0 + x * QB, x ? u.qn - na : na);
+        ok = ok && dev::mbar_wait_clk(q_full, (uint32_t)(n & 1), p.err);
+        const int steps = 2 * tl.nt;
         bool begun = false;
-        // step k: the PV of tile k and the S of tile k + 1
-        bool now = false;  // this query tile takes key tile k
-        for (int k = -1; k < nt && ok; ++k) {
-          const bool next = k + 1 < nt && ((k + 1 >= k0 && k + 1 < k1) || k + 1 >= kp);
-          // a stage is given back by both threads, also by one whose query tile
-          // does not take the key tile, and only once it has landed (so
-          // neither can give it back twice in a row)
-          if (k >= 0) {
-            ok = dev::mbar_wait(&vfull[vst], vph, p.err);
-            if (now) {
-              ok = ok && dev::mbar_wait(&p_full[x], pph, p.err);
-              pph ^= 1u;
-              if (!begun && used) ok = ok && dev::mbar_wait(&o_free[x], oph, p.err);
+        if (steps == 0) dev::umma_commit(q_free);
+        int hs = tl.first_half(), hv = hs;  // the halves of the next S and the next PV
+        // step j: the PV of half j and the S of half j + 2, into the buffer
+        // that this PV (or an earlier one) has read.  A stage is given back by
+        // both threads, also by one whose query tile does not take it, and
+        // only once it has landed (so neither can give it back twice in a row)
+        for (int j = -2; j < steps && ok; ++j) {
+          if (j >= 0) {
+            const int hf = 1 - (j & 1);
+            if (hf) ok = dev::mbar_wait_clk(&vfull[vst], vph, p.err);
+            if (ok && seen(hv)) {
+              const uint32_t b = cp & 1;
+              ok = dev::mbar_wait_clk(&p_full[2 * x + b], (cp >> 1) & 1, p.err);
+              if (!begun && used) ok = ok && dev::mbar_wait_clk(&o_free[x], oph, p.err);
               if (!ok) break;
               dev::tc_fence_after();
-              const uint64_t vb = dv + (uint64_t)(vst * (T::TILE >> 4));
+              const uint64_t vb = dv + (uint64_t)(vst * (T::TILE >> 4)) +
+                                  (uint64_t)((T::FP8 ? hf * (D * 128) : hf * 4 * 16 * 128) >> 4);
 #pragma unroll
-              for (int ks = 0; ks < kKeys / 16; ++ks) {
-                const uint64_t off = T::FP8 ? (uint64_t)(((ks >> 2) * (D * 128) + (ks & 3) * 32) >> 4)
-                                            : (uint64_t)((ks * 16 * 128) >> 4);
-                dev::umma_ts(to, ts + 8 * ks, vb + off, idesc_o, (begun || ks > 0) ? 1u : 0u);
-              }
+              for (int ks = 0; ks < kHalf / 16; ++ks)
+                dev::umma_ts(to, ts + b * kHalf + 8 * ks, vb + (uint64_t)((T::FP8 ? ks * 32 : ks * 16 * 128) >> 4),
+                             idesc_o, (begun || ks > 0) ? 1u : 0u);
+              dev::umma_commit(&pv_done[2 * x + b]);
               begun = true;
+              ++cp;
             }
             if (!ok) break;
-            dev::umma_commit(&vempty[vst]);
-            if (++vst == T::NV) {
-              vst = 0;
-              vph ^= 1u;
+            hv = tl.next_half(hv);
+            if (!hf) {
+              dev::umma_commit(&vempty[vst]);
+              if (++vst == T::NV) {
+                vst = 0;
+                vph ^= 1u;
+              }
             }
           }
-          if (k + 1 < nt) {
-            ok = dev::mbar_wait(&kfull[kst], kph, p.err);
+          if (j + 2 < steps) {
+            const int hf = 1 - (j & 1);
+            if (hf) ok = dev::mbar_wait_clk(&kfull[kst], kph, p.err);
             if (!ok) break;
-            if (next) {
+            if (seen(hs)) {
+              const uint32_t b = cs & 1;
               dev::tc_fence_after();
-              const uint64_t kb = dk + (uint64_t)(kst * (T::TILE >> 4));
+              const uint64_t kb = dk + (uint64_t)(kst * (T::TILE >> 4)) + (uint64_t)((hf * kHalf * 128) >> 4);
 #pragma unroll
               for (int ks = 0; ks < D / 16; ++ks) {
                 const uint64_t off = (uint64_t)(((ks >> 2) * kTileRow + (ks & 3) * 32) >> 4);
-                dev::umma_ss(ts, dq + off, kb + off, idesc_s, ks > 0 ? 1u : 0u);
+                dev::umma_ss(ts + b * kHalf, dq + off, kb + off, idesc_s, ks > 0 ? 1u : 0u);
               }
-              dev::umma_commit(&s_full[x]);
+              dev::umma_commit(&s_full[2 * x + b]);
+              ++cs;
             }
-            dev::umma_commit(&kempty[kst]);
-            if (++kst == T::NK) {
-              kst = 0;
-              kph ^= 1u;
+            hs = tl.next_half(hs);
+            if (!hf) {
+              dev::umma_commit(&kempty[kst]);
+              if (++kst == T::NK) {
+                kst = 0;
+                kph ^= 1u;
+              }
             }
+            if (j + 3 == steps) dev::umma_commit(q_free);
           }
-          if (k + 1 == max(0, nt - 1)) dev::umma_commit(q_free);
-          now = next;
         }
         if (begun) {
-          dev::umma_commit(&o_done[x]);
           used = true;
           oph ^= 1u;
         }
       }
       // every MMA issued has completed before TMEM may be freed
       dev::umma_commit(done);
-      dev::mbar_wait(done, 0, nullptr, 100000000ull);
+      dev::mbar_wait_clk(done, 0, nullptr, 1ll << 28);
     }
     __syncwarp();
   } else if (warp < 8) {
@@ -531,16 +544,16 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
     const int x = warp >> 2, quarter = warp & 3;
     const int r = 32 * quarter + lane;  // this thread's row of tile x: its TMEM lane
     const uint32_t lane_addr = (uint32_t)(32 * quarter) << 16;
-    const uint32_t ts = tbase + x * kKeys + lane_addr, to = tbase + 2 * kKeys + x * D + lane_addr;
+    const uint32_t ts0 = tbase + x * 2 * kHalf + lane_addr, to = tbase + 4 * kHalf + x * D + lane_addr;
     uint8_t* qs = smem + T::Q + x * T::TILE;
-    uint32_t scount = 0, ucount = 0;
+    uint32_t sc = 0;  // half tiles done
     uint64_t poly2[5];
 #pragma unroll
     for (int i = 0; i < 5; ++i) poly2[i] = dev::f2(p.mod.poly[i], p.mod.poly[i]);
     int gv = 0;  // key tiles before this unit (the V ring's position)
     bool ok = true;
     auto wait_ok = [&](uint64_t* bar, uint32_t parity) {
-      if (ok) ok = __all_sync(0xffffffffu, dev::mbar_wait(bar, parity, p.err));
+      if (ok) ok = __all_sync(0xffffffffu, dev::mbar_wait_clk(bar, parity, p.err));
     };
     for (int n = 0;; ++n) {
       Unit u;
@@ -552,8 +565,7 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
       const Tiles<BS> tl(u, p);
       const int na = min(u.qn, QB);
       const int px = u.p0 + x * QB, nx = x ? u.qn - na : na;  // this tile's positions
-      int k0, k1, kp;
-      tl.steps(px, nx, k0, k1, kp);
+      const Seen seen(tl, px, nx);
       const bool valid = r < nx * G;
       const int pos = px + r / G;
       const int qh = u.h * G + r % G;
@@ -590,18 +602,18 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
       const float y_in = valid ? cap_in * (0.5f / 1.4426950408889634f) : 0.f;
       float ref = -1e30f, lsum = 0.f;
       bool first = true;
-      for (int k = 0; k < tl.nt; ++k) {
-        const int t = tl.tile(k);
-        if (!((k >= k0 && k < k1) || k >= kp)) continue;
-        wait_ok(&s_full[x], scount & 1);
-        ++scount;
+      int h = tl.first_half();
+      for (int j = 0; j < 2 * tl.nt; ++j, h = tl.next_half(h)) {
+        if (!seen(h)) continue;
+        const uint32_t b = sc & 1, ts = ts0 + b * kHalf;
+        wait_ok(&s_full[2 * x + b], (sc >> 1) & 1);
         dev::tc_fence_after();
-        const int key0 = t * kKeys;
-        // the row sees keys [wlo, hi) and [0, pl) of the tile
+        const int key0 = h * kHalf;
+        // the row sees keys [wlo, hi) and [0, pl) of the half tile
         const int hi = valid ? min(pos + 1, u.len) - key0 : 0;
         const int wlo = tl.window > 0 ? pos - tl.window + 1 - key0 : 0;
         const int pl = valid ? u.pfx - key0 : 0;
-        const bool whole = (hi >= kKeys && wlo <= 0) || pl >= kKeys;
+        const bool whole = (hi >= kHalf && wlo <= 0) || pl >= kHalf;
         const bool edge = !__all_sync(0xffffffffu, whole);
         const bool ahead = SLOPES && __any_sync(0xffffffffu, slope != 0.f && pl > pos + 1 - key0);
         const float dist = (float)(pos - key0);
@@ -697,12 +709,12 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
         if (!slow) {
           // weights over the reference in hand, kept in registers until they
           // are known to be in range (S is needed again if not)
-          uint32_t pk[kKeys / 2], w[2][32];
+          uint32_t pk[kHalf / 2], w[2][32];
           dev::tmem_ld32_start(ts, w[0]);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < 2; ++c) {
             dev::tmem_wait32(w[c & 1]);
-            if (c < 3) dev::tmem_ld32_start(ts + 32 * (c + 1), w[(c + 1) & 1]);
+            if (c < 1) dev::tmem_ld32_start(ts + 32 * (c + 1), w[(c + 1) & 1]);
             plain_chunk(c, w[c & 1], pk + 16 * c);
           }
           float s0, s1;
@@ -711,7 +723,7 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
           slow = __any_sync(0xffffffffu, !(sum <= T::BIG) || (CAPS && !(fmaxf(zm0, zm1) <= kCapFast * kCapFast)));
           if (!slow) {
             lsum += sum;
-            dev::tmem_st64(ts, pk);
+            dev::tmem_st32(ts, pk);
           }
         }
         if (slow) {
@@ -722,7 +734,7 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
             m = -INFINITY;
             zmax = 0.f;
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < 2; ++c) {
               float a[32];
               any_args(c, a, 0.f, exact, zmax);
 #pragma unroll
@@ -731,13 +743,15 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
             if (!CAPS || exact || !__any_sync(0xffffffffu, !(zmax <= kCapFast * kCapFast))) break;
             exact = true;
           }
-          // the reference moves where the weights would grow past 2^8.  O is
-          // at rest: this tile's S was issued behind the previous PV
+          // the reference moves where the weights would grow past 2^8; O is
+          // rescaled once the previous PV is complete
           const bool move = m > ref + 8.f;
           const float alpha = move ? dev::ex2(ref - m) : 1.f;
           if (move) ref = m;
           lsum *= alpha;
           if (!first && __any_sync(0xffffffffu, move)) {
+            wait_ok(&pv_done[2 * x + (b ^ 1)], ((sc - 1) >> 1) & 1);
+            dev::tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               uint32_t w[32];
@@ -748,7 +762,7 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
             }
           }
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < 2; ++c) {
             float a[32];
             any_args(c, a, ref, exact, zmax);
             uint32_t pk[16];
@@ -763,9 +777,9 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
           // the other's)
           auto zero_v = [&](int z0, int z1) {
             if (z0 >= z1) return;
-            const int gg = gv + k;
+            const int gg = gv + (j >> 1);
             wait_ok(&vfull[gg % T::NV], (uint32_t)((gg / T::NV) & 1));
-            uint8_t* vt = smem + T::V + (gg % T::NV) * T::TILE;
+            uint8_t* vt = smem + T::V + (gg % T::NV) * T::TILE + (1 - (j & 1)) * kHalf * 128;
             for (int i = tid & 127; i < (z1 - z0) * T::NCH * 8; i += 128) {
               const int key = z0 + i / (T::NCH * 8), rest = i % (T::NCH * 8);
               *reinterpret_cast<uint4*>(vt + (rest >> 3) * kTileRow + key * 128 + (rest & 7) * 16) =
@@ -773,20 +787,20 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           };
-          zero_v(max(0, max(u.len, u.pfx) - key0), min(kKeys, tl.nb * BS - key0));
-          zero_v(max(u.pfx, key0) - key0, min(tl.lo, key0 + kKeys) - key0);
+          zero_v(max(0, max(u.len, u.pfx) - key0), min(kHalf, tl.nb * BS - key0));
+          zero_v(max(u.pfx, key0) - key0, min(tl.lo, key0 + kHalf) - key0);
         }
         dev::tc_fence_before();
         __syncwarp();
-        if (lane == 0) dev::mbar_arrive(&p_full[x]);
+        if (lane == 0) dev::mbar_arrive(&p_full[2 * x + b]);
+        ++sc;
       }
       gv += tl.nt;
       // ---- O / sum -> the output row; then O is free ----
       const int64_t at = ((int64_t)(u.row0 + x * QB + r / G) * hq + qh) * D;
       uint4* dst = reinterpret_cast<uint4*>(p.out + at * 2);
       if (!first) {
-        wait_ok(&o_done[x], ucount & 1);
-        ++ucount;
+        wait_ok(&pv_done[2 * x + ((sc - 1) & 1)], ((sc - 1) >> 1) & 1);
         dev::tc_fence_after();
         const float inv = lsum > 0.f ? osc / lsum : (lsum == 0.f ? 0.f : lsum);  // nothing visible: 0; NaN stays
 #pragma unroll
@@ -822,7 +836,7 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
       int rst = 0;
       uint32_t rph = 0;
       auto wait_ok = [&](uint64_t* bar, uint32_t parity) {
-        if (ok) ok = __all_sync(0xffffffffu, dev::mbar_wait(bar, parity, p.err));
+        if (ok) ok = __all_sync(0xffffffffu, dev::mbar_wait_clk(bar, parity, p.err));
       };
       auto to_f16 = [&](const uint4& b, uint4& lo, uint4& hi) {
         dev::e4m3x4_to_f16x2(b.x, lo.x, lo.y);

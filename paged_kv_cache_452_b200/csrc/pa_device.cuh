@@ -62,6 +62,21 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int32_
   return true;
 }
 
+// The same bound by the SM's own clock, which is cheap to read: a wait that
+// ends just after its first try then ends at once (2^32 clocks: over 2 s).
+__device__ __forceinline__ bool mbar_wait_clk(uint64_t* bar, uint32_t parity, int32_t* err,
+                                              long long limit = 1ll << 32) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (clock64() - t0 > limit) {
+      if (err) atomicCAS(err, 0, 1);
+      return false;
+    }
+  }
+  return true;
+}
+
 // ---- TMA / bulk copies --------------------------------------------------------
 __device__ __forceinline__ void prefetch_tmap(const CUtensorMap* m) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
