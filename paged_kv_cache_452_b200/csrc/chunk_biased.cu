@@ -438,8 +438,14 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
   } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
     // ==================== MMA issue: one thread per query tile ====================
     reg_dec<T::FP8>();
-    if (lane == 0) {
-      const int x = warp - kMmaWarp;
+    {
+      // the whole warp runs this loop, converged; lane 0 issues
+      auto uni = [](auto v) { return __shfl_sync(0xffffffffu, v, 0); };
+      const uint32_t on = lane == 0;
+      const int x = uni(warp) - kMmaWarp;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return (bool)__all_sync(0xffffffffu, dev::mbar_wait_clk(bar, parity, p.err));
+      };
       const uint32_t idesc_s = T::FP8 ? dev::umma_idesc_f16(kHalf, false) : dev::umma_idesc_bf16(kHalf, false);
       const uint32_t idesc_o = T::FP8 ? dev::umma_idesc_f16(D, false) : dev::umma_idesc_bf16(D, true);
       const uint64_t dq = dev::umma_desc_sw128(dev::smem_u32(smem + T::Q + x * T::TILE), 16, 1024);
@@ -447,7 +453,7 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
       // V: bf16 MN-major (d contiguous, 64-wide chunks kTileRow apart); e4m3's
       // converted tile K-major (keys contiguous, 64-key chunks of D rows)
       const uint64_t dv = dev::umma_desc_sw128(dev::smem_u32(smem + T::V), T::FP8 ? 16 : kTileRow, 1024);
-      const uint32_t ts = tbase + x * 2 * kHalf, to = tbase + 4 * kHalf + x * D;
+      const uint32_t tb = uni(tbase), ts = tb + x * 2 * kHalf, to = tb + 4 * kHalf + x * D;
       // ring positions and barrier phases by counters: every instruction here
       // delays the tensor core's next tile
       int kst = 0, vst = 0;
@@ -457,15 +463,22 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
       for (int n = 0;; ++n) {
         Unit u;
         read_unit(n, u, ok);
-        dev::mbar_arrive(&uq_empty[n % kUQ]);
+        u.s = uni(u.s);
+        ok = ok && u.s >= 0;
+        u.p0 = uni(u.p0);
+        u.qn = uni(u.qn);
+        u.len = uni(u.len);
+        u.pfx = uni(u.pfx);
+        __syncwarp();
+        if (on) dev::mbar_arrive(&uq_empty[n % kUQ]);
         if (u.s < 0) break;
         const Tiles<BS> tl(u, p);
         const int na = min(u.qn, QB);  // positions of tile A; B has the rest
         const Seen seen(tl, u.p0 + x * QB, x ? u.qn - na : na);
-        ok = ok && dev::mbar_wait_clk(q_full, (uint32_t)(n & 1), p.err);
+        ok = ok && wait(q_full, (uint32_t)(n & 1));
         const int steps = 2 * tl.nt;
         bool begun = false;
-        if (steps == 0) dev::umma_commit(q_free);
+        if (steps == 0) dev::umma_commit_if(on, q_free);
         int hs = tl.first_half(), hv = hs;  // the halves of the next S and the next PV
         // step j: the PV of half j and the S of half j + 2, into the buffer
         // that this PV (or an earlier one) has read.  A stage is given back by
@@ -474,27 +487,27 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
         for (int j = -2; j < steps && ok; ++j) {
           if (j >= 0) {
             const int hf = 1 - (j & 1);
-            if (hf) ok = dev::mbar_wait_clk(&vfull[vst], vph, p.err);
+            if (hf) ok = wait(&vfull[vst], vph);
             if (ok && seen(hv)) {
               const uint32_t b = cp & 1;
-              ok = dev::mbar_wait_clk(&p_full[2 * x + b], (cp >> 1) & 1, p.err);
-              if (!begun && used) ok = ok && dev::mbar_wait_clk(&o_free[x], oph, p.err);
+              ok = wait(&p_full[2 * x + b], (cp >> 1) & 1);
+              if (!begun && used) ok = ok && wait(&o_free[x], oph);
               if (!ok) break;
               dev::tc_fence_after();
               const uint64_t vb = dv + (uint64_t)(vst * (T::TILE >> 4)) +
                                   (uint64_t)((T::FP8 ? hf * (D * 128) : hf * 4 * 16 * 128) >> 4);
 #pragma unroll
               for (int ks = 0; ks < kHalf / 16; ++ks)
-                dev::umma_ts(to, ts + b * kHalf + 8 * ks, vb + (uint64_t)((T::FP8 ? ks * 32 : ks * 16 * 128) >> 4),
+                dev::umma_ts_if(on, to, ts + b * kHalf + 8 * ks, vb + (uint64_t)((T::FP8 ? ks * 32 : ks * 16 * 128) >> 4),
                              idesc_o, (begun || ks > 0) ? 1u : 0u);
-              dev::umma_commit(&pv_done[2 * x + b]);
+              dev::umma_commit_if(on, &pv_done[2 * x + b]);
               begun = true;
               ++cp;
             }
             if (!ok) break;
             hv = tl.next_half(hv);
             if (!hf) {
-              dev::umma_commit(&vempty[vst]);
+              dev::umma_commit_if(on, &vempty[vst]);
               if (++vst == T::NV) {
                 vst = 0;
                 vph ^= 1u;
@@ -503,7 +516,7 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
           }
           if (j + 2 < steps) {
             const int hf = 1 - (j & 1);
-            if (hf) ok = dev::mbar_wait_clk(&kfull[kst], kph, p.err);
+            if (hf) ok = wait(&kfull[kst], kph);
             if (!ok) break;
             if (seen(hs)) {
               const uint32_t b = cs & 1;
@@ -512,20 +525,20 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
 #pragma unroll
               for (int ks = 0; ks < D / 16; ++ks) {
                 const uint64_t off = (uint64_t)(((ks >> 2) * kTileRow + (ks & 3) * 32) >> 4);
-                dev::umma_ss(ts + b * kHalf, dq + off, kb + off, idesc_s, ks > 0 ? 1u : 0u);
+                dev::umma_ss_if(on, ts + b * kHalf, dq + off, kb + off, idesc_s, ks > 0 ? 1u : 0u);
               }
-              dev::umma_commit(&s_full[2 * x + b]);
+              dev::umma_commit_if(on, &s_full[2 * x + b]);
               ++cs;
             }
             hs = tl.next_half(hs);
             if (!hf) {
-              dev::umma_commit(&kempty[kst]);
+              dev::umma_commit_if(on, &kempty[kst]);
               if (++kst == T::NK) {
                 kst = 0;
                 kph ^= 1u;
               }
             }
-            if (j + 3 == steps) dev::umma_commit(q_free);
+            if (j + 3 == steps) dev::umma_commit_if(on, q_free);
           }
         }
         if (begun) {
@@ -534,7 +547,7 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
         }
       }
       // every MMA issued has completed before TMEM may be freed
-      dev::umma_commit(done);
+      dev::umma_commit_if(on, done);
       dev::mbar_wait_clk(done, 0, nullptr, 1ll << 28);
     }
     __syncwarp();
@@ -600,6 +613,13 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
       // y = x * y_in is what the cap's tanh takes (a row past the unit holds
       // anything and must not ask for the exact form)
       const float y_in = valid ? cap_in * (0.5f / 1.4426950408889634f) : 0.f;
+      // Halves that are plain to every row of this warp: each of their keys is
+      // seen and none lies past a row's position: h < ppre, or pbeg <= h < pend
+      const int rlo = min(32 * quarter, max(0, nx * G - 1)), rhi = min(32 * quarter + 31, max(0, nx * G - 1));
+      const int pmin = px + rlo / G, pmax = px + rhi / G;
+      const int pend = (min(pmin + 1, u.len)) / kHalf;
+      const int pbeg = tl.window > 0 ? (max(0, pmax - tl.window + 1) + kHalf - 1) / kHalf : 0;
+      const int ppre = (SLOPES ? min(u.pfx, pmin + 1) : u.pfx) / kHalf;
       float ref = -1e30f, lsum = 0.f;
       bool first = true;
       int h = tl.first_half();
@@ -609,51 +629,65 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
         wait_ok(&s_full[2 * x + b], (sc >> 1) & 1);
         dev::tc_fence_after();
         const int key0 = h * kHalf;
+        const float dist = (float)(pos - key0);
+        bool slow = first || !(h < ppre || (h >= pbeg && h < pend));
+        if (!slow) {
+          // Weights over the reference in hand, kept in registers until they
+          // are known to be in range (the scores are needed again if not).
+          // Arithmetic on pairs: with two warps per SM sub-partition issue
+          // slots count as much as the exponentials.
+          uint32_t pk[kHalf / 2];
+          uint64_t sum2 = 0;
+          float z2[2] = {0.f, 0.f};
+          const uint64_t in = CAPS ? dev::f2(y_in, y_in) : dev::f2(scale, scale);
+          const uint64_t step = dev::f2(2.f * slope, 2.f * slope);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t w[32];
+            dev::tmem_ld32(ts + 32 * c, w);
+            const float base = SLOPES ? fmaf(-slope, dist - (float)(32 * c), -ref) : -ref;
+            uint64_t off = dev::f2(base, SLOPES ? base + slope : base);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const uint64_t v = dev::f2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+              uint64_t a;
+              if constexpr (CAPS) {
+                const uint64_t y = dev::mul2(v, in), z = dev::mul2(y, y);
+                float z0, z1;
+                dev::f2_split(z, z0, z1);
+                z2[i & 1] = dev::max3(z2[i & 1], z0, z1);
+                uint64_t q = dev::fma2(z, poly2[4], poly2[3]);
+                q = dev::fma2(z, q, poly2[2]);
+                q = dev::fma2(z, q, poly2[1]);
+                q = dev::fma2(z, q, poly2[0]);
+                a = dev::fma2(y, q, off);
+              } else {
+                a = dev::fma2(v, in, off);
+              }
+              if (SLOPES) off = dev::add2(off, step);
+              float e0, e1;
+              dev::f2_split(a, e0, e1);
+              e0 = dev::ex2(e0);
+              e1 = dev::ex2(e1);
+              sum2 = dev::add2(sum2, dev::f2(e0, e1));
+              pk[16 * c + i] = T::FP8 ? dev::pack_f16(e0, e1) : dev::pack_bf16(e0, e1);
+            }
+          }
+          float sum, odd;
+          dev::f2_split(sum2, sum, odd);
+          sum += odd;
+          slow = __any_sync(0xffffffffu,
+                            valid && (!(sum <= T::BIG) || (CAPS && !(fmaxf(z2[0], z2[1]) <= kCapFast * kCapFast))));
+          if (!slow) {
+            lsum += sum;
+            dev::tmem_st32(ts, pk);
+          }
+        }
+        if (slow) {
         // the row sees keys [wlo, hi) and [0, pl) of the half tile
         const int hi = valid ? min(pos + 1, u.len) - key0 : 0;
         const int wlo = tl.window > 0 ? pos - tl.window + 1 - key0 : 0;
         const int pl = valid ? u.pfx - key0 : 0;
-        const bool whole = (hi >= kHalf && wlo <= 0) || pl >= kHalf;
-        const bool edge = !__all_sync(0xffffffffu, whole);
-        const bool ahead = SLOPES && __any_sync(0xffffffffu, slope != 0.f && pl > pos + 1 - key0);
-        const float dist = (float)(pos - key0);
-        // 32 scores of the row's tile (in w) -> weights over the reference, as
-        // packed pairs; every key of the chunk is visible and none lies past the
-        // row's position.  Arithmetic on pairs: issue slots count.
-        uint64_t sum2 = 0;
-        float zm0 = 0.f, zm1 = 0.f;
-        auto plain_chunk = [&](int c, const uint32_t (&w)[32], uint32_t* out) {
-          const float base = SLOPES ? fmaf(-slope, dist - (float)(32 * c), -ref) : -ref;
-          uint64_t b = SLOPES ? dev::f2(base, base + slope) : dev::f2(base, base);
-          const uint64_t step = dev::f2(2.f * slope, 2.f * slope);
-          const uint64_t in = CAPS ? dev::f2(y_in, y_in) : dev::f2(scale, scale);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const uint64_t x = dev::f2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
-            uint64_t a;
-            if constexpr (CAPS) {
-              const uint64_t y = dev::mul2(x, in), z = dev::mul2(y, y);
-              float z0, z1;
-              dev::f2_split(z, z0, z1);
-              if (i & 1) zm1 = dev::max3(zm1, z0, z1);
-              else zm0 = dev::max3(zm0, z0, z1);
-              uint64_t q = dev::fma2(z, poly2[4], poly2[3]);
-              q = dev::fma2(z, q, poly2[2]);
-              q = dev::fma2(z, q, poly2[1]);
-              q = dev::fma2(z, q, poly2[0]);
-              a = dev::fma2(y, q, b);
-            } else {
-              a = dev::fma2(x, in, b);
-            }
-            if (SLOPES) b = dev::add2(b, step);
-            float e0, e1;
-            dev::f2_split(a, e0, e1);
-            e0 = dev::ex2(e0);
-            e1 = dev::ex2(e1);
-            sum2 = dev::add2(sum2, dev::f2(e0, e1));
-            out[i] = T::FP8 ? dev::pack_f16(e0, e1) : dev::pack_bf16(e0, e1);
-          }
-        };
         // 32 scores of any tile -> exponents s - rf in log2 units: masks, keys
         // past the row's position (their distance has the other sign), and with
         // `exact` the cap's exact form
@@ -705,28 +739,6 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
           }
           return (s4[0] + s4[1]) + (s4[2] + s4[3]);
         };
-        bool slow = first || edge || ahead;
-        if (!slow) {
-          // weights over the reference in hand, kept in registers until they
-          // are known to be in range (S is needed again if not)
-          uint32_t pk[kHalf / 2], w[2][32];
-          dev::tmem_ld32_start(ts, w[0]);
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            dev::tmem_wait32(w[c & 1]);
-            if (c < 1) dev::tmem_ld32_start(ts + 32 * (c + 1), w[(c + 1) & 1]);
-            plain_chunk(c, w[c & 1], pk + 16 * c);
-          }
-          float s0, s1;
-          dev::f2_split(sum2, s0, s1);
-          const float sum = s0 + s1;
-          slow = __any_sync(0xffffffffu, !(sum <= T::BIG) || (CAPS && !(fmaxf(zm0, zm1) <= kCapFast * kCapFast)));
-          if (!slow) {
-            lsum += sum;
-            dev::tmem_st32(ts, pk);
-          }
-        }
-        if (slow) {
           // the row max first, then the weights, chunk by chunk over S
           bool exact = false;
           float m, zmax;
@@ -769,8 +781,6 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
             lsum += chunk_sum(a, pk);
             dev::tmem_st16(ts + 16 * c, pk);  // over scores already read
           }
-        }
-        first = false;
         if constexpr (!T::FP8) {
           // V rows that no row of the unit sees may hold anything (0 * NaN):
           // each query tile zeroes them before its own PV (neither waits for
@@ -790,6 +800,8 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
           zero_v(max(0, max(u.len, u.pfx) - key0), min(kHalf, tl.nb * BS - key0));
           zero_v(max(u.pfx, key0) - key0, min(tl.lo, key0 + kHalf) - key0);
         }
+        }
+        first = false;
         dev::tc_fence_before();
         __syncwarp();
         if (lane == 0) dev::mbar_arrive(&p_full[2 * x + b]);
