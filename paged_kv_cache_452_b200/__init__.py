@@ -19,6 +19,7 @@ PA_F32, PA_BF16, PA_FP8_E4M3 = 0, 1, 2
 _CODES = {"f32": PA_F32, "bf16": PA_BF16, "e4m3": PA_FP8_E4M3}
 _TORCH = {PA_F32: torch.float32, PA_BF16: torch.bfloat16, PA_FP8_E4M3: torch.uint8}
 _NAMES = {v: k for k, v in _CODES.items()}
+_SIZES = {PA_F32: 4, PA_BF16: 2, PA_FP8_E4M3: 1}
 
 
 class CacheDesc(ctypes.Structure):
@@ -101,55 +102,59 @@ def pa_cache_write(desc, k_new, v_new, slot_mapping, k_cache, v_cache, stream=No
                                 _ptr(k_cache), _ptr(v_cache), _stream(stream)), "pa_cache_write")
 
 
-def _rows(who, name, t, dtype, device, heads, dim, contiguous=True):
-    """Checks a [tokens][heads][dim] tensor and returns the elements between two tokens' rows."""
-    if t.dtype != dtype or t.device != device or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise PaError(1, f"{who}: {name} must be [tokens][{heads}][{dim}] of {dtype} on {device}, got "
-                         f"{tuple(t.shape)} of {t.dtype} on {t.device}")
+def _rows(who, name, t, dtype, dev, n, heads, dim):
+    """Checks a [n][heads][dim] tensor whose tokens' rows may lie apart; the elements between two of them."""
+    if t.dtype != dtype or t.get_device() != dev or t.shape != (n, heads, dim):
+        raise PaError(1, f"{who}: {name} must be {(n, heads, dim)} of {dtype} on cuda:{dev}, got {tuple(t.shape)} of "
+                         f"{t.dtype} on {t.device}")
     step, head, one = t.stride()
-    n = t.shape[0]
-    if one != 1 or (heads > 1 and head != dim) or (n > 1 and (step != heads * dim if contiguous else step < heads * dim)):
+    if one != 1 or (head != dim and heads > 1) or (n > 1 and step < heads * dim):
         raise PaError(1, f"{who}: {name} has strides {t.stride()}")
     return step if n > 1 else heads * dim
 
 
-def _array(who, name, t, dtype, device, shape):
+def _array(who, name, t, dtype, dev, shape):
     """Checks a contiguous tensor of a given type, place and shape."""
-    if t.dtype != dtype or t.device != device or t.shape != shape or not t.is_contiguous():
-        raise PaError(1, f"{who}: {name} must be a contiguous {tuple(shape)} of {dtype} on {device}, got "
+    if t.dtype != dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        raise PaError(1, f"{who}: {name} must be a contiguous {tuple(shape)} of {dtype} on cuda:{dev}, got "
                          f"{tuple(t.shape)} of {t.dtype} on {t.device}")
 
 
-def _pools(who, desc, k_cache, v_cache, device):
+def _pools(who, desc, k_cache, v_cache, dev):
     """Checks the pools against the desc (any view of the same bytes is taken)."""
-    need = desc.num_blocks * desc.num_kv_heads * desc.block_size * desc.head_dim * desc.kv_torch_dtype.itemsize
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if t.device != device or not t.is_contiguous() or t.numel() * t.element_size() != need:
-            raise PaError(1, f"{who}: {name} must hold {need} contiguous bytes on {device}")
-    for name, t in (("k_head_scales", desc._keep[0]), ("v_head_scales", desc._keep[1])):
-        if isinstance(t, torch.Tensor):
-            _array(who, name, t, torch.float32, device, (desc.num_kv_heads,))
+    need = desc.num_blocks * desc.num_kv_heads * desc.block_size * desc.head_dim * _SIZES[desc.kv_dtype]
+    for t in (k_cache, v_cache):
+        if t.nbytes != need or t.get_device() != dev or not t.is_contiguous():
+            name = "k_cache" if t is k_cache else "v_cache"
+            raise PaError(1, f"{who}: {name} must hold {need} contiguous bytes on cuda:{dev}")
+    if desc.k_head_scales or desc.v_head_scales:
+        for name, t in (("k_head_scales", desc._keep[0]), ("v_head_scales", desc._keep[1])):
+            if isinstance(t, torch.Tensor):
+                _array(who, name, t, torch.float32, dev, (desc.num_kv_heads,))
 
 
-class _On:
-    """Makes a device current for a call (the library launches on the current one)."""
+def _call(who, dev, stream, f, *args):
+    """f(*args, stream) with the tensors' device current (the library launches on the current one), on that device's
+    current stream if none is given."""
+    if dev < 0:
+        raise PaError(1, f"{who}: tensors must be on a CUDA device")
+    was = torch.cuda.current_device()
+    if was != dev:
+        torch.cuda.set_device(dev)
+    try:
+        rc = f(*args, _stream(stream))
+        if rc != 0:
+            raise PaError(rc, f"{who}: {lib().pa_last_error().decode()}")
+    finally:
+        if was != dev:
+            torch.cuda.set_device(was)
 
-    def __init__(self, who, device, stream):
-        if device.type != "cuda":
-            raise PaError(1, f"{who}: tensors must be on a CUDA device, got {device}")
-        self.stream, self.back = stream, None
-        self.device = device.index
 
-    def __enter__(self):
-        was = torch.cuda.current_device()
-        if was != self.device:
-            torch.cuda.set_device(self.device)
-            self.back = was
-        return _stream(self.stream)
-
-    def __exit__(self, *exc):
-        if self.back is not None:
-            torch.cuda.set_device(self.back)
+def _parameter(who, name, t, dtypes, dims):
+    """Checks a tensor that a parameter block holds: contiguous, of one of the dtypes; its device's index."""
+    if t.dtype not in dtypes or t.dim() != dims or not t.is_contiguous():
+        raise PaError(1, f"{who}: {name} must be a contiguous {dims}-d tensor of {dtypes}, got {tuple(t.shape)} of {t.dtype}")
+    return t.get_device()
 
 
 class QkPrep(ctypes.Structure):
@@ -162,9 +167,20 @@ class QkPrep(ctypes.Structure):
     def make(cls, q_weight=None, k_weight=None, eps=1e-6, cos_sin=None, interleaved=False):
         """q_weight / k_weight: device [head_dim] in the query dtype, or None (no norm).  cos_sin: device fp32
         [num_positions][rot_dim], a position's cosines and then its sines, or None (no rotation)."""
-        n, rot = (int(cos_sin.shape[0]), int(cos_sin.shape[1])) if cos_sin is not None else (0, 0)
+        who = "QkPrep.make"
+        held = [(t.dtype, t.shape[0], _parameter(who, name, t, (torch.float32, torch.bfloat16), 1))
+                for name, t in (("q_weight", q_weight), ("k_weight", k_weight)) if t is not None]
+        devs = {h[2] for h in held}
+        n = rot = 0
+        if cos_sin is not None:
+            devs.add(_parameter(who, "cos_sin", cos_sin, (torch.float32,), 2))
+            n, rot = (int(v) for v in cos_sin.shape)
+        if len(devs) > 1 or len({h[:2] for h in held}) > 1:
+            raise PaError(1, f"{who}: weights of one dtype and length, and all tensors on one device")
         p = cls(_ptr(q_weight), _ptr(k_weight), float(eps), _ptr(cos_sin), n, rot, int(bool(interleaved)))
         p._keep = (q_weight, k_weight, cos_sin)
+        p._dev = devs.pop() if devs else None
+        p._weights = held[0][:2] if held else None
         return p
 
 
@@ -172,43 +188,36 @@ def pa_norm_rope_write(desc, prep, q, k, v, positions, slot_mapping, q_out, k_ca
     """Norm and rotation of q [T][Hq][D] and k [T][Hkv][D], queries to q_out, k and v to the pools through int64
     slots.  q, k, v may be slices of one projection's output (token stride above a row); positions: int32 [T]
     (None without a rotation table); q_out contiguous, or q itself."""
-    who, device, dt = "pa_norm_rope_write", q.device, desc.q_torch_dtype
-    n, hkv, d = int(q.shape[0]), desc.num_kv_heads, desc.head_dim
-    qs = _rows(who, "q", q, dt, device, desc.num_q_heads, d, False)
-    ks = _rows(who, "k", k, dt, device, hkv, d, False)
-    vs = _rows(who, "v", v, dt, device, hkv, d, False)
-    _rows(who, "q_out", q_out, dt, device, desc.num_q_heads, d)
-    if k.shape[0] != n or v.shape[0] != n or q_out.shape[0] != n:
-        raise PaError(1, f"{who}: q, k, v and q_out differ in tokens")
-    _array(who, "slot_mapping", slot_mapping, torch.int64, device, (n,))
-    qw, kw, cs = prep._keep
-    if cs is not None:
-        _array(who, "cos_sin", cs, torch.float32, device, (prep.num_positions, prep.rot_dim))
-        if positions is None:
-            raise PaError(1, f"{who}: a rotation needs positions")
+    who, dev, dt = "pa_norm_rope_write", q.get_device(), desc.q_torch_dtype
+    n, hq, hkv, d = q.shape[0], desc.num_q_heads, desc.num_kv_heads, desc.head_dim
+    qs = _rows(who, "q", q, dt, dev, n, hq, d)
+    ks = _rows(who, "k", k, dt, dev, n, hkv, d)
+    vs = _rows(who, "v", v, dt, dev, n, hkv, d)
+    _array(who, "q_out", q_out, dt, dev, (n, hq, d))
+    _array(who, "slot_mapping", slot_mapping, torch.int64, dev, (n,))
     if positions is not None:
-        _array(who, "positions", positions, torch.int32, device, (n,))
-    for name, w in (("q_weight", qw), ("k_weight", kw)):
-        if w is not None:
-            _array(who, name, w, dt, device, (d,))
-    _pools(who, desc, k_cache, v_cache, device)
-    with _On(who, device, stream) as st:
-        _check(lib().pa_norm_rope_write(ctypes.byref(desc), ctypes.byref(prep), _ptr(q), qs, _ptr(k), ks, _ptr(v), vs,
-                                        _ptr(positions), _ptr(slot_mapping), n, _ptr(q_out), _ptr(k_cache),
-                                        _ptr(v_cache), st), who)
+        _array(who, "positions", positions, torch.int32, dev, (n,))
+    elif prep.cos_sin:
+        raise PaError(1, f"{who}: a rotation needs positions")
+    if (prep._dev is not None and prep._dev != dev) or (prep._weights is not None and prep._weights != (dt, d)):
+        raise PaError(1, f"{who}: prep holds q_weight, k_weight or cos_sin of another device, dtype or head_dim")
+    _pools(who, desc, k_cache, v_cache, dev)
+    _call(who, dev, stream, lib().pa_norm_rope_write, ctypes.byref(desc), ctypes.byref(prep), q.data_ptr(), qs,
+          k.data_ptr(), ks, v.data_ptr(), vs, _ptr(positions), slot_mapping.data_ptr(), n, q_out.data_ptr(),
+          k_cache.data_ptr(), v_cache.data_ptr())
 
 
 def pa_cache_read(desc, slot_mapping, k_cache, v_cache, k_out, v_out, stream=None):
     """Rows of int64 slots out of the pools into k_out, v_out [T][Hkv][D], dequantised."""
-    who, device, dt = "pa_cache_read", k_out.device, desc.q_torch_dtype
-    n = int(slot_mapping.shape[0])
-    _array(who, "slot_mapping", slot_mapping, torch.int64, device, (n,))
-    for name, t in (("k_out", k_out), ("v_out", v_out)):
-        _array(who, name, t, dt, device, (n, desc.num_kv_heads, desc.head_dim))
-    _pools(who, desc, k_cache, v_cache, device)
-    with _On(who, device, stream) as st:
-        _check(lib().pa_cache_read(ctypes.byref(desc), _ptr(slot_mapping), n, _ptr(k_cache), _ptr(v_cache),
-                                   _ptr(k_out), _ptr(v_out), st), who)
+    who, dev, dt = "pa_cache_read", k_out.get_device(), desc.q_torch_dtype
+    n = slot_mapping.shape[0]
+    shape = (n, desc.num_kv_heads, desc.head_dim)
+    _array(who, "slot_mapping", slot_mapping, torch.int64, dev, (n,))
+    _array(who, "k_out", k_out, dt, dev, shape)
+    _array(who, "v_out", v_out, dt, dev, shape)
+    _pools(who, desc, k_cache, v_cache, dev)
+    _call(who, dev, stream, lib().pa_cache_read, ctypes.byref(desc), slot_mapping.data_ptr(), n, k_cache.data_ptr(),
+          v_cache.data_ptr(), k_out.data_ptr(), v_out.data_ptr())
 
 
 def pa_copy_blocks(desc, src, dst, k_cache, v_cache, stream=None):
@@ -348,8 +357,19 @@ class ScoreMod(ctypes.Structure):
         """softcap: cap * tanh(score / cap), 0 for none; window: keys a row sees up to itself, 0 for all; slopes:
         device fp32 [num_q_heads], the score loses slope * distance; prefix_lens: device int32 [num_seqs], leading
         keys that every row sees."""
+        who = "ScoreMod.make"
+        devs = set()
+        if slopes is not None:
+            devs.add(_parameter(who, "slopes", slopes, (torch.float32,), 1))
+        if prefix_lens is not None:
+            devs.add(_parameter(who, "prefix_lens", prefix_lens, (torch.int32,), 1))
+        if len(devs) > 1:
+            raise PaError(1, f"{who}: slopes and prefix_lens on one device")
         m = cls(float(softcap), int(window), _ptr(slopes), _ptr(prefix_lens))
         m._keep = (slopes, prefix_lens)
+        m._dev = devs.pop() if devs else None
+        m._heads = slopes.shape[0] if slopes is not None else None
+        m._seqs = prefix_lens.shape[0] if prefix_lens is not None else None
         return m
 
 
@@ -361,50 +381,45 @@ def pa_biased_workspace_size(desc, num_seqs, num_tokens) -> int:
 
 
 def _biased_args(who, desc, mod, q, k_cache, v_cache, block_tables, seq_lens, out, workspace):
-    device, dt = q.device, desc.q_torch_dtype
-    shape = (q.shape[0], desc.num_q_heads, desc.head_dim)
-    _array(who, "q", q, dt, device, shape)
-    _array(who, "out", out, dt, device, shape)
-    n = int(seq_lens.shape[0])
-    _array(who, "seq_lens", seq_lens, torch.int32, device, (n,))
+    dev, dt, hq = q.get_device(), desc.q_torch_dtype, desc.num_q_heads
+    shape = (q.shape[0], hq, desc.head_dim)
+    _array(who, "q", q, dt, dev, shape)
+    _array(who, "out", out, dt, dev, shape)
+    n = seq_lens.shape[0]
+    _array(who, "seq_lens", seq_lens, torch.int32, dev, (n,))
     if block_tables.dim() != 2:
         raise PaError(1, f"{who}: block_tables must be [num_seqs][max_blocks]")
-    _array(who, "block_tables", block_tables, torch.int32, device, (n, block_tables.shape[1]))
-    slopes, prefix = mod._keep
-    if slopes is not None:
-        _array(who, "slopes", slopes, torch.float32, device, (desc.num_q_heads,))
-    if prefix is not None:
-        _array(who, "prefix_lens", prefix, torch.int32, device, (n,))
-    if workspace.device != device or not workspace.is_contiguous():
-        raise PaError(1, f"{who}: workspace must be contiguous on {device}")
-    _pools(who, desc, k_cache, v_cache, device)
-    return device, n
+    _array(who, "block_tables", block_tables, torch.int32, dev, (n, block_tables.shape[1]))
+    if ((mod._dev is not None and mod._dev != dev) or (mod._heads is not None and mod._heads != hq) or
+            (mod._seqs is not None and mod._seqs != n)):
+        raise PaError(1, f"{who}: mod holds slopes or prefix_lens of another device, head or sequence count")
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise PaError(1, f"{who}: workspace must be contiguous on cuda:{dev}")
+    _pools(who, desc, k_cache, v_cache, dev)
+    return dev, n
 
 
 def pa_decode_biased(desc, mod, q, k_cache, v_cache, block_tables, seq_lens, scale, out, workspace, stream=None):
     """pa_decode with capped, distance-biased or window- and prefix-masked scores (mod: a ScoreMod)."""
     who = "pa_decode_biased"
-    device, s = _biased_args(who, desc, mod, q, k_cache, v_cache, block_tables, seq_lens, out, workspace)
-    if q.shape[0] != s:
-        raise PaError(1, f"{who}: {q.shape[0]} query rows for {s} sequences")
-    with _On(who, device, stream) as st:
-        _check(lib().pa_decode_biased(ctypes.byref(desc), ctypes.byref(mod), _ptr(q), _ptr(k_cache), _ptr(v_cache),
-                                      _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens), s, float(scale),
-                                      _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(), st),
-               who)
+    dev, n = _biased_args(who, desc, mod, q, k_cache, v_cache, block_tables, seq_lens, out, workspace)
+    if q.shape[0] != n:
+        raise PaError(1, f"{who}: {q.shape[0]} query rows for {n} sequences")
+    _call(who, dev, stream, lib().pa_decode_biased, ctypes.byref(desc), ctypes.byref(mod), q.data_ptr(),
+          k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), block_tables.shape[1], seq_lens.data_ptr(), n,
+          scale, out.data_ptr(), workspace.data_ptr(), workspace.nbytes)
 
 
 def pa_decode_chunked_prefill_biased(desc, mod, q, k_cache, v_cache, block_tables, query_start_loc, seq_lens,
                                      max_q_len, scale, out, workspace, stream=None):
     """pa_decode_chunked_prefill with capped, distance-biased or window- and prefix-masked scores (mod: a ScoreMod)."""
     who = "pa_decode_chunked_prefill_biased"
-    device, s = _biased_args(who, desc, mod, q, k_cache, v_cache, block_tables, seq_lens, out, workspace)
-    _array(who, "query_start_loc", query_start_loc, torch.int32, device, (s + 1,))
-    with _On(who, device, stream) as st:
-        _check(lib().pa_decode_chunked_prefill_biased(
-            ctypes.byref(desc), ctypes.byref(mod), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
-            block_tables.shape[1], _ptr(query_start_loc), _ptr(seq_lens), s, q.shape[0], int(max_q_len), float(scale),
-            _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(), st), who)
+    dev, n = _biased_args(who, desc, mod, q, k_cache, v_cache, block_tables, seq_lens, out, workspace)
+    _array(who, "query_start_loc", query_start_loc, torch.int32, dev, (n + 1,))
+    _call(who, dev, stream, lib().pa_decode_chunked_prefill_biased, ctypes.byref(desc), ctypes.byref(mod), q.data_ptr(),
+          k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
+          query_start_loc.data_ptr(), seq_lens.data_ptr(), n, q.shape[0], max_q_len, scale, out.data_ptr(),
+          workspace.data_ptr(), workspace.nbytes)
 
 
 def default_scale(head_dim):

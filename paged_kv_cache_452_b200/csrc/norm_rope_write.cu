@@ -18,34 +18,41 @@
 // chunks of four.  A lane's two chunks hold both halves of its pairs (chunk
 // c of the first half and of the second half; interleaved pairs sit inside a
 // chunk), so the rotation needs no exchange between lanes and only the norm
-// reduces over the row's lanes.  A row group takes four head rows of one
-// token, all loads first, and reads the token's cos and sin once.
+// reduces over the row's lanes.  A row group takes a few head rows of one
+// token, all loads first and kept as they came, and reads the token's cos and
+// sin once.  e4m3 V, whose pool is d-major, goes by windows of 16 tokens: a
+// lane takes four elements of 16 rows and stores 16 bytes per element where
+// the window's slots fill an aligned part of a block (single bytes otherwise).
 #include <cuda_runtime.h>
 
 #include "pa_device.cuh"
 #include "pa_kernels.h"
+#include "slot_window.cuh"
 
 namespace pa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kHeads = 4;  // head rows of one token per row group
 
+// Four elements as they lie in memory.
+template <typename T> struct Four { using V = uint2; };
+template <> struct Four<float> { using V = uint4; };
+
+__device__ __forceinline__ void unpack(const uint2& v, float (&x)[4]) {
+  x[0] = dev::bf16_bits_to_f32(v.x & 0xFFFFu);
+  x[1] = dev::bf16_bits_to_f32(v.x >> 16);
+  x[2] = dev::bf16_bits_to_f32(v.y & 0xFFFFu);
+  x[3] = dev::bf16_bits_to_f32(v.y >> 16);
+}
+__device__ __forceinline__ void unpack(const uint4& v, float (&x)[4]) {
+  x[0] = __uint_as_float(v.x);
+  x[1] = __uint_as_float(v.y);
+  x[2] = __uint_as_float(v.z);
+  x[3] = __uint_as_float(v.w);
+}
 template <typename T>
-__device__ __forceinline__ void load4(const T* p, float (&x)[4]) {
-  if constexpr (sizeof(T) == 4) {
-    const float4 v = *reinterpret_cast<const float4*>(p);
-    x[0] = v.x;
-    x[1] = v.y;
-    x[2] = v.z;
-    x[3] = v.w;
-  } else {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    x[0] = dev::bf16_bits_to_f32(v.x & 0xFFFFu);
-    x[1] = dev::bf16_bits_to_f32(v.x >> 16);
-    x[2] = dev::bf16_bits_to_f32(v.y & 0xFFFFu);
-    x[3] = dev::bf16_bits_to_f32(v.y >> 16);
-  }
+__device__ __forceinline__ typename Four<T>::V load4(const T* p) {
+  return *reinterpret_cast<const typename Four<T>::V*>(p);
 }
 template <typename T>
 __device__ __forceinline__ void store4(T* p, const float (&x)[4]) {
@@ -55,21 +62,102 @@ __device__ __forceinline__ void store4(T* p, const float (&x)[4]) {
     *reinterpret_cast<uint2*>(p) = make_uint2(dev::pack_bf16(x[0], x[1]), dev::pack_bf16(x[2], x[3]));
   }
 }
-__device__ __forceinline__ uint32_t quant4(const float (&x)[4], float scale) {
-  const uint32_t lo = dev::e4m3x2_from_f32(__fdiv_rn(x[0], scale), __fdiv_rn(x[1], scale));
-  const uint32_t hi = dev::e4m3x2_from_f32(__fdiv_rn(x[2], scale), __fdiv_rn(x[3], scale));
-  return lo | (hi << 16);
+__device__ __forceinline__ uint32_t quant2(float a, float b, float scale) {
+  return dev::e4m3x2_from_f32(__fdiv_rn(a, scale), __fdiv_rn(b, scale));
 }
 
-// T: element type of the new rows; FP8: an e4m3 pool.
-template <typename T, int D, bool FP8>
-__global__ void __launch_bounds__(kThreads) norm_rope_write_kernel(const NormRopeParams p) {
+// e4m3 V of one window of tokens and one kv head per D / 4 lanes.
+template <typename T, int D>
+__device__ __forceinline__ void write_v_window(const NormRopeParams& p, int64_t item) {
+  constexpr int LANES = D / 4;
+  const int hkv = p.num_kv_heads;
+  const int64_t heads = (hkv * LANES + 31) / 32 * (32 / LANES);  // heads per window, in whole warps
+  const int64_t win = item / heads;
+  const int h = (int)(item % heads);
+  const int d0 = 4 * (threadIdx.x % LANES);
+  const bool live = h < hkv;
+  const float scale = !live ? 1.f : p.v_head ? __ldg(p.v_head + h) : p.v_scale;
+  const int64_t end = dev::window_start(p.slots, p.num_tokens, win + 1);
+  for (int64_t t = dev::window_start(p.slots, p.num_tokens, win); t < end; t += dev::kWindow) {
+    const int n = (int)min((int64_t)dev::kWindow, end - t);
+    int64_t s0;
+    bool whole = dev::window_aligned(p.slots, t, n, p.num_slots, &s0);
+    // a token whose position is outside the table is left out
+    if (p.cos_sin) {
+      const int pos = (threadIdx.x & 31) < n ? __ldg(p.positions + t + (threadIdx.x & 31)) : 0;
+      whole = whole && __all_sync(0xffffffffu, pos >= 0 && pos < p.num_positions);
+    }
+    typename Four<T>::V raw[dev::kWindow];
+    if (live) {
+#pragma unroll
+      for (int j = 0; j < dev::kWindow; ++j)
+        raw[j] = load4(reinterpret_cast<const T*>(p.v) + (t + min(j, n - 1)) * p.v_stride + (int64_t)h * D + d0);
+    }
+    if (!live) continue;
+    uint32_t code[4][4];  // [element][4 tokens]
+#pragma unroll
+    for (int j = 0; j < dev::kWindow; j += 2) {
+      float a[4], b[4];
+      unpack(raw[j], a);
+      unpack(raw[j + 1], b);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t two = quant2(a[e], b[e], scale);
+        if (j & 2) code[e][j >> 2] |= two << 16;
+        else code[e][j >> 2] = two;
+      }
+    }
+    if (whole) {
+      const int64_t blk = s0 / p.block_size;
+      uint8_t* dst = p.v_cache + ((blk * hkv + h) * D + d0) * p.block_size + s0 % p.block_size;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        *reinterpret_cast<uint4*>(dst + (int64_t)e * p.block_size) =
+            make_uint4(code[e][0], code[e][1], code[e][2], code[e][3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < dev::kWindow; ++j) {
+        if (j >= n) break;
+        const int64_t slot = __ldg(p.slots + t + j);
+        if (slot < 0 || slot >= p.num_slots) continue;
+        if (p.cos_sin) {
+          const int pos = __ldg(p.positions + t + j);
+          if (pos < 0 || pos >= p.num_positions) continue;
+        }
+        const int64_t blk = slot / p.block_size;
+        uint8_t* dst = p.v_cache + ((blk * hkv + h) * D + d0) * p.block_size + slot % p.block_size;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dst[(int64_t)e * p.block_size] = (uint8_t)(code[e][j >> 2] >> (8 * (j & 3)));
+      }
+    }
+  }
+}
+
+// T: element type of the new rows; FP8: an e4m3 pool; HEADS: head rows of one
+// token per row group.  Blocks from `row_blocks` on write e4m3 V.
+template <typename T, int D, bool FP8, int HEADS>
+__global__ void __launch_bounds__(kThreads) norm_rope_write_kernel(const NormRopeParams p, unsigned row_blocks) {
   dev::grid_dep_wait();
   dev::grid_dep_launch();
+  const int hq = p.num_q_heads, hkv = p.num_kv_heads;
+  if constexpr (FP8) {
+    if (blockIdx.x >= row_blocks) {
+      constexpr int PER = kThreads / (D / 4);
+      const int64_t heads = (hkv * (D / 4) + 31) / 32 * (32 / (D / 4));
+      const int64_t items = ((int64_t)p.num_tokens + dev::kWindow - 1) / dev::kWindow * heads;
+      const int64_t item = (int64_t)(blockIdx.x - row_blocks) * PER + threadIdx.x / (D / 4);
+      if (item < items) write_v_window<T, D>(p, item);  // whole warps: items are a multiple of a warp's
+      return;
+    }
+  }
   constexpr int LANES = D / 8;  // lanes of a head row
-  const int hq = p.num_q_heads, hkv = p.num_kv_heads, nh = hq + 2 * hkv;
-  const int per_token = (nh + kHeads - 1) / kHeads;
+  const int nh = hq + (FP8 ? 1 : 2) * hkv;
+  const int per_token = (nh + HEADS - 1) / HEADS;
   const int64_t items = (int64_t)p.num_tokens * per_token;
+  const int64_t item = (int64_t)blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
+  const bool live = item < items;  // whole warps stay for the norm's shuffles
+  const int64_t t = live ? item / per_token : 0;
+  const int h0 = live ? (int)(item % per_token) * HEADS : nh;
   const int c = threadIdx.x % LANES;
   const int rot = p.rot_dim, half = rot >> 1;
   const bool turns = 8 * c < rot;  // this lane's elements are rotated
@@ -79,145 +167,127 @@ __global__ void __launch_bounds__(kThreads) norm_rope_write_kernel(const NormRop
     a0 = 4 * c;
     a1 = half + 4 * c;
   }
-  float qw[2][4], kw[2][4];
+  const int pos = p.cos_sin ? __ldg(p.positions + t) : 0;
+  const int64_t slot = __ldg(p.slots + t);
+  using V = typename Four<T>::V;
+  V raw[HEADS][2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) qw[0][i] = qw[1][i] = kw[0][i] = kw[1][i] = 1.f;
-  if (p.q_weight) {
-    load4(reinterpret_cast<const T*>(p.q_weight) + a0, qw[0]);
-    load4(reinterpret_cast<const T*>(p.q_weight) + a1, qw[1]);
+  for (int j = 0; j < HEADS; ++j) {
+    const int h = h0 + j;
+    raw[j][0] = raw[j][1] = V{};
+    if (h < nh) {
+      const T* row = h < hq ? reinterpret_cast<const T*>(p.q) + t * p.q_stride + (int64_t)h * D
+                   : h < hq + hkv ? reinterpret_cast<const T*>(p.k) + t * p.k_stride + (int64_t)(h - hq) * D
+                                  : reinterpret_cast<const T*>(p.v) + t * p.v_stride + (int64_t)(h - hq - hkv) * D;
+      raw[j][0] = load4(row + a0);
+      raw[j][1] = load4(row + a1);
+    }
   }
-  if (p.k_weight) {
-    load4(reinterpret_cast<const T*>(p.k_weight) + a0, kw[0]);
-    load4(reinterpret_cast<const T*>(p.k_weight) + a1, kw[1]);
+  const bool known = p.cos_sin == nullptr || (pos >= 0 && pos < p.num_positions);
+  const bool in_pool = slot >= 0 && slot < p.num_slots;
+  const int64_t blk = in_pool ? slot / p.block_size : 0;
+  const int off = in_pool ? (int)(slot % p.block_size) : 0;
+  // cos and sin of the lane's four pairs
+  float cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
+  if (turns && known && p.cos_sin) {
+    unpack(__ldg(reinterpret_cast<const uint4*>(p.cos_sin + (int64_t)pos * rot + 4 * c)), cs);
+    unpack(__ldg(reinterpret_cast<const uint4*>(p.cos_sin + (int64_t)pos * rot + half + 4 * c)), sn);
   }
-  const int64_t step = (int64_t)gridDim.x * (kThreads / LANES);
-  // whole warps iterate together (the norm's shuffles); a row group past the
-  // end works on nothing
-  const int64_t first = (int64_t)blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
-  const int64_t warp_first = first - (threadIdx.x & 31) / LANES;
-  for (int64_t base = warp_first; base < items; base += step) {
-    const int64_t item = base + (threadIdx.x & 31) / LANES;
-    const bool live = item < items;
-    const int64_t t = live ? item / per_token : 0;
-    const int h0 = live ? (int)(item % per_token) * kHeads : nh;
-    const int pos = p.cos_sin ? __ldg(p.positions + t) : 0;
-    const int64_t slot = __ldg(p.slots + t);
-    const bool known = p.cos_sin == nullptr || (pos >= 0 && pos < p.num_positions);
-    const bool in_pool = slot >= 0 && slot < p.num_slots;
-    const int64_t blk = in_pool ? slot / p.block_size : 0;
-    const int off = in_pool ? (int)(slot % p.block_size) : 0;
-    float x[kHeads][2][4];
 #pragma unroll
-    for (int j = 0; j < kHeads; ++j) {
-      const int h = h0 + j;
+  for (int j = 0; j < HEADS; ++j) {
+    const int h = h0 + j;
+    const bool is_q = h < hq, is_v = h >= hq + hkv;
+    float x[2][4];
+    unpack(raw[j][0], x[0]);
+    unpack(raw[j][1], x[1]);
+    const T* weight = reinterpret_cast<const T*>(is_q ? p.q_weight : p.k_weight);
+    // the whole warp takes part in the sums: its row groups may hold heads of
+    // different kinds
+    float ss = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[j][0][i] = x[j][1][i] = 0.f;
-      if (h < nh) {
-        const T* row = h < hq ? reinterpret_cast<const T*>(p.q) + t * p.q_stride + (int64_t)h * D
-                     : h < hq + hkv ? reinterpret_cast<const T*>(p.k) + t * p.k_stride + (int64_t)(h - hq) * D
-                                    : reinterpret_cast<const T*>(p.v) + t * p.v_stride + (int64_t)(h - hq - hkv) * D;
-        load4(row + a0, x[j][0]);
-        load4(row + a1, x[j][1]);
+    for (int i = 0; i < 4; ++i) ss += x[0][i] * x[0][i] + x[1][i] * x[1][i];
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if (!is_v && weight) {
+      const float inv = rsqrtf(ss * (1.f / D) + p.eps);
+      float w[2][4];
+      unpack(load4(weight + a0), w[0]);
+      unpack(load4(weight + a1), w[1]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[0][i] *= inv * w[0][i];
+        x[1][i] *= inv * w[1][i];
       }
     }
-    // cos and sin of the lane's four pairs
-    float cs[4], sn[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      cs[i] = 1.f;
-      sn[i] = 0.f;
-    }
-    if (turns && known && p.cos_sin) {
-      const float4 cv = __ldg(reinterpret_cast<const float4*>(p.cos_sin + (int64_t)pos * rot + 4 * c));
-      const float4 sv = __ldg(reinterpret_cast<const float4*>(p.cos_sin + (int64_t)pos * rot + half + 4 * c));
-      cs[0] = cv.x, cs[1] = cv.y, cs[2] = cv.z, cs[3] = cv.w;
-      sn[0] = sv.x, sn[1] = sv.y, sn[2] = sv.z, sn[3] = sv.w;
-    }
-#pragma unroll
-    for (int j = 0; j < kHeads; ++j) {
-      const int h = h0 + j;
-      float ss = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) ss += x[j][0][i] * x[j][0][i] + x[j][1][i] * x[j][1][i];
-#pragma unroll
-      for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (h >= nh || !known) continue;
-      const bool is_q = h < hq, is_v = h >= hq + hkv;
-      if (!is_q && !in_pool) continue;
-      if (!is_v) {
-        const bool norm = is_q ? p.q_weight != nullptr : p.k_weight != nullptr;
-        const float inv = norm ? rsqrtf(ss * (1.f / D) + p.eps) : 1.f;
+    if (h >= nh || !known || (!is_q && !in_pool)) continue;
+    if (!is_v && turns) {
+      if (!p.interleaved) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          x[j][0][i] *= inv * (is_q ? qw[0][i] : kw[0][i]);
-          x[j][1][i] *= inv * (is_q ? qw[1][i] : kw[1][i]);
+          const float a = x[0][i], b = x[1][i];
+          x[0][i] = a * cs[i] - b * sn[i];
+          x[1][i] = b * cs[i] + a * sn[i];
         }
-        if (turns) {
-          if (!p.interleaved) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float a = x[j][0][i], b = x[j][1][i];
-              x[j][0][i] = a * cs[i] - b * sn[i];
-              x[j][1][i] = b * cs[i] + a * sn[i];
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float(&ch)[4] = x[j][i >> 1];
-              const float a = ch[2 * (i & 1)], b = ch[2 * (i & 1) + 1];
-              ch[2 * (i & 1)] = a * cs[i] - b * sn[i];
-              ch[2 * (i & 1) + 1] = b * cs[i] + a * sn[i];
-            }
-          }
-        }
-      }
-      if (is_q) {
-        T* dst = reinterpret_cast<T*>(p.q_out) + (t * hq + h) * D;
-        store4(dst + a0, x[j][0]);
-        store4(dst + a1, x[j][1]);
-        continue;
-      }
-      const int kvh = is_v ? h - hq - hkv : h - hq;
-      uint8_t* pool = is_v ? p.v_cache : p.k_cache;
-      if constexpr (!FP8) {
-        T* dst = reinterpret_cast<T*>(pool) + ((blk * hkv + kvh) * p.block_size + off) * D;
-        store4(dst + a0, x[j][0]);
-        store4(dst + a1, x[j][1]);
       } else {
-        const float* head = is_v ? p.v_head : p.k_head;
-        const float scale = head ? __ldg(head + kvh) : (is_v ? p.v_scale : p.k_scale);
-        const uint32_t w0 = quant4(x[j][0], scale), w1 = quant4(x[j][1], scale);
-        if (!is_v) {
-          uint8_t* dst = pool + ((blk * hkv + kvh) * p.block_size + off) * D;
-          *reinterpret_cast<uint32_t*>(dst + a0) = w0;
-          *reinterpret_cast<uint32_t*>(dst + a1) = w1;
-        } else {  // d-major V: one byte per element
-          uint8_t* dst = pool + (blk * hkv + kvh) * D * p.block_size + off;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            dst[(int64_t)(a0 + i) * p.block_size] = (uint8_t)(w0 >> (8 * i));
-            dst[(int64_t)(a1 + i) * p.block_size] = (uint8_t)(w1 >> (8 * i));
-          }
+        for (int i = 0; i < 4; ++i) {
+          float(&ch)[4] = x[i >> 1];
+          const float a = ch[2 * (i & 1)], b = ch[2 * (i & 1) + 1];
+          ch[2 * (i & 1)] = a * cs[i] - b * sn[i];
+          ch[2 * (i & 1) + 1] = b * cs[i] + a * sn[i];
         }
       }
+    }
+    if (is_q) {
+      T* dst = reinterpret_cast<T*>(p.q_out) + (t * hq + h) * D;
+      store4(dst + a0, x[0]);
+      store4(dst + a1, x[1]);
+      continue;
+    }
+    const int kvh = is_v ? h - hq - hkv : h - hq;
+    const int64_t row = ((blk * hkv + kvh) * p.block_size + off) * D;
+    if constexpr (!FP8) {
+      T* dst = reinterpret_cast<T*>(is_v ? p.v_cache : p.k_cache) + row;
+      store4(dst + a0, x[0]);
+      store4(dst + a1, x[1]);
+    } else {
+      const float scale = p.k_head ? __ldg(p.k_head + kvh) : p.k_scale;
+      uint8_t* dst = p.k_cache + row;
+      *reinterpret_cast<uint32_t*>(dst + a0) = quant2(x[0][0], x[0][1], scale) | quant2(x[0][2], x[0][3], scale) << 16;
+      *reinterpret_cast<uint32_t*>(dst + a1) = quant2(x[1][0], x[1][1], scale) | quant2(x[1][2], x[1][3], scale) << 16;
     }
   }
 }
 
-template <typename T, int D, bool FP8>
-cudaError_t launch(const NormRopeParams& p, int num_sms, cudaStream_t stream) {
-  const int per_token = (p.num_q_heads + 2 * p.num_kv_heads + kHeads - 1) / kHeads;
-  const int groups = kThreads / (D / 8);
-  const int64_t need = ((int64_t)p.num_tokens * per_token + groups - 1) / groups;
-  const int64_t most = (int64_t)num_sms * 8;
-  norm_rope_write_kernel<T, D, FP8><<<(unsigned)(need < most ? need : most), kThreads, 0, stream>>>(p);
+template <typename T, int D, bool FP8, int HEADS>
+cudaError_t launch(const NormRopeParams& p, cudaStream_t stream) {
+  const int nh = p.num_q_heads + (FP8 ? 1 : 2) * p.num_kv_heads;
+  const int64_t items = (int64_t)p.num_tokens * ((nh + HEADS - 1) / HEADS);
+  const int64_t rows = (items + kThreads / (D / 8) - 1) / (kThreads / (D / 8));
+  int64_t vwin = 0;
+  if (FP8) {
+    const int64_t heads = (p.num_kv_heads * (D / 4) + 31) / 32 * (32 / (D / 4));
+    const int64_t v = ((int64_t)p.num_tokens + dev::kWindow - 1) / dev::kWindow * heads;
+    vwin = (v + kThreads / (D / 4) - 1) / (kThreads / (D / 4));
+  }
+  if (rows + vwin > INT32_MAX) return cudaErrorNotSupported;
+  norm_rope_write_kernel<T, D, FP8, HEADS>
+      <<<(unsigned)(rows + vwin), kThreads, 0, stream>>>(p, (unsigned)rows);
   return cudaGetLastError();
+}
+
+// Head rows per row group: one while the whole step then fits the GPU at once
+// (latency: a decode step of 64 tokens), else four (bytes in flight).
+template <typename T, int D, bool FP8>
+cudaError_t launch_h(const NormRopeParams& p, int num_sms, cudaStream_t stream) {
+  const int64_t rows = (int64_t)p.num_tokens * (p.num_q_heads + 2 * p.num_kv_heads);
+  return rows * (D / 8) <= (int64_t)num_sms * 2048 ? launch<T, D, FP8, 1>(p, stream) : launch<T, D, FP8, 4>(p, stream);
 }
 
 template <typename T, bool FP8>
 cudaError_t launch_d(const NormRopeParams& p, int num_sms, cudaStream_t stream) {
-  if (p.head_dim == 64) return launch<T, 64, FP8>(p, num_sms, stream);
-  if (p.head_dim == 128) return launch<T, 128, FP8>(p, num_sms, stream);
+  if (p.head_dim == 64) return launch_h<T, 64, FP8>(p, num_sms, stream);
+  if (p.head_dim == 128) return launch_h<T, 128, FP8>(p, num_sms, stream);
   return cudaErrorNotSupported;
 }
 

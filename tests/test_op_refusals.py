@@ -72,9 +72,11 @@ def test_bindings_refuse_wrong_tensors():
         assert "CUDA device" not in str(pytest.raises(pa.PaError, pa.pa_norm_rope_write, desc, prep,
                                                       **{**good, **bad}).value)
     with pytest.raises(pa.PaError, match="q_weight"):
-        pa.pa_norm_rope_write(desc, pa.QkPrep.make(w.float(), w, 1e-6, cs), **good)
+        pa.pa_norm_rope_write(desc, pa.QkPrep.make(w.float(), w.float(), 1e-6, cs), **good)
     with pytest.raises(pa.PaError, match="cos_sin"):
-        pa.pa_norm_rope_write(desc, pa.QkPrep.make(w, w, 1e-6, cs.double()), **good)
+        pa.QkPrep.make(w, w, 1e-6, cs.double())
+    with pytest.raises(pa.PaError, match="weights"):
+        pa.QkPrep.make(w, w.float(), 1e-6, cs)
     with pytest.raises(pa.PaError, match="k_out"):
         pa.pa_cache_read(desc, slots, kc, vc, k[:2], v)
     with pytest.raises(pa.PaError, match="CUDA device"):
@@ -129,8 +131,10 @@ def test_biased_bindings_refuse_wrong_tensors():
     bad = [dict(q=good["q"].float()), dict(q=good["q"][:1]), dict(out=good["out"][:, :4]), dict(k_cache=kc[:2]),
            dict(block_tables=good["block_tables"].long()), dict(block_tables=good["block_tables"][0]),
            dict(seq_lens=good["seq_lens"].long())]
-    bad_mods = [pa.ScoreMod.make(slopes=torch.zeros(4)), pa.ScoreMod.make(slopes=torch.zeros(8).double()),
-                pa.ScoreMod.make(prefix_lens=torch.zeros(3, dtype=i32)), pa.ScoreMod.make(prefix_lens=torch.zeros(2))]
+    bad_mods = [pa.ScoreMod.make(slopes=torch.zeros(4)), pa.ScoreMod.make(prefix_lens=torch.zeros(3, dtype=i32))]
+    for kw in (dict(slopes=torch.zeros(8).double()), dict(prefix_lens=torch.zeros(2)), dict(slopes=torch.zeros(16)[::2])):
+        with pytest.raises(pa.PaError, match="ScoreMod"):
+            pa.ScoreMod.make(**kw)
     chunk = dict(query_start_loc=torch.zeros(3, dtype=i32), max_q_len=1)
     for f, more in ((pa.pa_decode_biased, {}), (pa.pa_decode_chunked_prefill_biased, chunk)):
         with pytest.raises(pa.PaError, match="CUDA device"):
