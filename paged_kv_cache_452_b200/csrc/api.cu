@@ -622,6 +622,8 @@ int pa_norm_rope_write(const pa_cache_desc* d, const pa_qk_prep* prep, const voi
   }
   if (d->kv_dtype != kFP8 && d->kv_dtype != d->q_dtype)
     return fail(PA_ERR_UNSUPPORTED, "%s: q dtype %d into kv dtype %d", who, d->q_dtype, d->kv_dtype);
+  if ((int64_t)num_tokens * (d->num_q_heads + 2 * d->num_kv_heads + 6) >= (int64_t)INT32_MAX)
+    return fail(PA_ERR_UNSUPPORTED, "%s: 2^31 head rows in one call", who);
   if (num_tokens == 0) return PA_OK;
   if (!q || !k || !v || (prep->cos_sin && !positions) || !slot_mapping || !q_out || !k_cache || !v_cache)
     return fail(PA_ERR_INVALID_ARG, "%s: NULL pointer", who);
@@ -673,6 +675,7 @@ int pa_norm_rope_write(const pa_cache_desc* d, const pa_qk_prep* prep, const voi
   p.head_dim = d->head_dim;
   p.block_size = d->block_size;
   p.num_slots = (int64_t)d->num_blocks * d->block_size;
+  p.bs_shift = d->block_size == 16 ? 4 : 5;
   p.k_scale = d->k_scale;
   p.v_scale = d->v_scale;
   if (d->kv_dtype == kFP8) {
@@ -691,6 +694,8 @@ int pa_cache_read(const pa_cache_desc* d, const int64_t* slot_mapping, int32_t n
   if (num_tokens < 0) return fail(PA_ERR_INVALID_ARG, "%s: num_tokens < 0", who);
   if (d->kv_dtype != kFP8 && d->kv_dtype != d->q_dtype)
     return fail(PA_ERR_UNSUPPORTED, "%s: kv dtype %d into q dtype %d", who, d->kv_dtype, d->q_dtype);
+  if ((int64_t)num_tokens * (d->num_kv_heads + 2) >= (int64_t)INT32_MAX)
+    return fail(PA_ERR_UNSUPPORTED, "%s: 2^31 head rows in one call", who);
   if (num_tokens == 0) return PA_OK;
   if (!slot_mapping || !k_cache || !v_cache || !k_out || !v_out)
     return fail(PA_ERR_INVALID_ARG, "%s: NULL pointer", who);
@@ -710,6 +715,7 @@ int pa_cache_read(const pa_cache_desc* d, const int64_t* slot_mapping, int32_t n
   p.head_dim = d->head_dim;
   p.block_size = d->block_size;
   p.num_slots = (int64_t)d->num_blocks * d->block_size;
+  p.bs_shift = d->block_size == 16 ? 4 : 5;
   p.k_scale = d->k_scale;
   p.v_scale = d->v_scale;
   if (d->kv_dtype == kFP8) {

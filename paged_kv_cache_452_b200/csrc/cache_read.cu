@@ -50,7 +50,7 @@ __device__ __forceinline__ void read_v_window(const CacheReadParams& p, int64_t 
     if (!live) continue;
     T* dst = reinterpret_cast<T*>(p.v_out) + (t * hkv + h) * D + d0;
     if (whole) {
-      const uint8_t* src = p.v_cache + ((s0 / p.block_size * hkv + h) * D + d0) * p.block_size + s0 % p.block_size;
+      const uint8_t* src = p.v_cache + (((s0 >> p.bs_shift) * hkv + h) * D + d0) * p.block_size + (s0 & (p.block_size - 1));
       uint4 raw[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) raw[e] = *reinterpret_cast<const uint4*>(src + (int64_t)e * p.block_size);
@@ -77,7 +77,7 @@ __device__ __forceinline__ void read_v_window(const CacheReadParams& p, int64_t 
         const int64_t slot = __ldg(p.slots + t + j);
         if (slot < 0 || slot >= p.num_slots) continue;
         const uint8_t* src =
-            p.v_cache + ((slot / p.block_size * hkv + h) * D + d0) * p.block_size + slot % p.block_size;
+            p.v_cache + (((slot >> p.bs_shift) * hkv + h) * D + d0) * p.block_size + (slot & (p.block_size - 1));
         float x[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[e] = dev::e4m3_to_f32(src[(int64_t)e * p.block_size]) * scale;
@@ -114,11 +114,11 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheReadPar
     const int64_t r = idx >= per_side ? idx - per_side : idx;
     row[j] = -1;
     if (idx < total) {
-      const int64_t th = r / CH;
-      const int64_t slot = __ldg(p.slots + th / hkv);
-      head[j] = (int)(th % hkv);
+      const uint32_t th = (uint32_t)(r / CH), t = dev::fdiv(th, p.heads);
+      const int64_t slot = __ldg(p.slots + t);
+      head[j] = (int)(th - t * hkv);
       if (slot >= 0 && slot < p.num_slots)
-        row[j] = ((slot / p.block_size * hkv + head[j]) * p.block_size + slot % p.block_size) * D + r % CH * VEC;
+        row[j] = (((slot >> p.bs_shift) * hkv + head[j]) * p.block_size + (slot & (p.block_size - 1))) * D + r % CH * VEC;
     }
   }
   if constexpr (!FP8) {
@@ -175,7 +175,9 @@ cudaError_t launch(const CacheReadParams& p, cudaStream_t stream) {
     vwin = (v + kThreads / (D / 4) - 1) / (kThreads / (D / 4));
   }
   if (rows + vwin > INT32_MAX) return cudaErrorNotSupported;
-  cache_read_kernel<T, D, FP8, VECS><<<(unsigned)(rows + vwin), kThreads, 0, stream>>>(p, (unsigned)rows);
+  CacheReadParams q = p;
+  q.heads = fast_div((uint32_t)p.num_kv_heads);
+  cache_read_kernel<T, D, FP8, VECS><<<(unsigned)(rows + vwin), kThreads, 0, stream>>>(q, (unsigned)rows);
   return cudaGetLastError();
 }
 

@@ -108,8 +108,8 @@ __device__ __forceinline__ void write_v_window(const NormRopeParams& p, int64_t 
       }
     }
     if (whole) {
-      const int64_t blk = s0 / p.block_size;
-      uint8_t* dst = p.v_cache + ((blk * hkv + h) * D + d0) * p.block_size + s0 % p.block_size;
+      const int64_t blk = s0 >> p.bs_shift;
+      uint8_t* dst = p.v_cache + ((blk * hkv + h) * D + d0) * p.block_size + (s0 & (p.block_size - 1));
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         *reinterpret_cast<uint4*>(dst + (int64_t)e * p.block_size) =
@@ -124,8 +124,8 @@ __device__ __forceinline__ void write_v_window(const NormRopeParams& p, int64_t 
           const int pos = __ldg(p.positions + t + j);
           if (pos < 0 || pos >= p.num_positions) continue;
         }
-        const int64_t blk = slot / p.block_size;
-        uint8_t* dst = p.v_cache + ((blk * hkv + h) * D + d0) * p.block_size + slot % p.block_size;
+        const int64_t blk = slot >> p.bs_shift;
+        uint8_t* dst = p.v_cache + ((blk * hkv + h) * D + d0) * p.block_size + (slot & (p.block_size - 1));
 #pragma unroll
         for (int e = 0; e < 4; ++e) dst[(int64_t)e * p.block_size] = (uint8_t)(code[e][j >> 2] >> (8 * (j & 3)));
       }
@@ -151,16 +151,20 @@ __global__ void __launch_bounds__(kThreads) norm_rope_write_kernel(const NormRop
     }
   }
   constexpr int LANES = D / 8;  // lanes of a head row
-  const int nh = hq + (FP8 ? 1 : 2) * hkv;
-  const int per_token = (nh + HEADS - 1) / HEADS;
-  const int64_t items = (int64_t)p.num_tokens * per_token;
-  const int64_t item = (int64_t)blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
+  // A token's row groups: its query heads', its keys', its values' (in e4m3
+  // the windows'), HEADS rows each: a group's rows are of one kind.
+  const uint32_t item = blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
+  const uint32_t items = (uint32_t)p.num_tokens * p.per_token.d;
   const bool live = item < items;  // whole warps stay for the norm's shuffles
-  const int64_t t = live ? item / per_token : 0;
-  const int h0 = live ? (int)(item % per_token) * HEADS : nh;
+  const uint32_t t = live ? dev::fdiv(item, p.per_token) : 0;
+  int g = live ? (int)(item - t * p.per_token.d) : 0;
+  const int gq = (hq + HEADS - 1) / HEADS, gk = (hkv + HEADS - 1) / HEADS;
+  const bool is_q = g < gq, is_v = g >= gq + gk;
+  g -= is_q ? 0 : is_v ? gq + gk : gq;
+  const int h0 = g * HEADS, nh = live ? (is_q ? hq : hkv) : 0;
   const int c = threadIdx.x % LANES;
   const int rot = p.rot_dim, half = rot >> 1;
-  const bool turns = 8 * c < rot;  // this lane's elements are rotated
+  const bool turns = 8 * c < rot && !is_v;  // this lane's elements are rotated
   // the lane's two chunks of four elements
   int a0 = 8 * c, a1 = 8 * c + 4;
   if (turns && !p.interleaved) {
@@ -171,64 +175,79 @@ __global__ void __launch_bounds__(kThreads) norm_rope_write_kernel(const NormRop
   const int64_t slot = __ldg(p.slots + t);
   using V = typename Four<T>::V;
   V raw[HEADS][2];
+  const T* rows = is_q   ? reinterpret_cast<const T*>(p.q) + t * p.q_stride
+                  : is_v ? reinterpret_cast<const T*>(p.v) + t * p.v_stride
+                         : reinterpret_cast<const T*>(p.k) + t * p.k_stride;
+  rows += h0 * D;
 #pragma unroll
   for (int j = 0; j < HEADS; ++j) {
-    const int h = h0 + j;
     raw[j][0] = raw[j][1] = V{};
-    if (h < nh) {
-      const T* row = h < hq ? reinterpret_cast<const T*>(p.q) + t * p.q_stride + (int64_t)h * D
-                   : h < hq + hkv ? reinterpret_cast<const T*>(p.k) + t * p.k_stride + (int64_t)(h - hq) * D
-                                  : reinterpret_cast<const T*>(p.v) + t * p.v_stride + (int64_t)(h - hq - hkv) * D;
-      raw[j][0] = load4(row + a0);
-      raw[j][1] = load4(row + a1);
+    if (h0 + j < nh) {
+      raw[j][0] = load4(rows + j * D + a0);
+      raw[j][1] = load4(rows + j * D + a1);
     }
   }
   const bool known = p.cos_sin == nullptr || (pos >= 0 && pos < p.num_positions);
   const bool in_pool = slot >= 0 && slot < p.num_slots;
-  const int64_t blk = in_pool ? slot / p.block_size : 0;
-  const int off = in_pool ? (int)(slot % p.block_size) : 0;
-  // cos and sin of the lane's four pairs
-  float cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
-  if (turns && known && p.cos_sin) {
+  // The norm's factor r is applied last (it commutes with weight and turn).
+  float w[2][4], cs[4], sn[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[0][i] = w[1][i] = 1.f;
+  const T* weight = reinterpret_cast<const T*>(is_q ? p.q_weight : p.k_weight);
+  const bool norm = !is_v && weight != nullptr;
+  if (norm) {
+    unpack(load4(weight + a0), w[0]);
+    unpack(load4(weight + a1), w[1]);
+  }
+  const bool turn = turns && known;  // (rot is 0 without a table)
+  if (turn) {
     unpack(__ldg(reinterpret_cast<const uint4*>(p.cos_sin + (int64_t)pos * rot + 4 * c)), cs);
     unpack(__ldg(reinterpret_cast<const uint4*>(p.cos_sin + (int64_t)pos * rot + half + 4 * c)), sn);
   }
+  T* dst;  // the group's first row in q_out or in a pool of T
+  uint8_t* dst8 = nullptr;
+  int64_t step = D;
+  if (is_q) {
+    dst = reinterpret_cast<T*>(p.q_out) + ((int64_t)t * hq + h0) * D;
+  } else {
+    const int64_t blk = in_pool ? slot >> p.bs_shift : 0;
+    const int off = in_pool ? (int)(slot & (p.block_size - 1)) : 0;
+    step = p.block_size * D;
+    const int64_t at = (blk * hkv + h0) * step + off * D;
+    dst = reinterpret_cast<T*>(is_v ? p.v_cache : p.k_cache) + at;
+    dst8 = p.k_cache + at;
+  }
 #pragma unroll
   for (int j = 0; j < HEADS; ++j) {
-    const int h = h0 + j;
-    const bool is_q = h < hq, is_v = h >= hq + hkv;
     float x[2][4];
     unpack(raw[j][0], x[0]);
     unpack(raw[j][1], x[1]);
-    const T* weight = reinterpret_cast<const T*>(is_q ? p.q_weight : p.k_weight);
-    // the whole warp takes part in the sums: its row groups may hold heads of
+    float r = 1.f;
+    // the whole warp takes part in the sums: its row groups may be of
     // different kinds
-    float ss = 0.f;
+    if (p.q_weight || p.k_weight) {
+      float ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) ss += x[0][i] * x[0][i] + x[1][i] * x[1][i];
+      for (int i = 0; i < 4; ++i) ss += x[0][i] * x[0][i] + x[1][i] * x[1][i];
 #pragma unroll
-    for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (!is_v && weight) {
-      const float inv = rsqrtf(ss * (1.f / D) + p.eps);
-      float w[2][4];
-      unpack(load4(weight + a0), w[0]);
-      unpack(load4(weight + a1), w[1]);
+      for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (norm) r = rsqrtf(ss * (1.f / D) + p.eps);
+    }
+    if (h0 + j >= nh || !known || (!is_q && !in_pool)) continue;
+    if (!is_v) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        x[0][i] *= inv * w[0][i];
-        x[1][i] *= inv * w[1][i];
+        x[0][i] *= w[0][i];
+        x[1][i] *= w[1][i];
       }
-    }
-    if (h >= nh || !known || (!is_q && !in_pool)) continue;
-    if (!is_v && turns) {
-      if (!p.interleaved) {
+      if (turn && !p.interleaved) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float a = x[0][i], b = x[1][i];
           x[0][i] = a * cs[i] - b * sn[i];
           x[1][i] = b * cs[i] + a * sn[i];
         }
-      } else {
+      } else if (turn) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float(&ch)[4] = x[i >> 1];
@@ -237,32 +256,32 @@ __global__ void __launch_bounds__(kThreads) norm_rope_write_kernel(const NormRop
           ch[2 * (i & 1) + 1] = b * cs[i] + a * sn[i];
         }
       }
+      if (norm) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[0][i] *= r;
+          x[1][i] *= r;
+        }
+      }
     }
-    if (is_q) {
-      T* dst = reinterpret_cast<T*>(p.q_out) + (t * hq + h) * D;
-      store4(dst + a0, x[0]);
-      store4(dst + a1, x[1]);
-      continue;
-    }
-    const int kvh = is_v ? h - hq - hkv : h - hq;
-    const int64_t row = ((blk * hkv + kvh) * p.block_size + off) * D;
-    if constexpr (!FP8) {
-      T* dst = reinterpret_cast<T*>(is_v ? p.v_cache : p.k_cache) + row;
-      store4(dst + a0, x[0]);
-      store4(dst + a1, x[1]);
+    if (!FP8 || is_q) {
+      store4(dst + j * step + a0, x[0]);
+      store4(dst + j * step + a1, x[1]);
     } else {
-      const float scale = p.k_head ? __ldg(p.k_head + kvh) : p.k_scale;
-      uint8_t* dst = p.k_cache + row;
-      *reinterpret_cast<uint32_t*>(dst + a0) = quant2(x[0][0], x[0][1], scale) | quant2(x[0][2], x[0][3], scale) << 16;
-      *reinterpret_cast<uint32_t*>(dst + a1) = quant2(x[1][0], x[1][1], scale) | quant2(x[1][2], x[1][3], scale) << 16;
+      const float scale = p.k_head ? __ldg(p.k_head + h0 + j) : p.k_scale;
+      uint8_t* out = dst8 + j * step;
+      *reinterpret_cast<uint32_t*>(out + a0) = quant2(x[0][0], x[0][1], scale) | quant2(x[0][2], x[0][3], scale) << 16;
+      *reinterpret_cast<uint32_t*>(out + a1) = quant2(x[1][0], x[1][1], scale) | quant2(x[1][2], x[1][3], scale) << 16;
     }
   }
 }
 
 template <typename T, int D, bool FP8, int HEADS>
 cudaError_t launch(const NormRopeParams& p, cudaStream_t stream) {
-  const int nh = p.num_q_heads + (FP8 ? 1 : 2) * p.num_kv_heads;
-  const int64_t items = (int64_t)p.num_tokens * ((nh + HEADS - 1) / HEADS);
+  NormRopeParams q = p;
+  const int gk = (p.num_kv_heads + HEADS - 1) / HEADS;
+  q.per_token = fast_div((uint32_t)((p.num_q_heads + HEADS - 1) / HEADS + (FP8 ? 1 : 2) * gk));
+  const int64_t items = (int64_t)p.num_tokens * q.per_token.d;
   const int64_t rows = (items + kThreads / (D / 8) - 1) / (kThreads / (D / 8));
   int64_t vwin = 0;
   if (FP8) {
@@ -270,9 +289,9 @@ cudaError_t launch(const NormRopeParams& p, cudaStream_t stream) {
     const int64_t v = ((int64_t)p.num_tokens + dev::kWindow - 1) / dev::kWindow * heads;
     vwin = (v + kThreads / (D / 4) - 1) / (kThreads / (D / 4));
   }
-  if (rows + vwin > INT32_MAX) return cudaErrorNotSupported;
+  if (items > INT32_MAX || rows + vwin > INT32_MAX) return cudaErrorNotSupported;
   norm_rope_write_kernel<T, D, FP8, HEADS>
-      <<<(unsigned)(rows + vwin), kThreads, 0, stream>>>(p, (unsigned)rows);
+      <<<(unsigned)(rows + vwin), kThreads, 0, stream>>>(q, (unsigned)rows);
   return cudaGetLastError();
 }
 

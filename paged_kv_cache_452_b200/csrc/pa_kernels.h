@@ -24,6 +24,19 @@ struct CacheWriteParams {
 };
 cudaError_t launch_cache_write(const CacheWriteParams& p, int in_dtype, int kv_dtype, cudaStream_t stream);
 
+// Division of n < 2^31 by a fixed d >= 1 as a multiplication: the quotient is
+// (umulhi(n, mul) + n) >> shift (round-up method: mul = floor(2^32 (2^shift -
+// d) / d) + 1 with shift = ceil(log2 d)).
+struct FastDiv {
+  uint32_t mul, shift, d;
+};
+inline FastDiv fast_div(uint32_t d) {
+  FastDiv f = {0, 0, d};
+  while (f.shift < 31 && (1u << f.shift) < d) ++f.shift;
+  f.mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << f.shift) - d)) / d + 1);
+  return f;
+}
+
 // pa_norm_rope_write: norms, rotation and cache write of a step's new rows.
 struct NormRopeParams {
   const uint8_t* q;
@@ -45,6 +58,8 @@ struct NormRopeParams {
   float k_scale, v_scale;
   const float* k_head;  // per-kv-head scales (device) or nullptr: k_scale / v_scale
   const float* v_head;
+  int32_t bs_shift;      // log2 of block_size
+  FastDiv per_token;     // the launch's: row groups of a token
 };
 cudaError_t launch_norm_rope_write(const NormRopeParams& p, int q_dtype, int kv_dtype, int num_sms,
                                    cudaStream_t stream);
@@ -61,6 +76,8 @@ struct CacheReadParams {
   float k_scale, v_scale;
   const float* k_head;  // per-kv-head scales (device) or nullptr: k_scale / v_scale
   const float* v_head;
+  int32_t bs_shift;      // log2 of block_size
+  FastDiv heads;         // num_kv_heads
 };
 cudaError_t launch_cache_read(const CacheReadParams& p, int q_dtype, int kv_dtype, int num_sms, cudaStream_t stream);
 

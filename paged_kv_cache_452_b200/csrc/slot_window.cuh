@@ -1,12 +1,17 @@
-// Windows of a slot list that a d-major e4m3 V pool is read and written by:
+// Index arithmetic of the row operators: division by a launch's constants, and
+// windows of a slot list that a d-major e4m3 V pool is read and written by:
 // 16 tokens whose slots fill an aligned half or whole block make one 16-byte
 // vector per element of head_dim, instead of 16 single bytes.
 #pragma once
 
 #include <stdint.h>
 
+#include "pa_kernels.h"
+
 namespace pa {
 namespace dev {
+
+__device__ __forceinline__ uint32_t fdiv(uint32_t n, const FastDiv& f) { return (__umulhi(n, f.mul) + n) >> f.shift; }
 
 constexpr int kWindow = 16;  // tokens; divides every block size
 
