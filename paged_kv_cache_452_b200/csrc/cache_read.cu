@@ -88,24 +88,24 @@ __device__ __forceinline__ void read_v_window(const CacheReadParams& p, int64_t 
 }
 
 // T: element type of the rows; FP8: an e4m3 pool; VECS: 16-byte vectors of the
-// output per thread.  Blocks from `row_blocks` on read e4m3 V.
+// output per thread.  The first `v_blocks` blocks read e4m3 V.
 template <typename T, int D, bool FP8, int VECS>
-__global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheReadParams p, unsigned row_blocks) {
+__global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheReadParams p, unsigned v_blocks) {
   dev::grid_dep_wait();
   dev::grid_dep_launch();
   const int hkv = p.num_kv_heads;
   if constexpr (FP8) {
-    if (blockIdx.x >= row_blocks) {
+    if (blockIdx.x < v_blocks) {
       const int64_t heads = (hkv * (D / 4) + 31) / 32 * (32 / (D / 4));
       const int64_t items = ((int64_t)p.num_tokens + dev::kWindow - 1) / dev::kWindow * heads;
-      const int64_t item = (int64_t)(blockIdx.x - row_blocks) * (kThreads / (D / 4)) + threadIdx.x / (D / 4);
+      const int64_t item = (int64_t)blockIdx.x * (kThreads / (D / 4)) + threadIdx.x / (D / 4);
       if (item < items) read_v_window<T, D>(p, item);  // whole warps: items are a multiple of a warp's
       return;
     }
   }
   constexpr int VEC = 16 / sizeof(T), CH = D / VEC;  // elements of a vector, vectors of a row
   const int64_t per_side = (int64_t)p.num_tokens * hkv * CH, total = (FP8 ? 1 : 2) * per_side;
-  const int64_t i0 = (int64_t)blockIdx.x * (kThreads * VECS) + threadIdx.x;
+  const int64_t i0 = (int64_t)(blockIdx.x - (FP8 ? v_blocks : 0u)) * (kThreads * VECS) + threadIdx.x;
   int64_t row[VECS];  // element of the pool, -1: none
   int head[VECS];
 #pragma unroll
@@ -177,7 +177,7 @@ cudaError_t launch(const CacheReadParams& p, cudaStream_t stream) {
   if (rows + vwin > INT32_MAX) return cudaErrorNotSupported;
   CacheReadParams q = p;
   q.heads = fast_div((uint32_t)p.num_kv_heads);
-  cache_read_kernel<T, D, FP8, VECS><<<(unsigned)(rows + vwin), kThreads, 0, stream>>>(q, (unsigned)rows);
+  cache_read_kernel<T, D, FP8, VECS><<<(unsigned)(rows + vwin), kThreads, 0, stream>>>(q, (unsigned)vwin);
   return cudaGetLastError();
 }
 

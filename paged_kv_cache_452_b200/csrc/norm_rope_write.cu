@@ -21,7 +21,7 @@
 // reduces over the row's lanes.  A row group takes a few head rows of one
 // token, all loads first and kept as they came, and reads the token's cos and
 // sin once.  e4m3 V, whose pool is d-major, goes by windows of 16 tokens: a
-// lane takes four elements of 16 rows and stores 16 bytes per element where
+// lane takes two elements of 16 rows and stores 16 bytes per element where
 // the window's slots fill an aligned part of a block (single bytes otherwise).
 #include <cuda_runtime.h>
 
@@ -50,6 +50,19 @@ __device__ __forceinline__ void unpack(const uint4& v, float (&x)[4]) {
   x[2] = __uint_as_float(v.z);
   x[3] = __uint_as_float(v.w);
 }
+// The same as two packed pairs.
+__device__ __forceinline__ void unpack2(const uint2& v, uint64_t (&x)[2]) {
+  x[0] = dev::f2(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u));
+  x[1] = dev::f2(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u));
+}
+__device__ __forceinline__ void unpack2(const uint4& v, uint64_t (&x)[2]) {
+  x[0] = dev::f2(__uint_as_float(v.x), __uint_as_float(v.y));
+  x[1] = dev::f2(__uint_as_float(v.z), __uint_as_float(v.w));
+}
+__device__ __forceinline__ void split2(const uint64_t (&x)[2], float (&y)[4]) {
+  dev::f2_split(x[0], y[0], y[1]);
+  dev::f2_split(x[1], y[2], y[3]);
+}
 template <typename T>
 __device__ __forceinline__ typename Four<T>::V load4(const T* p) {
   return *reinterpret_cast<const typename Four<T>::V*>(p);
@@ -66,18 +79,16 @@ __device__ __forceinline__ uint32_t quant2(float a, float b, float scale) {
   return dev::e4m3x2_from_f32(__fdiv_rn(a, scale), __fdiv_rn(b, scale));
 }
 
-// e4m3 V of one window of tokens and one kv head per D / 4 lanes.
+// e4m3 V of one window of tokens and one kv head per D / 2 lanes.
 template <typename T, int D>
 __device__ __forceinline__ void write_v_window(const NormRopeParams& p, int64_t item) {
-  constexpr int LANES = D / 4;
+  constexpr int LANES = D / 2;  // whole warps
   const int hkv = p.num_kv_heads;
-  const int64_t heads = (hkv * LANES + 31) / 32 * (32 / LANES);  // heads per window, in whole warps
-  const int64_t win = item / heads;
-  const int h = (int)(item % heads);
-  const int d0 = 4 * (threadIdx.x % LANES);
-  const bool live = h < hkv;
-  const float scale = !live ? 1.f : p.v_head ? __ldg(p.v_head + h) : p.v_scale;
-  const int64_t end = dev::window_start(p.slots, p.num_tokens, win + 1);
+  const uint32_t win = dev::fdiv((uint32_t)item, p.heads);
+  const int h = (int)((uint32_t)item - win * hkv);
+  const int d0 = 2 * (threadIdx.x % LANES);
+  const float scale = p.v_head ? __ldg(p.v_head + h) : p.v_scale;
+  const int64_t end = dev::window_start(p.slots, p.num_tokens, (int64_t)win + 1);
   for (int64_t t = dev::window_start(p.slots, p.num_tokens, win); t < end; t += dev::kWindow) {
     const int n = (int)min((int64_t)dev::kWindow, end - t);
     int64_t s0;
@@ -87,33 +98,40 @@ __device__ __forceinline__ void write_v_window(const NormRopeParams& p, int64_t 
       const int pos = (threadIdx.x & 31) < n ? __ldg(p.positions + t + (threadIdx.x & 31)) : 0;
       whole = whole && __all_sync(0xffffffffu, pos >= 0 && pos < p.num_positions);
     }
-    typename Four<T>::V raw[dev::kWindow];
-    if (live) {
+    uint32_t code[2][4];  // [element][4 tokens]
+    const T* src = reinterpret_cast<const T*>(p.v) + t * p.v_stride + h * D + d0;
+    float2 x[dev::kWindow];
 #pragma unroll
-      for (int j = 0; j < dev::kWindow; ++j)
-        raw[j] = load4(reinterpret_cast<const T*>(p.v) + (t + min(j, n - 1)) * p.v_stride + (int64_t)h * D + d0);
+    for (int j = 0; j < dev::kWindow; ++j) {
+      if constexpr (sizeof(T) == 4) {
+        x[j] = *reinterpret_cast<const float2*>(src + min(j, n - 1) * p.v_stride);
+      } else {  // kept as it came: the pair's upper element in y
+        x[j].x = __uint_as_float(*reinterpret_cast<const uint32_t*>(src + min(j, n - 1) * p.v_stride));
+      }
     }
-    if (!live) continue;
-    uint32_t code[4][4];  // [element][4 tokens]
 #pragma unroll
     for (int j = 0; j < dev::kWindow; j += 2) {
-      float a[4], b[4];
-      unpack(raw[j], a);
-      unpack(raw[j + 1], b);
+      if constexpr (sizeof(T) != 4) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t two = quant2(a[e], b[e], scale);
-        if (j & 2) code[e][j >> 2] |= two << 16;
-        else code[e][j >> 2] = two;
+        for (int k = j; k < j + 2; ++k) {
+          const uint32_t w = __float_as_uint(x[k].x);
+          x[k] = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+        }
+      }
+      const uint32_t lo = quant2(x[j].x, x[j + 1].x, scale), hi = quant2(x[j].y, x[j + 1].y, scale);
+      if (j & 2) {
+        code[0][j >> 2] |= lo << 16;
+        code[1][j >> 2] |= hi << 16;
+      } else {
+        code[0][j >> 2] = lo;
+        code[1][j >> 2] = hi;
       }
     }
     if (whole) {
-      const int64_t blk = s0 >> p.bs_shift;
-      uint8_t* dst = p.v_cache + ((blk * hkv + h) * D + d0) * p.block_size + (s0 & (p.block_size - 1));
+      uint8_t* dst = p.v_cache + (((s0 >> p.bs_shift) * hkv + h) * D + d0) * p.block_size + (s0 & (p.block_size - 1));
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        *reinterpret_cast<uint4*>(dst + (int64_t)e * p.block_size) =
-            make_uint4(code[e][0], code[e][1], code[e][2], code[e][3]);
+      for (int e = 0; e < 2; ++e)
+        *reinterpret_cast<uint4*>(dst + e * p.block_size) = make_uint4(code[e][0], code[e][1], code[e][2], code[e][3]);
     } else {
 #pragma unroll
       for (int j = 0; j < dev::kWindow; ++j) {
@@ -124,36 +142,37 @@ __device__ __forceinline__ void write_v_window(const NormRopeParams& p, int64_t 
           const int pos = __ldg(p.positions + t + j);
           if (pos < 0 || pos >= p.num_positions) continue;
         }
-        const int64_t blk = slot >> p.bs_shift;
-        uint8_t* dst = p.v_cache + ((blk * hkv + h) * D + d0) * p.block_size + (slot & (p.block_size - 1));
+        uint8_t* dst =
+            p.v_cache + (((slot >> p.bs_shift) * hkv + h) * D + d0) * p.block_size + (slot & (p.block_size - 1));
 #pragma unroll
-        for (int e = 0; e < 4; ++e) dst[(int64_t)e * p.block_size] = (uint8_t)(code[e][j >> 2] >> (8 * (j & 3)));
+        for (int e = 0; e < 2; ++e) dst[e * p.block_size] = (uint8_t)(code[e][j >> 2] >> (8 * (j & 3)));
       }
     }
   }
 }
 
-// T: element type of the new rows; FP8: an e4m3 pool; HEADS: head rows of one
-// token per row group.  Blocks from `row_blocks` on write e4m3 V.
-template <typename T, int D, bool FP8, int HEADS>
-__global__ void __launch_bounds__(kThreads) norm_rope_write_kernel(const NormRopeParams p, unsigned row_blocks) {
+// FULL: every head is normed and rotated over its whole width in halves (what
+// most calls ask for): issue slots bound the general form (at 4344 tokens it
+// took 23 us, 70% of them busy), so this one multiplies weights and angles
+// together once per group, works on pairs of elements and moves V rows as they
+// are.
+template <typename T, int D, bool FP8, int HEADS, bool FULL>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) norm_rope_write_kernel(const NormRopeParams p, unsigned v_blocks) {
   dev::grid_dep_wait();
   dev::grid_dep_launch();
   const int hq = p.num_q_heads, hkv = p.num_kv_heads;
   if constexpr (FP8) {
-    if (blockIdx.x >= row_blocks) {
-      constexpr int PER = kThreads / (D / 4);
-      const int64_t heads = (hkv * (D / 4) + 31) / 32 * (32 / (D / 4));
-      const int64_t items = ((int64_t)p.num_tokens + dev::kWindow - 1) / dev::kWindow * heads;
-      const int64_t item = (int64_t)(blockIdx.x - row_blocks) * PER + threadIdx.x / (D / 4);
-      if (item < items) write_v_window<T, D>(p, item);  // whole warps: items are a multiple of a warp's
+    if (blockIdx.x < v_blocks) {
+      const int64_t items = ((int64_t)p.num_tokens + dev::kWindow - 1) / dev::kWindow * hkv;
+      const int64_t item = (int64_t)blockIdx.x * (kThreads / (D / 2)) + threadIdx.x / (D / 2);
+      if (item < items) write_v_window<T, D>(p, item);
       return;
     }
   }
   constexpr int LANES = D / 8;  // lanes of a head row
   // A token's row groups: its query heads', its keys', its values' (in e4m3
   // the windows'), HEADS rows each: a group's rows are of one kind.
-  const uint32_t item = blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
+  const uint32_t item = (blockIdx.x - (FP8 ? v_blocks : 0u)) * (kThreads / LANES) + threadIdx.x / LANES;
   const uint32_t items = (uint32_t)p.num_tokens * p.per_token.d;
   const bool live = item < items;  // whole warps stay for the norm's shuffles
   const uint32_t t = live ? dev::fdiv(item, p.per_token) : 0;
@@ -167,7 +186,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_write_kernel(const NormRop
   const bool turns = 8 * c < rot && !is_v;  // this lane's elements are rotated
   // the lane's two chunks of four elements
   int a0 = 8 * c, a1 = 8 * c + 4;
-  if (turns && !p.interleaved) {
+  if (FULL ? !is_v : turns && !p.interleaved) {
     a0 = 4 * c;
     a1 = half + 4 * c;
   }
@@ -189,6 +208,77 @@ __global__ void __launch_bounds__(kThreads) norm_rope_write_kernel(const NormRop
   }
   const bool known = p.cos_sin == nullptr || (pos >= 0 && pos < p.num_positions);
   const bool in_pool = slot >= 0 && slot < p.num_slots;
+  if constexpr (FULL) {
+    if (!live || !known || (!is_q && !in_pool)) return;  // whole row groups: the sums below stay within one
+    const uint32_t group = LANES == 32 ? 0xffffffffu : ((1u << LANES) - 1u) << (threadIdx.x & 31 & ~(LANES - 1));
+    const int step = is_q ? D : p.block_size * D;
+    const int64_t at = is_q ? ((int64_t)t * hq + h0) * D
+                            : ((slot >> p.bs_shift) * hkv + h0) * step + (slot & (p.block_size - 1)) * D;
+    if (is_v) {
+      T* out = reinterpret_cast<T*>(p.v_cache) + at + a0;
+#pragma unroll
+      for (int j = 0; j < HEADS; ++j) {
+        if (h0 + j >= nh) break;
+        *reinterpret_cast<V*>(out + j * step) = raw[j][0];
+        *reinterpret_cast<V*>(out + j * step + 4) = raw[j][1];
+      }
+      return;
+    }
+    const T* weight = reinterpret_cast<const T*>(is_q ? p.q_weight : p.k_weight);
+    uint64_t w0[2], w1[2], c[2], s[2], ac[2], bs[2], bc[2], as[2];
+    unpack2(load4(weight + a0), w0);
+    unpack2(load4(weight + a1), w1);
+    unpack2(__ldg(reinterpret_cast<const uint4*>(p.cos_sin + (int64_t)pos * D + a0)), c);
+    unpack2(__ldg(reinterpret_cast<const uint4*>(p.cos_sin + (int64_t)pos * D + a1)), s);
+    const uint64_t minus = dev::f2(-1.f, -1.f);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      ac[i] = dev::mul2(w0[i], c[i]);
+      as[i] = dev::mul2(w0[i], s[i]);
+      bc[i] = dev::mul2(w1[i], c[i]);
+      bs[i] = dev::mul2(dev::mul2(w1[i], s[i]), minus);
+    }
+    T* out = reinterpret_cast<T*>(is_q ? p.q_out : p.k_cache) + at;
+    uint8_t* out8 = p.k_cache + at;
+#pragma unroll
+    for (int j = 0; j < HEADS; ++j) {
+      if (h0 + j >= nh) break;
+      uint64_t a[2], b[2];
+      unpack2(raw[j][0], a);
+      unpack2(raw[j][1], b);
+      uint64_t q2 = dev::mul2(a[0], a[0]);
+      q2 = dev::fma2(a[1], a[1], q2);
+      q2 = dev::fma2(b[0], b[0], q2);
+      q2 = dev::fma2(b[1], b[1], q2);
+      float ss, odd;
+      dev::f2_split(q2, ss, odd);
+      ss += odd;
+#pragma unroll
+      for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(group, ss, o);
+      const float r = rsqrtf(ss * (1.f / D) + p.eps);
+      const uint64_t r2 = dev::f2(r, r);
+      uint64_t ya[2], yb[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        ya[i] = dev::mul2(dev::fma2(a[i], ac[i], dev::mul2(b[i], bs[i])), r2);
+        yb[i] = dev::mul2(dev::fma2(b[i], bc[i], dev::mul2(a[i], as[i])), r2);
+      }
+      float x[2][4];
+      split2(ya, x[0]);
+      split2(yb, x[1]);
+      if (!FP8 || is_q) {
+        store4(out + j * step + a0, x[0]);
+        store4(out + j * step + a1, x[1]);
+      } else {
+        const float scale = p.k_head ? __ldg(p.k_head + h0 + j) : p.k_scale;
+        *reinterpret_cast<uint32_t*>(out8 + j * step + a0) =
+            quant2(x[0][0], x[0][1], scale) | quant2(x[0][2], x[0][3], scale) << 16;
+        *reinterpret_cast<uint32_t*>(out8 + j * step + a1) =
+            quant2(x[1][0], x[1][1], scale) | quant2(x[1][2], x[1][3], scale) << 16;
+      }
+    }
+    return;
+  }
   // The norm's factor r is applied last (it commutes with weight and turn).
   float w[2][4], cs[4], sn[4];
 #pragma unroll
@@ -206,7 +296,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_write_kernel(const NormRop
   }
   T* dst;  // the group's first row in q_out or in a pool of T
   uint8_t* dst8 = nullptr;
-  int64_t step = D;
+  int step = D;
   if (is_q) {
     dst = reinterpret_cast<T*>(p.q_out) + ((int64_t)t * hq + h0) * D;
   } else {
@@ -276,7 +366,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_write_kernel(const NormRop
   }
 }
 
-template <typename T, int D, bool FP8, int HEADS>
+template <typename T, int D, bool FP8, int HEADS, bool FULL>
 cudaError_t launch(const NormRopeParams& p, cudaStream_t stream) {
   NormRopeParams q = p;
   const int gk = (p.num_kv_heads + HEADS - 1) / HEADS;
@@ -285,13 +375,13 @@ cudaError_t launch(const NormRopeParams& p, cudaStream_t stream) {
   const int64_t rows = (items + kThreads / (D / 8) - 1) / (kThreads / (D / 8));
   int64_t vwin = 0;
   if (FP8) {
-    const int64_t heads = (p.num_kv_heads * (D / 4) + 31) / 32 * (32 / (D / 4));
-    const int64_t v = ((int64_t)p.num_tokens + dev::kWindow - 1) / dev::kWindow * heads;
-    vwin = (v + kThreads / (D / 4) - 1) / (kThreads / (D / 4));
+    const int64_t v = ((int64_t)p.num_tokens + dev::kWindow - 1) / dev::kWindow * p.num_kv_heads;
+    vwin = (v + kThreads / (D / 2) - 1) / (kThreads / (D / 2));
+    q.heads = fast_div((uint32_t)p.num_kv_heads);
   }
   if (items > INT32_MAX || rows + vwin > INT32_MAX) return cudaErrorNotSupported;
-  norm_rope_write_kernel<T, D, FP8, HEADS>
-      <<<(unsigned)(rows + vwin), kThreads, 0, stream>>>(q, (unsigned)rows);
+  norm_rope_write_kernel<T, D, FP8, HEADS, FULL>
+      <<<(unsigned)(rows + vwin), kThreads, 0, stream>>>(q, (unsigned)vwin);
   return cudaGetLastError();
 }
 
@@ -300,7 +390,10 @@ cudaError_t launch(const NormRopeParams& p, cudaStream_t stream) {
 template <typename T, int D, bool FP8>
 cudaError_t launch_h(const NormRopeParams& p, int num_sms, cudaStream_t stream) {
   const int64_t rows = (int64_t)p.num_tokens * (p.num_q_heads + 2 * p.num_kv_heads);
-  return rows * (D / 8) <= (int64_t)num_sms * 2048 ? launch<T, D, FP8, 1>(p, stream) : launch<T, D, FP8, 4>(p, stream);
+  const bool full = p.cos_sin && p.rot_dim == D && !p.interleaved && p.q_weight && p.k_weight;
+  if (rows * (D / 8) <= (int64_t)num_sms * 2048)
+    return full ? launch<T, D, FP8, 1, true>(p, stream) : launch<T, D, FP8, 1, false>(p, stream);
+  return full ? launch<T, D, FP8, 4, true>(p, stream) : launch<T, D, FP8, 4, false>(p, stream);
 }
 
 template <typename T, bool FP8>

@@ -60,6 +60,7 @@ struct NormRopeParams {
   const float* v_head;
   int32_t bs_shift;      // log2 of block_size
   FastDiv per_token;     // the launch's: row groups of a token
+  FastDiv heads;         // the launch's: num_kv_heads
 };
 cudaError_t launch_norm_rope_write(const NormRopeParams& p, int q_dtype, int kv_dtype, int num_sms,
                                    cudaStream_t stream);
