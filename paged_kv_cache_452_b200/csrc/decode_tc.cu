@@ -242,7 +242,7 @@ __device__ __forceinline__ void fused_write(const DecodeParams& p, uint8_t* st, 
 // last block to its first: the nearest keys carry the largest weights, so the
 // softmax reference that a piece's first tile sets serves the others (from the
 // first block on it moved, and rescaled the outputs, at almost every tile:
-// 272 us instead of 257 on 32 contexts of up to 32768 keys in e4m3).
+// 15 us of 272 on 32 contexts of up to 32768 keys in e4m3).
 // p.num_kv_heads counts cut groups (mod.sub of them share a pool
 // kv head), so that any group takes this kernel.
 template <int KV, int D, int BS, bool MOD>
@@ -386,10 +386,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<KV>())
       const bool opens = i == skip || t == wbeg;
       int end = nb + skip;  // blocks of the row up to its context's end
       if constexpr (MOD) {
-        const Span sp = seq_span<BS>(p, s, min(__ldg(p.rows.seq_lens + s), p.max_blocks * BS));
         if (p.mod.slopes) i = nb - 1 - i;
-        if (i >= sp.np) i += sp.gap;
-        end += sp.gap;
+        if (p.mod.window > 0) {  // (no gap without one, and no load on the way to the table entry)
+          const Span sp = seq_span<BS>(p, s, min(__ldg(p.rows.seq_lens + s), p.max_blocks * BS));
+          if (i >= sp.np) i += sp.gap;
+          end += sp.gap;
+        }
       }
       d.blk = __ldg(p.block_tables + (int64_t)s * p.max_blocks + i);
       if (d.blk < 0 || d.blk >= p.num_blocks) {  // bad table entry: flag, read block 0
@@ -429,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<KV>())
     // one copy per lane, all in the same instructions: lanes 0..NCH-1 take
     // the K tile's 128-byte column boxes, the next lanes the V tile, the
     // next one the query rows
-    const int ph = MOD ? hj / p.mod.sub : hj;  // kv head of the pool
+    const int ph = MOD && p.mod.sub > 1 ? hj / p.mod.sub : hj;  // kv head of the pool (a division only where the group is cut)
     const int32_t krow = (blkj * pool_heads + ph) * BS;
     if (lane < C::NCH) {
       dev::tma_load_2d(st + lane * BS * 128, &tm_k, lane * (128 / C::ELEM), krow, &full[st_i], pol);
@@ -476,11 +478,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<KV>())
     const int skip = seq_skip(p, pfx, s);  // tile a holds block `skip` of the row
     int row = 0, len = 0;
     // this kv head's softmax and output scales (e4m3 per-head dequantisation)
-    const int ph = MOD ? h / p.mod.sub : h;
+    const int ph = MOD && p.mod.sub > 1 ? h / p.mod.sub : h;
     const float khs = p.k_head ? __ldg(p.k_head + ph) : 1.f;
     const float sl2 = p.k_head ? p.scale_log2 * khs : p.scale_log2;
     const float osc = p.v_head ? p.out_scale * __ldg(p.v_head + ph) : p.out_scale;
     Span span{0, 0, 0, 0};
+    const float kf0 = (float)(C::FP8 ? kperm(g) : g), kf1 = (float)(C::FP8 ? kperm(g + 8) : g + 8);  // this thread's keys of a tile
     float cap_in = 0.f, sp0 = 0.f, sp1 = 0.f;  // the piece's cap factor and this thread's columns' slopes (log2 units)
     if constexpr (MOD) {
       span = seq_span<BS>(p, s, min(__ldg(p.rows.seq_lens + s), p.max_blocks * BS));
@@ -549,26 +552,34 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<KV>())
       float bias0 = 0.f, bias1 = 0.f;  // of the tile's first key
       bool edge = false;
       if constexpr (MOD) {
-        if (p.mod.slopes) key0 = (b - 1 - tile) * BS;
-        if (key0 >= span.np * BS) key0 += span.gap * BS;
-        const float dist = (float)(len - 1 - key0);
-        bias0 = -sp0 * dist;
-        bias1 = -sp1 * dist;
-        edge = key0 + BS > len || (key0 < span.lo && key0 + BS > span.pfx);
-        // keys of the tile outside the prefix and the window: their weights are
-        // 0, but 0 * NaN would poison P V, so their V rows are zeroed
-        const int z0 = max(span.pfx, key0) - key0, z1 = min(span.lo, key0 + BS) - key0;
-        if (z0 < z1) {
+        const int li = p.mod.slopes ? b - 1 - tile : tile - a;  // the tile's place among its blocks
+        key0 = (li >= span.np ? li + span.gap : li) * BS;
+        if (p.mod.slopes) {
+          const float dist = (float)(len - 1 - key0);
+          bias0 = -sp0 * dist;
+          bias1 = -sp1 * dist;
+        }
+        // only the last tile, and under a window those at the prefix's end and
+        // the window's start, hold keys that are not seen
+        edge = li == nb - 1 || (span.lo > 0 && (unsigned)(li - span.np + 1) < 2u);
+        if (edge) {
+          // their weights are 0, but 0 * NaN would poison P V: their V rows
+          // (the prefix's and window's outside, and past the context) are zeroed
           uint8_t* vt = ring + (size_t)stage * STAGE + C::TILE;
-          if constexpr (!C::FP8) {
-            for (int i = lane; i < (z1 - z0) * C::NCH * 8; i += 32) {
-              const int key = z0 + i / (C::NCH * 8), rest = i % (C::NCH * 8);
-              *reinterpret_cast<uint4*>(vt + (rest >> 3) * (BS * 128) + key * 128 + (rest & 7) * 16) =
-                  make_uint4(0, 0, 0, 0);
+          auto zero = [&](int z0, int z1) {
+            if (z0 >= z1) return;
+            if constexpr (!C::FP8) {
+              for (int i = lane; i < (z1 - z0) * C::NCH * 8; i += 32) {
+                const int key = z0 + i / (C::NCH * 8), rest = i % (C::NCH * 8);
+                *reinterpret_cast<uint4*>(vt + (rest >> 3) * (BS * 128) + key * 128 + (rest & 7) * 16) =
+                    make_uint4(0, 0, 0, 0);
+              }
+            } else {
+              for (int i = lane; i < D * (z1 - z0); i += 32) vt[(i / (z1 - z0)) * BS + z0 + i % (z1 - z0)] = 0;
             }
-          } else {
-            for (int i = lane; i < D * (z1 - z0); i += 32) vt[(i / (z1 - z0)) * BS + z0 + i % (z1 - z0)] = 0;
-          }
+          };
+          zero(max(span.pfx, key0) - key0, min(span.lo, key0 + BS) - key0);
+          zero(len - key0, BS);
           __syncwarp();
         }
       } else if (p.k_new != nullptr && tile == b - 1) {
@@ -578,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<KV>())
         fused_write<C>(p, ring + (size_t)stage * STAGE, s, h, row, len, len - 1 - key0, skip + nb, lane);
         __syncwarp();
       }
-      if (len - key0 < BS) {
+      if (!MOD && len - key0 < BS) {
         // Slots past the context hold whatever the pool last stored there
         // (possibly NaN/Inf bit patterns): their scores are masked to -inf,
         // but 0 * NaN would still poison P*V, so their V rows are zeroed.
@@ -638,19 +649,23 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<KV>())
         const int r1 = key0 + 16 * km + (C::FP8 ? kperm(g + 8) : g + 8);
         if constexpr (MOD) {
           float x[4] = {acc0[0] + acc1[0], acc0[1] + acc1[1], acc0[2] + acc1[2], acc0[3] + acc1[3]};
-          float mul = sl2;
           if (p.mod.cap_out > 0.f) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[i] = dev::capped(x[i], cap_in, p.mod.cap_out);
-            mul = 1.f;
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] *= sl2;
           }
-          // minus slope times distance: the tile's first key's, and the key's
-          // place in the tile
-          const float k0 = (float)(r0 - key0), k1 = (float)(r1 - key0);
-          sc[km][0] = fmaf(x[0], mul, fmaf(sp0, k0, bias0));
-          sc[km][1] = fmaf(x[1], mul, fmaf(sp1, k0, bias1));
-          sc[km][2] = fmaf(x[2], mul, fmaf(sp0, k1, bias0));
-          sc[km][3] = fmaf(x[3], mul, fmaf(sp1, k1, bias1));
+          if (p.mod.slopes) {
+            // minus slope times distance: the tile's first key's, and the
+            // key's place in the tile
+            x[0] += fmaf(sp0, kf0 + 16.f * km, bias0);
+            x[1] += fmaf(sp1, kf0 + 16.f * km, bias1);
+            x[2] += fmaf(sp0, kf1 + 16.f * km, bias0);
+            x[3] += fmaf(sp1, kf1 + 16.f * km, bias1);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sc[km][i] = x[i];
           if (edge) {  // (uniform) keys past the context, or between the prefix and the window
             const bool v0 = r0 < len && (r0 >= span.lo || r0 < span.pfx), v1 = r1 < len && (r1 >= span.lo || r1 < span.pfx);
             if (!v0) sc[km][0] = sc[km][1] = -INFINITY;
