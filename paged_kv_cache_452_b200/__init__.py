@@ -138,16 +138,15 @@ def _call(who, dev, stream, f, *args):
     current stream if none is given."""
     if dev < 0:
         raise PaError(1, f"{who}: tensors must be on a CUDA device")
-    was = torch.cuda.current_device()
-    if was != dev:
-        torch.cuda.set_device(dev)
-    try:
-        rc = f(*args, _stream(stream))
-        if rc != 0:
-            raise PaError(rc, f"{who}: {lib().pa_last_error().decode()}")
-    finally:
-        if was != dev:
-            torch.cuda.set_device(was)
+    # (a Stream object costs 3 us to make, a third of a small call)
+    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    if torch.cuda.current_device() == dev:
+        rc = f(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            rc = f(*args, handle)
+    if rc != 0:
+        raise PaError(rc, f"{who}: {lib().pa_last_error().decode()}")
 
 
 def _parameter(who, name, t, dtypes, dims):

@@ -4,10 +4,12 @@
 //
 // Row i of a sequence sees key j if j < prefix, or j <= i and (window) i - j <
 // window; its score is cap * tanh(scale q k / cap) - slope |i - j|, all in
-// fp32.  A CTA takes kPairs (position, head) pairs of one sequence and kv
-// head, so that a key row read serves several queries; its eight warps take
-// the visible 16-key tiles in turn, each with its own online softmax, and
-// merge at the end.  Bound: latency for short contexts, FMA issue for long.
+// fp32.  A CTA takes NP (position, head) pairs of one sequence and kv head, so
+// that a key row read serves several queries; its warps take the visible
+// 16-key tiles in turn, each with its own online softmax, and merge at the
+// end.  With one pair per CTA (few rows: a chain of loads per tile is what
+// bounds it) there are 16 warps and a tile's K and V are loaded together.
+// Bound: latency for short contexts, FMA issue for long.
 #include <cuda_runtime.h>
 
 #include "pa_device.cuh"
@@ -16,7 +18,6 @@
 namespace pa {
 namespace {
 
-constexpr int kWarps = 8;
 constexpr int kTile = 16;  // keys of a tile: block sizes are multiples of it
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -46,10 +47,15 @@ __device__ __forceinline__ void load_elems(const uint8_t* base, int64_t idx, flo
 template <int KV> struct KElem { using T = float; };
 template <> struct KElem<kFP8> { using T = uint8_t; };
 
+// (fp32 rows of 128 elements ahead need the registers of eight warps)
 template <int KV, int D, int NP>
-__global__ void __launch_bounds__(kWarps * 32) attn_biased_simt_kernel(const BiasedSimtParams bp) {
+constexpr int warps_of() { return NP == 1 && (D == 64 || KV == kFP8) ? 16 : 8; }
+
+template <int KV, int D, int NP>
+__global__ void __launch_bounds__(warps_of<KV, D, NP>() * 32) attn_biased_simt_kernel(const BiasedSimtParams bp) {
   dev::grid_dep_wait();
   const SimtParams& p = bp.a;
+  constexpr int kWarps = warps_of<KV, D, NP>();
   constexpr int E = D / 8;    // elements of a key row per lane (8 lanes a key, 4 keys a pass)
   constexpr int DV = D / 32;  // elements of the output per lane
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -112,11 +118,39 @@ __global__ void __launch_bounds__(kWarps * 32) attn_biased_simt_kernel(const Bia
     }
     const int off = key0 % bs;
     const int64_t kb = ((blk * hkv + kvh) * bs + off) * D;
+    // key 4 j + kg of the tile, and this lane's V elements (with several pairs
+    // loaded where they are used: registers)
+    constexpr bool kAhead = NP == 1;
+    float kall[kAhead ? 4 : 1][E];
+    float2 vall[kAhead && KV != kFP8 ? kTile : 1][DV / 2];
+    uint4 raw[KV == kFP8 ? DV : 1];
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        load_elems<typename KElem<KV>::T, E>(p.k_cache, kb + (4 * j + kg) * D + sub * E, kall[j]);
+      if constexpr (KV != kFP8) {
+#pragma unroll
+        for (int k = 0; k < kTile; ++k)
+#pragma unroll
+          for (int e = 0; e < DV / 2; ++e)
+            vall[k][e] = __ldg(reinterpret_cast<const float2*>(p.v_cache) + (kb + k * D + lane * DV) / 2 + e);
+      }
+    }
+    if constexpr (KV == kFP8) {
+#pragma unroll
+      for (int e = 0; e < DV; ++e)
+        raw[e] = __ldg(reinterpret_cast<const uint4*>(p.v_cache + ((blk * hkv + kvh) * D + lane * DV + e) * bs + off));
+    }
     float sc[NP][4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {  // key 4 j + kg of the tile
+    for (int j = 0; j < 4; ++j) {
       float kx[E];
-      load_elems<typename KElem<KV>::T, E>(p.k_cache, kb + (4 * j + kg) * D + sub * E, kx);
+      if constexpr (kAhead) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) kx[e] = kall[j][e];
+      } else {
+        load_elems<typename KElem<KV>::T, E>(p.k_cache, kb + (4 * j + kg) * D + sub * E, kx);
+      }
       const int key = key0 + 4 * j + kg;
 #pragma unroll
       for (int n = 0; n < NP; ++n) {
@@ -160,7 +194,9 @@ __global__ void __launch_bounds__(kWarps * 32) attn_biased_simt_kernel(const Bia
         const int64_t vb = kb + (int64_t)k * D + lane * DV;
 #pragma unroll
         for (int e = 0; e < DV; e += 2) {
-          const float2 v = __ldg(reinterpret_cast<const float2*>(reinterpret_cast<const float*>(p.v_cache) + vb + e));
+          float2 v;
+          if constexpr (kAhead) v = vall[k][e / 2];
+          else v = __ldg(reinterpret_cast<const float2*>(reinterpret_cast<const float*>(p.v_cache) + vb + e));
           vx[e] = v.x;
           vx[e + 1] = v.y;
         }
@@ -172,10 +208,6 @@ __global__ void __launch_bounds__(kWarps * 32) attn_biased_simt_kernel(const Bia
         }
       }
     } else {  // d-major: 16 keys of an element are contiguous
-      uint4 raw[DV];
-#pragma unroll
-      for (int e = 0; e < DV; ++e)
-        raw[e] = __ldg(reinterpret_cast<const uint4*>(p.v_cache + ((blk * hkv + kvh) * D + lane * DV + e) * bs + off));
 #pragma unroll
       for (int k = 0; k < kTile; ++k) {
         const int key = key0 + k;
@@ -233,7 +265,8 @@ cudaError_t launch(const BiasedSimtParams& p, cudaStream_t stream) {
   const int G = p.a.num_q_heads / p.a.num_kv_heads;
   const int64_t blocks = (int64_t)p.a.rows.num_rows * G / NP + p.a.rows.num_seqs;
   if (blocks > INT32_MAX || p.a.num_kv_heads > 65535) return cudaErrorNotSupported;
-  attn_biased_simt_kernel<KV, D, NP><<<dim3((unsigned)blocks, (unsigned)p.a.num_kv_heads), kWarps * 32, 0, stream>>>(p);
+  attn_biased_simt_kernel<KV, D, NP><<<dim3((unsigned)blocks, (unsigned)p.a.num_kv_heads),
+                                             warps_of<KV, D, NP>() * 32, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

@@ -46,6 +46,7 @@ constexpr int kTileRow = 128 * 128;  // bytes of a 64-element-wide chunk of a 12
 constexpr int kUQ = 4;       // unit queue entries
 constexpr int kGroup = 64;   // sequences of a group in the unit search
 constexpr int kMaxGroups = 256;  // groups: 16384 sequences
+constexpr int kMaxOrder = 64;    // up to so many chunks are taken longest context first
 constexpr int kKWarp = 8, kVWarp = 9, kMmaWarp = 10, kConvWarp = 12;  // warps 0..7: softmax of A, of B
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSmemOptIn = 232448;  // 227 KB per block
@@ -74,7 +75,8 @@ struct C {
   static constexpr int Q = 0, K = 2 * TILE, V = K + NK * TILE, R = V + NV * TILE, BARS = R + NR * RAW;
   static constexpr int NBARS = 2 * NK + 2 * NV + 2 * NR + 14 + 4 + 2 * kUQ;
   static constexpr int UQ = BARS + NBARS * 8, TSLOT = UQ + kUQ * 32, GROUPS = TSLOT + 16;
-  static constexpr int TOTAL = GROUPS + (kMaxGroups + 1) * 4 + 1024;
+  static constexpr int ORDER = GROUPS + (kMaxGroups + 1) * 4;  // bases, then sequences
+  static constexpr int TOTAL = ORDER + (kMaxOrder + 1) * 4 + kMaxOrder * 2 + 1024;
   static_assert(TOTAL <= kSmemOptIn, "shared memory");
   static_assert(256 + 2 * D <= (int)kTmemCols, "TMEM columns");
 };
@@ -181,8 +183,28 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
     return q > 1 ? (q + QB2 - 1) / QB2 : 0;  // single rows are the decode kernel's
   };
   const int groups = (S + kGroup - 1) / kGroup;
+  // The chunks by falling context where there are few (long units first leave
+  // a shorter tail; more of them even out by their number): obase, the unit
+  // blocks before each, and oseq, the sequence
+  int32_t* obase = reinterpret_cast<int32_t*>(smem + T::ORDER);
+  int16_t* oseq = reinterpret_cast<int16_t*>(obase + kMaxOrder + 1);
+  int32_t* found = reinterpret_cast<int32_t*>(tmem_slot + 1);
+  if (tid == 0) *found = 0;
+  __syncthreads();
   for (int g = warp; g < groups; g += T::THREADS / 32) {
-    int n = blocks_of(kGroup * g + 2 * lane) + blocks_of(kGroup * g + 2 * lane + 1);
+    int n = 0;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int s = kGroup * g + 2 * lane + e, nb = blocks_of(s);
+      n += nb;
+      if (nb > 0) {
+        const int at = atomicAdd(found, 1);
+        if (at < kMaxOrder) {
+          oseq[at] = (int16_t)s;
+          obase[at] = p.rows.seq_lens[s];
+        }
+      }
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
     if (lane == 0) gsum[g] = n;
@@ -231,6 +253,44 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
       run += __shfl_sync(0xffffffffu, x, 31);
     }
     if (lane == 0) gsum[groups] = run;
+  }
+  const int chunks = *found;
+  const bool ordered = chunks <= kMaxOrder;
+  {
+    // rank by (context, sequence): the same whatever order they were found in
+    int mine = -1, rank = 0, nb = 0;
+    if (ordered && tid < chunks) {
+      mine = oseq[tid];
+      nb = blocks_of(mine);
+      const int len = obase[tid];
+      for (int j = 0; j < chunks; ++j) rank += obase[j] > len || (obase[j] == len && oseq[j] < mine);
+    }
+    __syncthreads();
+    if (mine >= 0) {
+      oseq[rank] = (int16_t)mine;
+      obase[rank] = nb;
+    }
+    __syncthreads();
+    if (ordered && warp == 1) {
+      int v[2], run = 0;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int i = 32 * e + lane;
+        const int n = i < chunks ? obase[i] : 0;
+        int x = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        v[e] = run + x - n;
+        run += __shfl_sync(0xffffffffu, x, 31);
+      }
+      __syncwarp();
+      obase[lane] = v[0];
+      obase[32 + lane] = v[1];
+      if (lane == 0) obase[kMaxOrder] = run;
+    }
   }
   __syncthreads();
   dev::grid_dep_launch();
@@ -288,31 +348,45 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
         idx = __shfl_sync(0xffffffffu, idx, 0);
         if (ok && idx < nunits) {
           const int x = idx / hkv;
-          int lo = 0, hi = groups - 1;  // the last group with gsum <= x
-          while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (gsum[mid] <= x) lo = mid; else hi = mid - 1;
-          }
-          const int s0 = kGroup * lo + 2 * lane;  // this lane's two sequences
-          const int nb0 = blocks_of(s0), nb = nb0 + blocks_of(s0 + 1);
-          int inc = nb;
+          bool hit;
+          int before, mine;
+          if (ordered) {
+            const int r = __popc(__ballot_sync(0xffffffffu, lane < chunks && obase[lane] <= x)) +
+                          __popc(__ballot_sync(0xffffffffu, 32 + lane < chunks && obase[32 + lane] <= x)) - 1;
+            hit = true;
+            u.s = oseq[r];
+            before = obase[r];
+            mine = (r + 1 < chunks ? obase[r + 1] : obase[kMaxOrder]) - before;
+            before -= x;  // (below: the block's place among the sequence's)
+          } else {
+            int lo = 0, hi = groups - 1;  // the last group with gsum <= x
+            while (lo < hi) {
+              const int mid = (lo + hi + 1) >> 1;
+              if (gsum[mid] <= x) lo = mid; else hi = mid - 1;
+            }
+            const int s0 = kGroup * lo + 2 * lane;  // this lane's two sequences
+            const int nb0 = blocks_of(s0), nb = nb0 + blocks_of(s0 + 1);
+            int inc = nb;
 #pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += y;
-          }
-          const int local = x - gsum[lo];
-          const uint32_t hit = __ballot_sync(0xffffffffu, local >= inc - nb && local < inc);
-          const int who = hit ? __ffs(hit) - 1 : 0;
-          const int pair0 = __shfl_sync(0xffffffffu, inc - nb, who);
-          const int n0 = __shfl_sync(0xffffffffu, nb0, who), n1 = __shfl_sync(0xffffffffu, nb, who) - n0;
-          if (hit) {
+            for (int o = 1; o < 32; o <<= 1) {
+              const int y = __shfl_up_sync(0xffffffffu, inc, o);
+              if (lane >= o) inc += y;
+            }
+            const int local = x - gsum[lo];
+            const uint32_t who = __ballot_sync(0xffffffffu, local >= inc - nb && local < inc);
+            hit = who != 0;
+            const int src = hit ? __ffs(who) - 1 : 0;
+            const int pair0 = __shfl_sync(0xffffffffu, inc - nb, src);
+            const int n0 = __shfl_sync(0xffffffffu, nb0, src), n1 = __shfl_sync(0xffffffffu, nb, src) - n0;
             const int second = local - pair0 >= n0;
-            const int before = pair0 + (second ? n0 : 0), mine = second ? n1 : n0;
-            u.s = kGroup * lo + 2 * who + second;
+            u.s = hit ? kGroup * lo + 2 * src + second : -1;
+            mine = second ? n1 : n0;
+            before = pair0 + (second ? n0 : 0) - local;
+          }
+          if (hit) {
             u.h = idx % hkv;
             const int first = p.rows.qsl[u.s], qlen = p.rows.qsl[u.s + 1] - first;
-            const int qb = mine - 1 - (local - before);  // a sequence's last (longest) rows first
+            const int qb = mine - 1 + before;  // a sequence's last (longest) rows first
             int len = p.rows.seq_lens[u.s];
             u.p0 = len - qlen + qb * QB2;
             u.row0 = first + qb * QB2;
@@ -684,73 +758,61 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
           }
         }
         if (slow) {
-        // the row sees keys [wlo, hi) and [0, pl) of the half tile
-        const int hi = valid ? min(pos + 1, u.len) - key0 : 0;
-        const int wlo = tl.window > 0 ? pos - tl.window + 1 - key0 : 0;
-        const int pl = valid ? u.pfx - key0 : 0;
-        // 32 scores of any tile -> exponents s - rf in log2 units: masks, keys
-        // past the row's position (their distance has the other sign), and with
-        // `exact` the cap's exact form
-        auto any_args = [&](int c, float (&a)[32], float rf, bool exact, float& zmax) {
-          uint32_t w[32];
-          dev::tmem_ld32(ts + 32 * c, w);
-          // the chunk's visible keys, a bit each: [0, pl) and [wlo, hi)
-          auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
-          const uint32_t vis = below(pl - 32 * c) | (below(hi - 32 * c) & ~below(wlo - 32 * c));
-          // what a hidden key holds must not choose the cap's form
+          // The first step of a unit, a step with hidden keys, or weights (a
+          // score) that left the fast form's range: the row max, then the
+          // weights, 16 keys at a time over scores already read.  Rolled loops:
+          // this path is taken a few times per unit, and what it costs is
+          // above all fetching its instructions.
+          // The row sees keys [wlo, hi) and [0, pl) of the half tile, a bit each.
+          const int hi = valid ? min(pos + 1, u.len) - key0 : 0;
+          const int wlo = tl.window > 0 ? pos - tl.window + 1 - key0 : 0;
+          const int pl = valid ? u.pfx - key0 : 0;
+          auto below = [](int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull; };
+          const uint64_t vis = below(pl) | (below(hi) & ~below(wlo));
+          // 16 scores -> exponents s - rf in log2 units: masks, keys past the
+          // row's position (their distance has the other sign), and with
+          // `exact` the cap's exact form
+          auto args = [&](int c, float (&a)[16], float rf, bool exact, float& zmax) {
+            uint32_t w[16];
+            dev::tmem_ld16(ts + 16 * c, w);
+            const uint32_t v = (uint32_t)(vis >> (16 * c));
+            const float d = dist - (float)(16 * c);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) a[i] = (vis & (1u << i)) ? __uint_as_float(w[i]) : 0.f;
-          if constexpr (CAPS) {
-            if (exact) {
+            for (int i = 0; i < 16; ++i)  // (what a hidden key holds must not choose the cap's form)
+              a[i] = !CAPS || (v & (1u << i)) ? __uint_as_float(w[i]) : 0.f;
+            if constexpr (CAPS) {
+              if (exact) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) a[i] = dev::capped(a[i], cap_in, p.mod.cap_out);
-            } else {
-              float z0 = 0.f, z1 = 0.f;
+                for (int i = 0; i < 16; ++i) a[i] = dev::capped(a[i], cap_in, p.mod.cap_out);
+              } else {
 #pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const uint64_t y = dev::mul2(dev::f2(a[i], a[i + 1]), dev::f2(y_in, y_in)), z = dev::mul2(y, y);
-                float u0, u1;
-                dev::f2_split(z, u0, u1);
-                if (i & 2) z1 = dev::max3(z1, u0, u1);
-                else z0 = dev::max3(z0, u0, u1);
-                uint64_t q = dev::fma2(z, poly2[4], poly2[3]);
-                q = dev::fma2(z, q, poly2[2]);
-                q = dev::fma2(z, q, poly2[1]);
-                q = dev::fma2(z, q, poly2[0]);
-                dev::f2_split(dev::mul2(y, q), a[i], a[i + 1]);
+                for (int i = 0; i < 16; ++i) {
+                  const float y = a[i] * y_in, z = y * y;
+                  zmax = fmaxf(zmax, z);
+                  float q = fmaf(z, p.mod.poly[4], p.mod.poly[3]);
+                  q = fmaf(z, q, p.mod.poly[2]);
+                  q = fmaf(z, q, p.mod.poly[1]);
+                  a[i] = y * fmaf(z, q, p.mod.poly[0]);
+                }
               }
-              zmax = dev::max3(zmax, z0, z1);
             }
-          }
-          const float mul = CAPS ? 1.f : scale;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float off = SLOPES ? fmaf(-slope, fabsf(dist - (float)(32 * c + i)), -rf) : -rf;
-            a[i] = (vis & (1u << i)) ? fmaf(a[i], mul, off) : -INFINITY;
-          }
-        };
-        auto chunk_sum = [&](const float (&a)[32], uint32_t* out) {
-          float s4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float e0 = dev::ex2(a[2 * i]), e1 = dev::ex2(a[2 * i + 1]);
-            s4[i & 3] += e0 + e1;
-            out[i] = T::FP8 ? dev::pack_f16(e0, e1) : dev::pack_bf16(e0, e1);
-          }
-          return (s4[0] + s4[1]) + (s4[2] + s4[3]);
-        };
-          // the row max first, then the weights, chunk by chunk over S
+            for (int i = 0; i < 16; ++i) {
+              const float off = SLOPES ? fmaf(-slope, fabsf(d - (float)i), -rf) : -rf;
+              a[i] = (v & (1u << i)) ? (CAPS ? a[i] + off : fmaf(a[i], scale, off)) : -INFINITY;
+            }
+          };
           bool exact = false;
           float m, zmax;
           for (;;) {
             m = -INFINITY;
             zmax = 0.f;
 #pragma unroll 1
-            for (int c = 0; c < 2; ++c) {
-              float a[32];
-              any_args(c, a, 0.f, exact, zmax);
+            for (int c = 0; c < kHalf / 16; ++c) {
+              float a[16];
+              args(c, a, 0.f, exact, zmax);
 #pragma unroll
-              for (int i = 0; i < 32; i += 2) m = dev::max3(m, a[i], a[i + 1]);
+              for (int i = 0; i < 16; i += 2) m = dev::max3(m, a[i], a[i + 1]);
             }
             if (!CAPS || exact || !__any_sync(0xffffffffu, !(zmax <= kCapFast * kCapFast))) break;
             exact = true;
@@ -765,21 +827,27 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
             wait_ok(&pv_done[2 * x + (b ^ 1)], ((sc - 1) >> 1) & 1);
             dev::tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t w[32];
-              dev::tmem_ld32(to + 32 * c, w);
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t w[16];
+              dev::tmem_ld16(to + 16 * c, w);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * alpha);
-              dev::tmem_st32(to + 32 * c, w);
+              for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * alpha);
+              dev::tmem_st16(to + 16 * c, w);
             }
           }
 #pragma unroll 1
-          for (int c = 0; c < 2; ++c) {
-            float a[32];
-            any_args(c, a, ref, exact, zmax);
-            uint32_t pk[16];
-            lsum += chunk_sum(a, pk);
-            dev::tmem_st16(ts + 16 * c, pk);  // over scores already read
+          for (int c = 0; c < kHalf / 16; ++c) {
+            float a[16], s2[2] = {0.f, 0.f};
+            args(c, a, ref, exact, zmax);
+            uint32_t pk[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float e0 = dev::ex2(a[2 * i]), e1 = dev::ex2(a[2 * i + 1]);
+              s2[i & 1] += e0 + e1;
+              pk[i] = T::FP8 ? dev::pack_f16(e0, e1) : dev::pack_bf16(e0, e1);
+            }
+            lsum += s2[0] + s2[1];
+            dev::tmem_st8(ts + 8 * c, pk);
           }
         if constexpr (!T::FP8) {
           // V rows that no row of the unit sees may hold anything (0 * NaN):
@@ -821,12 +889,12 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
           dev::tmem_ld32(to + 32 * c, w);
           if (valid && ok) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t o[4];
+            for (int i = 0; i < 2; ++i) {
+              uint32_t o[8];
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                o[e] = dev::pack_bf16(__uint_as_float(w[8 * i + 2 * e]) * inv, __uint_as_float(w[8 * i + 2 * e + 1]) * inv);
-              dst[4 * c + i] = make_uint4(o[0], o[1], o[2], o[3]);
+              for (int e = 0; e < 8; ++e)
+                o[e] = dev::pack_bf16(__uint_as_float(w[16 * i + 2 * e]) * inv, __uint_as_float(w[16 * i + 2 * e + 1]) * inv);
+              dev::store32(dst + 4 * c + 2 * i, o);
             }
           }
         }
