@@ -772,6 +772,16 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
           // 16 scores -> exponents s - rf in log2 units: masks, keys past the
           // row's position (their distance has the other sign), and with
           // `exact` the cap's exact form
+          // the capped pair (y P(y^2)) of two raw scores
+          auto cap2 = [&](float x0, float x1, uint64_t& z) {
+            const uint64_t y = dev::mul2(dev::f2(x0, x1), dev::f2(y_in, y_in));
+            z = dev::mul2(y, y);
+            uint64_t q = dev::fma2(z, poly2[4], poly2[3]);
+            q = dev::fma2(z, q, poly2[2]);
+            q = dev::fma2(z, q, poly2[1]);
+            q = dev::fma2(z, q, poly2[0]);
+            return dev::mul2(y, q);
+          };
           auto args = [&](int c, float (&a)[16], float rf, bool exact, float& zmax) {
             uint32_t w[16];
             dev::tmem_ld16(ts + 16 * c, w);
@@ -786,13 +796,15 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
                 for (int i = 0; i < 16; ++i) a[i] = dev::capped(a[i], cap_in, p.mod.cap_out);
               } else {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  const float y = a[i] * y_in, z = y * y;
-                  zmax = fmaxf(zmax, z);
-                  float q = fmaf(z, p.mod.poly[4], p.mod.poly[3]);
-                  q = fmaf(z, q, p.mod.poly[2]);
-                  q = fmaf(z, q, p.mod.poly[1]);
-                  a[i] = y * fmaf(z, q, p.mod.poly[0]);
+                for (int i = 0; i < 16; i += 2) {
+                  uint64_t z;
+                  const uint64_t y = cap2(a[i], a[i + 1], z);
+                  if (SLOPES) {  // (without slopes the raw maximum has decided)
+                    float z0, z1;
+                    dev::f2_split(z, z0, z1);
+                    zmax = dev::max3(zmax, z0, z1);
+                  }
+                  dev::f2_split(y, a[i], a[i + 1]);
                 }
               }
             }
@@ -803,19 +815,47 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
             }
           };
           bool exact = false;
-          float m, zmax;
-          for (;;) {
-            m = -INFINITY;
-            zmax = 0.f;
+          float m, zmax = 0.f;
+          if constexpr (!SLOPES) {
+            // scale and cap are monotone: the raw maximum decides (and with the
+            // raw minimum whether the cap's polynomial serves)
+            float hi_raw = -INFINITY, lo_raw = INFINITY;
 #pragma unroll 1
             for (int c = 0; c < kHalf / 16; ++c) {
-              float a[16];
-              args(c, a, 0.f, exact, zmax);
+              uint32_t w[16];
+              dev::tmem_ld16(ts + 16 * c, w);
+              const uint32_t v = (uint32_t)(vis >> (16 * c));
 #pragma unroll
-              for (int i = 0; i < 16; i += 2) m = dev::max3(m, a[i], a[i + 1]);
+              for (int i = 0; i < 16; ++i) {
+                const float x = __uint_as_float(w[i]);
+                hi_raw = fmaxf(hi_raw, (v & (1u << i)) ? x : -INFINITY);
+                if (CAPS) lo_raw = fminf(lo_raw, (v & (1u << i)) ? x : INFINITY);
+              }
             }
-            if (!CAPS || exact || !__any_sync(0xffffffffu, !(zmax <= kCapFast * kCapFast))) break;
-            exact = true;
+            if constexpr (CAPS) {
+              const float most = vis ? fmaxf(fabsf(hi_raw), fabsf(lo_raw)) * y_in : 0.f;
+              exact = __any_sync(0xffffffffu, !(most <= kCapFast));
+              uint64_t z;
+              float capped, other;
+              dev::f2_split(cap2(hi_raw, 0.f, z), capped, other);
+              m = !vis ? -INFINITY : exact ? dev::capped(hi_raw, cap_in, p.mod.cap_out) : capped;
+            } else {
+              m = hi_raw * scale;
+            }
+          } else {
+            for (;;) {
+              m = -INFINITY;
+              zmax = 0.f;
+#pragma unroll 1
+              for (int c = 0; c < kHalf / 16; ++c) {
+                float a[16];
+                args(c, a, 0.f, exact, zmax);
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) m = dev::max3(m, a[i], a[i + 1]);
+              }
+              if (!CAPS || exact || !__any_sync(0xffffffffu, !(zmax <= kCapFast * kCapFast))) break;
+              exact = true;
+            }
           }
           // the reference moves where the weights would grow past 2^8; O is
           // rescaled once the previous PV is complete
