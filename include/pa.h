@@ -375,7 +375,10 @@ typedef struct {
                                  tokens); taken as 0 below 0 and as seq_lens[s] above it */
 } pa_score_mod;
 
-/* Scratch bytes pa_decode_biased and pa_decode_chunked_prefill_biased need. */
+/* Scratch bytes pa_decode_biased (num_tokens = num_seqs) and
+ * pa_decode_chunked_prefill_biased need.  With num_tokens > num_seqs that
+ * includes room for the partial results of chunks whose keys are split over
+ * several SMs (39 MB at head_dim 128 on a B200, half of it at 64). */
 size_t pa_biased_workspace_size(const pa_cache_desc* desc, int32_t num_seqs, int32_t num_tokens);
 
 /* pa_decode_biased: pa_decode under `mod`: sequence s's query row sits at

@@ -389,6 +389,21 @@ int check_mod(const pa_score_mod* m, float scale, const pa_cache_desc* d, int32_
   return PA_OK;
 }
 
+// The tensor-core paths' workspace: the decode's, and for a step of more rows
+// than sequences (some of them chunks) the cut units' from *parts_at on.
+size_t biased_workspace(const pa_cache_desc* d, int32_t num_seqs, int32_t num_tokens, int sms, size_t* parts_at) {
+  const int cut = cut_group(d->num_q_heads / d->num_kv_heads, 8);
+  size_t n = decode_tc_workspace_bytes(num_seqs, d->num_q_heads / cut, cut, d->head_dim, sms);
+  if (parts_at) *parts_at = 0;
+  if (num_tokens > num_seqs) {
+    n = (n + 255) / 256 * 256;
+    if (parts_at) *parts_at = n;
+    size_t ml_at, o_at;
+    n += chunk_biased_scratch(d->head_dim, sms, &ml_at, &o_at);
+  }
+  return n;
+}
+
 bool biased_tc(const pa_cache_desc* d) { return d->q_dtype == kBF16 && d->kv_dtype != kF32; }
 
 // Single-token rows of a biased step on the tensor-core decode (qsl null:
@@ -446,7 +461,7 @@ int run_decode_biased(const pa_cache_desc* d, const pa_score_mod* mod, const voi
 int run_prefill_biased(const pa_cache_desc* d, const pa_score_mod* mod, const void* q, const void* k_cache,
                        const void* v_cache, const int32_t* block_tables, int32_t max_blocks, const int32_t* qsl,
                        const int32_t* seq_lens, int32_t num_seqs, int32_t num_tokens, float scale, bool after_decode,
-                       void* out, void* workspace, cudaStream_t stream, const char* who) {
+                       void* out, void* workspace, size_t parts_at, cudaStream_t stream, const char* who) {
   int sms = 0;
   int rc = num_sms(&sms);
   if (rc) return rc;
@@ -486,6 +501,15 @@ int run_prefill_biased(const pa_cache_desc* d, const pa_score_mod* mod, const vo
   p.unit_ctr = static_cast<int32_t*>(workspace) + 2;
   p.unit_exit = static_cast<int32_t*>(workspace) + 3;
   p.after_decode = after_decode;
+  if (parts_at) {  // the workspace has room for cut units
+    size_t ml_at = 0, o_at = 0;
+    chunk_biased_scratch(d->head_dim, sms, &ml_at, &o_at);
+    uint8_t* at = static_cast<uint8_t*>(workspace) + parts_at;
+    p.part_slots = kPartSlots * sms;
+    p.part_cnt = reinterpret_cast<unsigned int*>(at);
+    p.part_ml = reinterpret_cast<float*>(at + ml_at);
+    p.part_o = reinterpret_cast<float*>(at + o_at);
+  }
   cudaError_t e = launch_chunk_biased(p, tm_k, tm_v, tm_q, d->kv_dtype, d->head_dim, d->block_size, num_tokens, sms,
                                       stream);
   if (e == cudaErrorNotSupported) return fail(PA_ERR_UNSUPPORTED, "%s: too many sequences for one launch", who);
@@ -948,8 +972,7 @@ size_t pa_biased_workspace_size(const pa_cache_desc* d, int32_t num_seqs, int32_
   if (!biased_tc(d)) return 256;
   int sms = 0;
   if (num_sms(&sms)) return 0;
-  const int cut = cut_group(d->num_q_heads / d->num_kv_heads, 8);
-  return decode_tc_workspace_bytes(num_seqs, d->num_q_heads / cut, cut, d->head_dim, sms);
+  return biased_workspace(d, num_seqs, num_tokens, sms, nullptr);
 }
 
 int pa_decode_biased(const pa_cache_desc* d, const pa_score_mod* mod, const void* q, const void* k_cache,
@@ -996,8 +1019,10 @@ int pa_decode_chunked_prefill_biased(const pa_cache_desc* d, const pa_score_mod*
   // single-token rows on the decode kernel (there are none when the rows fill
   // every sequence up to max_q_len), the others on the chunk kernel
   const bool decodes = max_q_len == 1 || (int64_t)num_seqs * max_q_len != num_tokens;
-  const size_t need = pa_biased_workspace_size(d, num_seqs, num_tokens);
-  if (need == 0) return PA_ERR_INVALID_ARG;  // the size query recorded why
+  int sms = 0;
+  if ((rc = num_sms(&sms))) return rc;
+  size_t parts_at = 0;
+  const size_t need = biased_workspace(d, num_seqs, num_tokens, sms, &parts_at);
   if (workspace_bytes < need)
     return fail(PA_ERR_INVALID_ARG, "%s: workspace %zu < %zu bytes", who, workspace_bytes, need);
   if (decodes) {
@@ -1006,7 +1031,7 @@ int pa_decode_chunked_prefill_biased(const pa_cache_desc* d, const pa_score_mod*
     if (rc || max_q_len == 1) return rc;
   }
   return run_prefill_biased(d, mod, q, k_cache, v_cache, block_tables, max_blocks_per_seq, query_start_loc, seq_lens,
-                            num_seqs, num_tokens, scale, decodes, out, workspace, st, who);
+                            num_seqs, num_tokens, scale, decodes, out, workspace, parts_at, st, who);
 }
 
 }  // extern "C"

@@ -44,6 +44,7 @@ constexpr int kKeys = 128;   // keys of a K/V tile
 constexpr int kHalf = 64;    // keys of a step: half a tile
 constexpr int kTileRow = 128 * 128;  // bytes of a 64-element-wide chunk of a 128-row tile
 constexpr int kUQ = 4;       // unit queue entries
+constexpr int kMaxParts = 8;
 constexpr int kGroup = 64;   // sequences of a group in the unit search
 constexpr int kMaxGroups = 256;  // groups: 16384 sequences
 constexpr int kMaxOrder = 64;    // up to so many chunks are taken longest context first
@@ -74,7 +75,7 @@ struct C {
   // shared memory
   static constexpr int Q = 0, K = 2 * TILE, V = K + NK * TILE, R = V + NV * TILE, BARS = R + NR * RAW;
   static constexpr int NBARS = 2 * NK + 2 * NV + 2 * NR + 14 + 4 + 2 * kUQ;
-  static constexpr int UQ = BARS + NBARS * 8, TSLOT = UQ + kUQ * 32, GROUPS = TSLOT + 16;
+  static constexpr int UQ = (BARS + NBARS * 8 + 15) / 16 * 16, TSLOT = UQ + kUQ * 48, GROUPS = TSLOT + 16;
   static constexpr int ORDER = GROUPS + (kMaxGroups + 1) * 4;  // bases, then sequences
   static constexpr int TOTAL = ORDER + (kMaxOrder + 1) * 4 + kMaxOrder * 2 + 1024;
   static_assert(TOTAL <= kSmemOptIn, "shared memory");
@@ -87,28 +88,37 @@ struct __align__(16) Unit {
   int row0, qn;    // first query row, positions (at most two tiles' worth)
   int p0;          // position of the first query
   int len, pfx;    // context, visible prefix
-  int pad;
+  int unit;        // the unit's number, where its keys are cut into parts
+  int part, parts; // this part of them
+  int pad[2];
 };
-static_assert(sizeof(Unit) == 32, "queue entry");
+static_assert(sizeof(Unit) == 48, "queue entry");
 
-// A unit's key tiles: [0, npt) and [npt + gap, npt + gap + ...), nt in all,
-// visited from the last.
+// A unit's key tiles: [0, npt) and [npt + gap, npt + gap + ...), visited from
+// the last; nt of them are this part's.
 template <int BS>
 struct Tiles {
   int kend, lo, nb, nt, npt, gap, window, pfx;
+  int all, from;  // tiles of the unit, and where this part of it starts
   __device__ __forceinline__ Tiles(const Unit& u, const PrefillParams& p) {
     window = p.mod.window;
     pfx = u.pfx;
     kend = max(min(u.len, u.p0 + u.qn), u.pfx);
     lo = window > 0 ? max(0, u.p0 - window + 1) : 0;
     nb = min((max(kend, 0) + BS - 1) / BS, p.max_blocks);
-    const int all = (nb * BS + kKeys - 1) / kKeys;
-    npt = min((pfx + kKeys - 1) / kKeys, all);
-    gap = max(0, min(lo / kKeys, all) - npt);
-    nt = all - gap;
+    const int tiles = (nb * BS + kKeys - 1) / kKeys;
+    npt = min((pfx + kKeys - 1) / kKeys, tiles);
+    gap = max(0, min(lo / kKeys, tiles) - npt);
+    all = tiles - gap;
+    from = 0;
+    nt = all;
+    if (u.parts > 1) {
+      from = all * u.part / u.parts;
+      nt = all * (u.part + 1) / u.parts - from;
+    }
   }
   __device__ __forceinline__ int tile(int k) const {
-    const int t = nt - 1 - k;
+    const int t = all - 1 - from - k;
     return t < npt ? t : t + gap;
   }
   // Half tiles, 64 keys each, in the order of the visits: step j is half 1 - j
@@ -294,7 +304,12 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
   }
   __syncthreads();
   dev::grid_dep_launch();
-  const int nunits = gsum[groups] * hkv;
+  // With few units their keys are cut into parts, so that every SM gets some
+  // and the last ones are short; a unit's parts leave (reference, sum, O) per
+  // row, and for each warp's rows the part that arrives last joins them.
+  const int whole = gsum[groups] * hkv;
+  const int parts = whole > 0 ? max(1, min(kMaxParts, p.part_slots / whole)) : 1;
+  const int nunits = whole * parts;
   auto finish_queue = [&]() {  // the last CTA puts the claim counter back to zero
     if (tid == 0) {
       __threadfence();
@@ -342,12 +357,14 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
       Unit u;
       u.s = -1;
       if (!is_v) {
-        // claim the next unit and publish it
-        int idx = 0;
-        if (ok && lane == 0) idx = atomicAdd(p.unit_ctr, 1);
-        idx = __shfl_sync(0xffffffffu, idx, 0);
-        if (ok && idx < nunits) {
-          const int x = idx / hkv;
+        // claim the next unit (part) and publish it; parts that a short unit
+        // does not have are passed over
+        while (ok && u.s < 0) {
+          int idx = 0;
+          if (lane == 0) idx = atomicAdd(p.unit_ctr, 1);
+          idx = __shfl_sync(0xffffffffu, idx, 0);
+          if (idx >= nunits) break;
+          const int id = idx / parts, x = id / hkv;
           bool hit;
           int before, mine;
           if (ordered) {
@@ -384,7 +401,10 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
             before = pair0 + (second ? n0 : 0) - local;
           }
           if (hit) {
-            u.h = idx % hkv;
+            u.h = id % hkv;
+            u.unit = id;
+            u.part = idx - id * parts;
+            u.parts = 1;
             const int first = p.rows.qsl[u.s], qlen = p.rows.qsl[u.s + 1] - first;
             const int qb = mine - 1 + before;  // a sequence's last (longest) rows first
             int len = p.rows.seq_lens[u.s];
@@ -397,7 +417,10 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
             }
             u.len = len;
             u.pfx = p.mod.prefix ? max(0, min(len, __ldg(p.mod.prefix + u.s))) : 0;
-            u.pad = 0;
+            if (parts > 1) {  // at least two tiles a part
+              u.parts = min(parts, max(1, Tiles<BS>(u, p).all / 2));
+              if (u.part >= u.parts) u.s = -1;
+            }
           }
         }
         const int slot = n % kUQ;
@@ -543,6 +566,8 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
         u.qn = uni(u.qn);
         u.len = uni(u.len);
         u.pfx = uni(u.pfx);
+        u.part = uni(u.part);
+        u.parts = uni(u.parts);
         __syncwarp();
         if (on) dev::mbar_arrive(&uq_empty[n % kUQ]);
         if (u.s < 0) break;
@@ -919,7 +944,81 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
       // ---- O / sum -> the output row; then O is free ----
       const int64_t at = ((int64_t)(u.row0 + x * QB + r / G) * hq + qh) * D;
       uint4* dst = reinterpret_cast<uint4*>(p.out + at * 2);
-      if (!first) {
+      if (u.parts > 1) {
+        // this part's rows, lane by lane side by side, then the join
+        const int64_t slot = ((int64_t)u.unit * parts + u.part) * 8 + warp;
+        float2* ml = reinterpret_cast<float2*>(p.part_ml) + slot * 32 + lane;
+        float4* po = reinterpret_cast<float4*>(p.part_o) + slot * (D / 4) * 32 + lane;
+        if (!first) {
+          wait_ok(&pv_done[2 * x + ((sc - 1) & 1)], ((sc - 1) >> 1) & 1);
+          dev::tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t w[16];
+            dev::tmem_ld16(to + 16 * c, w);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              __stcg(po + (4 * c + i) * 32, make_float4(__uint_as_float(w[4 * i]), __uint_as_float(w[4 * i + 1]),
+                                                        __uint_as_float(w[4 * i + 2]), __uint_as_float(w[4 * i + 3])));
+          }
+          dev::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) dev::mbar_arrive(&o_free[x]);
+        }
+        __stcg(ml, make_float2(ref, lsum));  // (no tile: the starting reference, 0)
+        __threadfence();
+        __syncwarp();
+        unsigned int* cnt = p.part_cnt + (int64_t)u.unit * 8 + warp;
+        int last = 0;
+        if (lane == 0) last = ok && atomicAdd(cnt, 1u) == (unsigned)u.parts - 1u;
+        last = __shfl_sync(0xffffffffu, last, 0);
+        if (last) {
+          __threadfence();
+          const float2* pml = reinterpret_cast<const float2*>(p.part_ml) + ((int64_t)u.unit * parts * 8 + warp) * 32 + lane;
+          const float4* pp = reinterpret_cast<const float4*>(p.part_o) +
+                             ((int64_t)u.unit * parts * 8 + warp) * (D / 4) * 32 + lane;
+          float M = -1e30f, L = 0.f, wt[kMaxParts];
+#pragma unroll
+          for (int q = 0; q < kMaxParts; ++q)
+            if (q < u.parts) M = fmaxf(M, __ldcg(pml + q * 8 * 32).x);
+#pragma unroll
+          for (int q = 0; q < kMaxParts; ++q) {
+            wt[q] = 0.f;
+            if (q < u.parts) {
+              const float2 v = __ldcg(pml + q * 8 * 32);
+              if (v.x > -1e29f) wt[q] = dev::ex2(v.x - M);  // (a row without a tile there left no O)
+              L = fmaf(v.y, wt[q], L);
+            }
+          }
+          const float inv = L > 0.f ? osc / L : (L == 0.f ? 0.f : L);
+#pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {  // (all parts' loads of a chunk are in flight together)
+            float4 o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int q = 0; q < kMaxParts; ++q) {
+              if (q >= u.parts || wt[q] == 0.f) continue;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float4 v = __ldcg(pp + ((int64_t)q * 8 * (D / 4) + 4 * c + i) * 32);
+                o[i].x = fmaf(v.x, wt[q], o[i].x);
+                o[i].y = fmaf(v.y, wt[q], o[i].y);
+                o[i].z = fmaf(v.z, wt[q], o[i].z);
+                o[i].w = fmaf(v.w, wt[q], o[i].w);
+              }
+            }
+            uint32_t out[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              out[2 * i] = dev::pack_bf16(o[i].x * inv, o[i].y * inv);
+              out[2 * i + 1] = dev::pack_bf16(o[i].z * inv, o[i].w * inv);
+            }
+            if (valid && ok) dev::store32(dst + 2 * c, out);
+          }
+          if (lane == 0) *cnt = 0u;  // ready for the next call
+        }
+      } else if (!first) {
         wait_ok(&pv_done[2 * x + ((sc - 1) & 1)], ((sc - 1) >> 1) & 1);
         dev::tc_fence_after();
         const float inv = lsum > 0.f ? osc / lsum : (lsum == 0.f ? 0.f : lsum);  // nothing visible: 0; NaN stays
@@ -1120,9 +1219,21 @@ cudaError_t launch_chunk_biased(const PrefillParams& p_in, const CUtensorMap& tm
   const int64_t bound = ((int64_t)num_tokens / qb2 + p.rows.num_seqs) * p.num_kv_heads;  // units, at most
   if (bound <= 0) return cudaSuccess;
   if (bound >= INT32_MAX) return cudaErrorNotSupported;
-  const int grid = (int)(bound < num_sms ? bound : num_sms);
+  // units are cut into at most kMaxParts parts each
+  const int64_t most = p.part_slots > 0 ? bound * kMaxParts : bound;
+  const int grid = (int)(most < num_sms ? most : num_sms);
   return kv == kBF16 ? launch_kv<kBF16>(p, tm_k, tm_v, tm_q, head_dim, block_size, grid, stream)
                      : launch_kv<kFP8>(p, tm_k, tm_v, tm_q, head_dim, block_size, grid, stream);
+}
+
+// Scratch of the cut units: arrival counters, (reference, sum) and O rows of
+// up to 2 slots per SM (a slot: one part of one unit, 256 rows; with 4 the 256
+// units of two long chunks were halved too, and took 415 us instead of 344).
+size_t chunk_biased_scratch(int head_dim, int num_sms, size_t* ml_at, size_t* o_at) {
+  const size_t slots = kPartSlots * (size_t)num_sms;
+  *ml_at = slots * 8 * 4;
+  *o_at = *ml_at + slots * 256 * 8;
+  return *o_at + slots * 256 * (size_t)head_dim * 4;
 }
 
 }  // namespace pa

@@ -203,6 +203,12 @@ struct PrefillParams {
   float* pfx_ml;               // [chunks][M][Hq][2] (max reference, sum), log2 domain
   float* pfx_o;                // [chunks][M][Hq][D]
   ScoreMod mod;                // the biased kernel's
+  // the biased kernel's cut units (part_slots 0: none are cut): counters, zero
+  // between calls, [slots][8]; (reference, sum) [slots][256][2]; O [slots][256][D]
+  int32_t part_slots;
+  unsigned int* part_cnt;
+  float* part_ml;
+  float* part_o;
   const uint8_t* k_raw;        // an e4m3 pool
   const uint8_t* v_raw;
   float out_scale;             // the biased kernel's: 1, or an e4m3 pool's V scale
@@ -247,6 +253,8 @@ cudaError_t launch_prefill_umma(const PrefillParams& p, const CUtensorMap& tm_k,
 cudaError_t launch_chunk_biased(const PrefillParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                 const CUtensorMap& tm_q, int kv, int head_dim, int block_size, int num_tokens,
                                 int num_sms, cudaStream_t stream);
+constexpr int kPartSlots = 2;  // slots per SM
+size_t chunk_biased_scratch(int head_dim, int num_sms, size_t* ml_at, size_t* o_at);
 cudaError_t launch_prefill_tc(const PrefillParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                               int head_dim, int block_size, int num_tokens, cudaStream_t stream);
 
