@@ -366,7 +366,7 @@ int pa_decode_chunked_prefill(const pa_cache_desc* desc, const void* q, const vo
  * (softcap 0: scale * q_i k_j), and the output is the softmax over the visible
  * keys.  Without prefix and window that is pa_decode's causal attention. */
 typedef struct {
-  float softcap;              /* 0 (none), or positive and finite */
+  float softcap;              /* 0 (none), or 1e-4 to 1e4 */
   int32_t window;             /* 0 (none), or the keys a row sees up to itself, itself included */
   const float* slopes;        /* NULL (none), or device fp32 [num_q_heads], finite */
   const int32_t* prefix_lens; /* NULL (none), or device int32 [num_seqs]: keys 0 .. prefix_lens[s] - 1 are

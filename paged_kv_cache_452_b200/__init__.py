@@ -128,7 +128,7 @@ def _pools(who, desc, k_cache, v_cache, dev):
             name = "k_cache" if t is k_cache else "v_cache"
             raise PaError(1, f"{who}: {name} must hold {need} contiguous bytes on cuda:{dev}")
     if desc.k_head_scales or desc.v_head_scales:
-        for name, t in (("k_head_scales", desc._keep[0]), ("v_head_scales", desc._keep[1])):
+        for name, t in zip(("k_head_scales", "v_head_scales"), getattr(desc, "_keep", ())):
             if isinstance(t, torch.Tensor):
                 _array(who, name, t, torch.float32, dev, (desc.num_kv_heads,))
 
@@ -161,6 +161,7 @@ class QkPrep(ctypes.Structure):
     _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("eps", ctypes.c_float),
                 ("cos_sin", ctypes.c_void_p), ("num_positions", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
                 ("interleaved", ctypes.c_int32)]
+    _dev = _weights = None
 
     @classmethod
     def make(cls, q_weight=None, k_weight=None, eps=1e-6, cos_sin=None, interleaved=False):
@@ -350,6 +351,7 @@ class ScoreMod(ctypes.Structure):
     """pa_score_mod: what the biased attention does to the scores (keeps its tensors alive)."""
     _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int32), ("slopes", ctypes.c_void_p),
                 ("prefix_lens", ctypes.c_void_p)]
+    _dev = _heads = _seqs = None
 
     @classmethod
     def make(cls, softcap=0.0, window=0, slopes=None, prefix_lens=None):

@@ -379,9 +379,13 @@ int check_mod(const pa_score_mod* m, float scale, const pa_cache_desc* d, int32_
   if (!m) return fail(PA_ERR_INVALID_ARG, "%s: mod is NULL", who);
   if (!(m->softcap >= 0.f) || !std::isfinite(m->softcap))
     return fail(PA_ERR_INVALID_ARG, "%s: softcap must be 0 or positive and finite", who);
+  if (m->softcap > 1e4f || (m->softcap > 0.f && m->softcap < 1e-4f))
+    return fail(PA_ERR_INVALID_ARG, "%s: softcap %g (0, or 1e-4 to 1e4)", who, (double)m->softcap);
   if (m->window < 0) return fail(PA_ERR_INVALID_ARG, "%s: window < 0", who);
   if (!(scale > 0.f) || !std::isfinite(scale))
     return fail(PA_ERR_INVALID_ARG, "%s: scale must be positive and finite", who);
+  if (m->softcap > 0.f && !(scale <= 1e20f))
+    return fail(PA_ERR_INVALID_ARG, "%s: scale %g with a softcap", who, (double)scale);
   if (!aligned(m->slopes, 4) || !aligned(m->prefix_lens, 4))
     return fail(PA_ERR_INVALID_ARG, "%s: misaligned slopes or prefix_lens", who);
   if ((int64_t)max_blocks * d->block_size >= (int64_t)INT32_MAX)

@@ -20,6 +20,7 @@ namespace {
 
 constexpr int kTile = 16;  // keys of a tile: block sizes are multiples of it
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kHalfLn2 = 0.34657359027997264f;  // cap_in holds 2 log2(e) times what tanh takes
 
 template <typename T, int E>
 __device__ __forceinline__ void load_elems(const uint8_t* base, int64_t idx, float (&x)[E]) {
@@ -160,7 +161,8 @@ __global__ void __launch_bounds__(warps_of<KV, D, NP>() * 32) attn_biased_simt_k
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
         const bool seen = key < len && (key < pfx || (key <= pos[n] && (W <= 0 || pos[n] - key < W)));
-        const float x = bp.mod.cap_out > 0.f ? dev::capped(dot, bp.mod.cap_in * kmul, bp.mod.cap_out)
+        // (tanhf: fp32 rows are held to fp32's rounding, and latency bounds)
+        const float x = bp.mod.cap_out > 0.f ? bp.mod.cap_out * tanhf(dot * (bp.mod.cap_in * kmul * kHalfLn2))
                                              : dot * (p.scale * kLog2e * kmul);
         sc[n][j] = seen ? fmaf(-slope[n], fabsf((float)(pos[n] - key)), x) : -INFINITY;
       }

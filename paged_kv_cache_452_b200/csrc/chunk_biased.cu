@@ -407,17 +407,19 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
             u.parts = 1;
             const int first = p.rows.qsl[u.s], qlen = p.rows.qsl[u.s + 1] - first;
             const int qb = mine - 1 + before;  // a sequence's last (longest) rows first
-            int len = p.rows.seq_lens[u.s];
+            int len = p.rows.seq_lens[u.s];  // (u.s is a sequence here; below it may be given up)
             u.p0 = len - qlen + qb * QB2;
             u.row0 = first + qb * QB2;
-            u.qn = min(QB2, qlen - qb * QB2);
+            // (never past the rows that q and out have, whatever query_start_loc says)
+            u.qn = min(min(QB2, qlen - qb * QB2), p.rows.num_rows - u.row0);
+            if (u.row0 < 0 || u.qn <= 0) u.s = -1;
             if (len > p.max_blocks * BS) {  // longer than its table row: flag, clamp
               if (lane == 0) atomicCAS(p.err, 0, 3);
               len = p.max_blocks * BS;
             }
             u.len = len;
-            u.pfx = p.mod.prefix ? max(0, min(len, __ldg(p.mod.prefix + u.s))) : 0;
-            if (parts > 1) {  // at least two tiles a part
+            u.pfx = p.mod.prefix && u.s >= 0 ? max(0, min(len, __ldg(p.mod.prefix + u.s))) : 0;
+            if (parts > 1 && u.s >= 0) {  // at least two tiles a part
               u.parts = min(parts, max(1, Tiles<BS>(u, p).all / 2));
               if (u.part >= u.parts) u.s = -1;
             }

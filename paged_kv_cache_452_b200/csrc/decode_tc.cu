@@ -336,7 +336,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<KV>())
   const int T = hkv * prefix[S];
   const int W = gridDim.x * kWarps;  // warps of the grid: the workers
   const int wk = blockIdx.x * kWarps + warp;
-  // a decode row with an empty context attends nothing: zero output
+  // a decode row with an empty context attends nothing: zero output (the
+  // biased form waits first: the kernel before this one may write the same rows)
+  if constexpr (MOD) dev::grid_dep_wait();
   for (int s = blockIdx.x; s < S; s += gridDim.x) {
     const int qlen = p.rows.qsl ? p.rows.qsl[s + 1] - p.rows.qsl[s] : 1;
     if (qlen == 1 && prefix[s + 1] == prefix[s]) {

@@ -211,6 +211,66 @@ def test_chunks_match_fp64(hq, hkv, d, bs, kv, q, shape, mod, cuda_device):
     assert torch.equal(first, b.out)
 
 
+@pytest.mark.parametrize("mod", [dict(), dict(cap=30.0, slopes=True), dict(window=700, prefix=[300, 0, 2500, 0]),
+                                 dict(slopes=True, prefix=[4000, 129, 1, 0])], ids=str)
+@pytest.mark.parametrize("hq,hkv,d,bs,kv", [(8, 2, 128, 16, "bf16"), (1, 1, 64, 32, "bf16"), (8, 1, 128, 32, "e4m3"),
+                                            (6, 2, 64, 16, "e4m3")])
+def test_few_rows_over_long_contexts(hq, hkv, d, bs, kv, mod, cuda_device):
+    """Few units: their keys are cut over several SMs and joined; short ones beside long ones have fewer parts."""
+    b = Batch(cuda_device, [16, 2, 70, 1], [4000, 130, 2500, 3000], hq, hkv, d, bs, kv, "bf16", **mod, seed=d)
+    for _ in range(3):  # the counters start every call at zero
+        b.out.fill_(float("nan"))
+        b.run(decode=False)
+        b.check()
+
+
+def test_many_chunks(cuda_device):
+    """More chunks than are put in order, between decode rows and empty sequences."""
+    rng = np.random.default_rng(2)
+    qlens = [int(rng.choice([0, 1, 1, 2, 5, 40])) for _ in range(300)]
+    lens = [q + int(rng.integers(0, 200)) if q else 7 for q in qlens]
+    b = Batch(cuda_device, qlens, lens, 4, 2, 64, 16, "bf16", "bf16", cap=20.0, window=50, seed=2)
+    b.run(decode=False)
+    b.check()
+
+
+def test_rows_of_others_stay(cuda_device):
+    """A row past the last sequence's, as in a padded batch, keeps what it held."""
+    for kv in ("bf16", "e4m3"):
+        b = Batch(cuda_device, [40, 1, 3], [90, 33, 200], 8, 2, 128, 16, kv, "bf16", cap=30.0, seed=5)
+        pad = 9
+        q, out = b.q, b.out
+        b.q = torch.cat([q, torch.full((pad, 8, 128), float("nan"), dtype=q.dtype, device=cuda_device)])
+        b.out = torch.full((q.shape[0] + pad, 8, 128), 3.0, dtype=q.dtype, device=cuda_device)
+        b.run(decode=False)
+        torch.cuda.synchronize()
+        assert bool((b.out[-pad:] == 3).all())
+        b.q, b.out = q, b.out[:-pad].contiguous()
+        b.check()
+
+
+def test_capped_fp32_keeps_fp32(cuda_device):
+    """The cap in fp32 rows: within 1e-5 of the fp64 result in the 2-norm."""
+    b = Batch(cuda_device, [1] * 5, [40, 128, 300, 64, 511], 4, 2, 64, 16, "f32", "f32", cap=50.0, slopes=True, seed=1)
+    b.run(decode=True)
+    exp, _ = b.expected()
+    assert float((b.out.double() - exp).norm() / exp.norm()) < 1e-5
+
+
+def test_decode_behind_a_chunk_on_the_same_output(cuda_device):
+    """Calls follow one another on one stream without a gap and over one output: a decode step right behind a chunk
+    step that writes the same rows, its empty contexts' zero rows included."""
+    big = Batch(cuda_device, [512, 512], [3000, 3500], 8, 2, 128, 16, "bf16", "bf16", cap=30.0, seed=1)
+    small = Batch(cuda_device, [1] * 6, [0, 40, 0, 900, 0, 17], 8, 2, 128, 16, "bf16", "bf16", cap=30.0, seed=2)
+    for _ in range(5):
+        small.out = big.out[:6]
+        big.run(decode=False)
+        small.run(decode=True)
+        torch.cuda.synchronize()
+        small.check()
+        assert bool((small.out[[0, 2, 4]] == 0).all())
+
+
 def test_a_group_of_more_than_128(cuda_device):
     b = Batch(cuda_device, [3, 1], [40, 90], 130, 1, 64, 16, "bf16", "bf16", cap=10.0, seed=3)
     b.run(decode=False)

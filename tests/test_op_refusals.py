@@ -98,7 +98,8 @@ def test_biased_attention_refusals():
             ctypes.byref(d) if d is not None else None, ctypes.byref(m) if m is not None else None, q, kc, vc, bt, mb,
             qsl, sl, n, t, mq, scale, out, ws, wb, None)
     bad_mods = [pa.ScoreMod(-1.0, 0, None, None), pa.ScoreMod(float("nan"), 0, None, None),
-                pa.ScoreMod(float("inf"), 0, None, None), pa.ScoreMod(0.0, -1, None, None),
+                pa.ScoreMod(float("inf"), 0, None, None), pa.ScoreMod(2e4, 0, None, None),
+                pa.ScoreMod(1e-5, 0, None, None), pa.ScoreMod(0.0, -1, None, None),
                 pa.ScoreMod(0.0, 0, P + 2, None), pa.ScoreMod(0.0, 0, None, P + 1)]
     for call in (decode, chunk):
         assert call(None, mod) == 1 and call(desc, None) == 1
@@ -108,6 +109,7 @@ def test_biased_attention_refusals():
                    dict(q=P + 8), dict(out=P + 2), dict(ws=P + 16), dict(n=-1), dict(mb=-1), dict(scale=0.0),
                    dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf"))):
             assert call(desc, mod, **kw) == 1, kw
+        assert call(desc, mod, scale=1e21) == 1  # with a cap
         assert call(f32, mod, wb=255) == 1  # workspace too small, fp32 path
         assert call(desc, mod, n=20000) == 2
         assert call(desc, mod, n=1, mb=1 << 27) == 2  # a table row of 2^31 tokens
