@@ -25,6 +25,8 @@
 // the window's slots fill an aligned part of a block (single bytes otherwise).
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "pa_device.cuh"
 #include "pa_kernels.h"
 #include "slot_window.cuh"
@@ -151,28 +153,20 @@ __device__ __forceinline__ void write_v_window(const NormRopeParams& p, int64_t 
   }
 }
 
+// T: element type of the new rows; FP8: an e4m3 pool; HEADS: head rows of one
+// token per row group; `block` counts CTA-sized pieces of the row groups.
 // FULL: every head is normed and rotated over its whole width in halves (what
 // most calls ask for): issue slots bound the general form (at 4344 tokens it
 // took 23 us, 70% of them busy), so this one multiplies weights and angles
 // together once per group, works on pairs of elements and moves V rows as they
 // are.
 template <typename T, int D, bool FP8, int HEADS, bool FULL>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) norm_rope_write_kernel(const NormRopeParams p, unsigned v_blocks) {
-  dev::grid_dep_wait();
-  dev::grid_dep_launch();
-  const int hq = p.num_q_heads, hkv = p.num_kv_heads;
-  if constexpr (FP8) {
-    if (blockIdx.x < v_blocks) {
-      const int64_t items = ((int64_t)p.num_tokens + dev::kWindow - 1) / dev::kWindow * hkv;
-      const int64_t item = (int64_t)blockIdx.x * (kThreads / (D / 2)) + threadIdx.x / (D / 2);
-      if (item < items) write_v_window<T, D>(p, item);
-      return;
-    }
-  }
+__device__ __forceinline__ void prepare_rows(const NormRopeParams& p, uint32_t block) {
   constexpr int LANES = D / 8;  // lanes of a head row
   // A token's row groups: its query heads', its keys', its values' (in e4m3
   // the windows'), HEADS rows each: a group's rows are of one kind.
-  const uint32_t item = (blockIdx.x - (FP8 ? v_blocks : 0u)) * (kThreads / LANES) + threadIdx.x / LANES;
+  const int hq = p.num_q_heads, hkv = p.num_kv_heads;
+  const uint32_t item = block * (kThreads / LANES) + threadIdx.x / LANES;
   const uint32_t items = (uint32_t)p.num_tokens * p.per_token.d;
   const bool live = item < items;  // whole warps stay for the norm's shuffles
   const uint32_t t = live ? dev::fdiv(item, p.per_token) : 0;
@@ -366,8 +360,29 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4) norm_rope_wr
   }
 }
 
+// The first `v_blocks` of `blocks` pieces of work are windows of e4m3 V, the
+// others row groups; a launch of more pieces than fit the GPU at once walks
+// them with resident CTAs.
 template <typename T, int D, bool FP8, int HEADS, bool FULL>
-cudaError_t launch(const NormRopeParams& p, cudaStream_t stream) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4)
+    norm_rope_write_kernel(const NormRopeParams p, uint32_t v_blocks, uint32_t blocks) {
+  dev::grid_dep_wait();
+  dev::grid_dep_launch();
+  for (uint32_t w = blockIdx.x; w < blocks; w += gridDim.x) {
+    if constexpr (FP8) {
+      if (w < v_blocks) {
+        const int64_t items = ((int64_t)p.num_tokens + dev::kWindow - 1) / dev::kWindow * p.num_kv_heads;
+        const int64_t item = (int64_t)w * (kThreads / (D / 2)) + threadIdx.x / (D / 2);
+        if (item < items) write_v_window<T, D>(p, item);
+        continue;
+      }
+    }
+    prepare_rows<T, D, FP8, HEADS, FULL>(p, w - (FP8 ? v_blocks : 0u));
+  }
+}
+
+template <typename T, int D, bool FP8, int HEADS, bool FULL>
+cudaError_t launch(const NormRopeParams& p, int num_sms, cudaStream_t stream) {
   NormRopeParams q = p;
   const int gk = (p.num_kv_heads + HEADS - 1) / HEADS;
   q.per_token = fast_div((uint32_t)((p.num_q_heads + HEADS - 1) / HEADS + (FP8 ? 1 : 2) * gk));
@@ -381,7 +396,7 @@ cudaError_t launch(const NormRopeParams& p, cudaStream_t stream) {
   }
   if (items > INT32_MAX || rows + vwin > INT32_MAX) return cudaErrorNotSupported;
   norm_rope_write_kernel<T, D, FP8, HEADS, FULL>
-      <<<(unsigned)(rows + vwin), kThreads, 0, stream>>>(q, (unsigned)vwin);
+      <<<(unsigned)std::min<int64_t>(rows + vwin, (int64_t)num_sms * (sizeof(T) == 4 ? 3 : 4)), kThreads, 0, stream>>>(q, (uint32_t)vwin, (uint32_t)(rows + vwin));
   return cudaGetLastError();
 }
 
@@ -392,8 +407,8 @@ cudaError_t launch_h(const NormRopeParams& p, int num_sms, cudaStream_t stream) 
   const int64_t rows = (int64_t)p.num_tokens * (p.num_q_heads + 2 * p.num_kv_heads);
   const bool full = p.cos_sin && p.rot_dim == D && !p.interleaved && p.q_weight && p.k_weight;
   if (rows * (D / 8) <= (int64_t)num_sms * 2048)
-    return full ? launch<T, D, FP8, 1, true>(p, stream) : launch<T, D, FP8, 1, false>(p, stream);
-  return full ? launch<T, D, FP8, 4, true>(p, stream) : launch<T, D, FP8, 4, false>(p, stream);
+    return full ? launch<T, D, FP8, 1, true>(p, num_sms, stream) : launch<T, D, FP8, 1, false>(p, num_sms, stream);
+  return full ? launch<T, D, FP8, 4, true>(p, num_sms, stream) : launch<T, D, FP8, 4, false>(p, num_sms, stream);
 }
 
 template <typename T, bool FP8>
