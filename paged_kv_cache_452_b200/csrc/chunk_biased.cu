@@ -724,15 +724,25 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
       float ref = -1e30f, lsum = 0.f;
       bool first = true;
       int h = tl.first_half();
-      for (int j = 0; j < 2 * tl.nt; ++j, h = tl.next_half(h)) {
-        if (!seen(h)) continue;
-        const uint32_t b = sc & 1, ts = ts0 + b * kHalf;
-        wait_ok(&s_full[2 * x + b], (sc >> 1) & 1);
-        dev::tc_fence_after();
-        const int key0 = h * kHalf;
-        const float dist = (float)(pos - key0);
-        bool slow = first || !(h < ppre || (h >= pbeg && h < pend));
-        if (!slow) {
+      for (int j = 0; j < 2 * tl.nt;) {
+        if (!seen(h)) {
+          ++j;
+          h = tl.next_half(h);
+          continue;
+        }
+        // the plain halves from here on, one under the other
+        int run = 0;
+        if (!first) {
+          if (h >= pbeg && h < pend) run = h + 1 - max(pbeg, tl.gap > 0 && h >= 2 * (tl.npt + tl.gap) ? 2 * (tl.npt + tl.gap) : 0);
+          else if (h < ppre) run = h + 1;
+          run = min(run, 2 * tl.nt - j);
+        }
+        bool landed = false;  // the scores of half h have been waited for
+        const bool ran = run > 0;
+        for (float dist = (float)(pos - h * kHalf); run > 0; --run, dist += (float)kHalf) {
+          const uint32_t b = sc & 1, ts = ts0 + b * kHalf;
+          wait_ok(&s_full[2 * x + b], (sc >> 1) & 1);
+          dev::tc_fence_after();
           // Weights over the reference in hand, kept in registers until they
           // are known to be in range (the scores are needed again if not).
           // Arithmetic on pairs: with two warps per SM sub-partition issue
@@ -777,14 +787,30 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
           float sum, odd;
           dev::f2_split(sum2, sum, odd);
           sum += odd;
-          slow = __any_sync(0xffffffffu,
-                            valid && (!(sum <= T::BIG) || (CAPS && !(fmaxf(z2[0], z2[1]) <= kCapFast * kCapFast))));
-          if (!slow) {
-            lsum += sum;
-            dev::tmem_st32(ts, pk);
-          }
+          landed = __any_sync(0xffffffffu, valid && (!(sum <= T::BIG) ||
+                                                      (CAPS && !(fmaxf(z2[0], z2[1]) <= kCapFast * kCapFast))));
+          if (landed) break;  // out of range: the long way below
+          lsum += sum;
+          dev::tmem_st32(ts, pk);
+          dev::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) dev::mbar_arrive(&p_full[2 * x + b]);
+          ++sc;
+          ++j;
+          --h;
         }
-        if (slow) {
+        if (ran && !landed) {
+          if (tl.gap > 0 && h == 2 * (tl.npt + tl.gap) - 1) h = 2 * tl.npt - 1;
+          continue;
+        }
+        const uint32_t b = sc & 1, ts = ts0 + b * kHalf;
+        if (!landed) {
+          wait_ok(&s_full[2 * x + b], (sc >> 1) & 1);
+          dev::tc_fence_after();
+        }
+        const int key0 = h * kHalf;
+        const float dist = (float)(pos - key0);
+        {
           // The first step of a unit, a step with hidden keys, or weights (a
           // score) that left the fast form's range: the row max, then the
           // weights, 16 keys at a time over scores already read.  Rolled loops:
@@ -941,6 +967,8 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
         __syncwarp();
         if (lane == 0) dev::mbar_arrive(&p_full[2 * x + b]);
         ++sc;
+        ++j;
+        h = tl.next_half(h);
       }
       gv += tl.nt;
       // ---- O / sum -> the output row; then O is free ----
