@@ -11,25 +11,42 @@
 // warps each, a thread per row.  While A's softmax runs, the tensor core does
 // B's products and the other way round, and both tiles use every K/V tile that
 // is brought in.  One persistent CTA per SM claims units from a counter.
-//  * TMEM (512 columns): S_A, S_B (128 each), O_A, O_B (head_dim each).  A
-//    tile's weights P (16 bit) go over the first 64 columns of its own S.
-//    One thread per query tile issues its MMAs, PV(k) then S(k+1): MMAs of one
-//    thread run in order, so S(k+1) finds P(k) consumed, and S(k+1) being
-//    complete says that O is at rest.
-//  * key tiles (128 keys) run from the last to the first: with a distance
-//    bias the nearest keys carry the largest weights, so the reference that a
-//    row's exponents get from its first tile serves the others.  A later tile
-//    skips the row max: its weights 2^(s - ref) only have to stay finite, and
-//    a sum above kBig sends the warp to a slow path that moves the reference
-//    and rescales O.  Tiles between the prefix and the window are skipped.
-//  * the cap's tanh is an odd polynomial of degree 9 on |y| <= 0.8 (minimax,
+//  * Steps of 64 keys: half a 128-key K/V tile.  TMEM (512 columns): two S
+//    buffers of 64 columns and O (head_dim columns) per query tile; a step's
+//    weights P (16 bit) go over the first half of its own S buffer.  One warp
+//    per query tile issues its MMAs, PV(j) then S(j + 2): MMAs of one thread run
+//    in order, so S(j + 2) finds P(j) consumed, and the softmax of step j + 1
+//    runs under both.  (Steps of 128 keys with one S buffer: 205 us instead of
+//    182 on six 640-row chunks with a distance bias; one warp issuing for both
+//    tiles in turn 196; a lock around each tile's products 210.)
+//  * Steps run from the last key to the first: with a distance bias the
+//    nearest keys carry the largest weights, so the reference that a row's
+//    exponents get from its first step serves the others.  A later step skips
+//    the row max: its weights 2^(s - ref) only have to stay finite, and a sum
+//    above BIG sends the warp to the long way that moves the reference and
+//    rescales O.  Tiles between the prefix and the window are skipped.
+//  * The cap's tanh is an odd polynomial of degree 9 on |y| <= 0.8 (minimax,
 //    3.5e-7 absolute), which leaves one special-function operation per score,
-//    the exponential; a tile with a larger |y| takes the exact form, which
-//    needs three.  Special-function throughput (16 lanes a clock an SM) is the
-//    bound: 128 x 128 exponentials take 1024 clocks, the tile's two MMAs 512.
+//    the exponential; a step with a larger |y| takes the exact form, which
+//    needs three.
+//  * Few units (a chunk or two): their keys are cut into up to eight parts,
+//    each a unit of the queue that leaves (reference, sum, O) per row; for each
+//    warp's rows the part that arrives last joins them in the order of the
+//    parts.  Nobody waits for another, and results do not depend on the order
+//    of arrival.  (One 512-row chunk over 8300 keys: 155 -> 112 us.)
 //  * e4m3 pools: blocks land raw (bulk copies), four converter warps write them
-//    as f16 (exact) into the swizzled K and V tiles, V transposed to key-major
-//    order by its d-major blocks, and the queries are rounded to f16; P is f16.
+//    as f16 (exact) into the swizzled K and V tiles, V as rows of d with
+//    their keys contiguous (what its d-major blocks give), and the queries are rounded to f16; P is f16.
+//
+// What bounds it (measured on B200, clocks per step of both query tiles): the
+// products 1280 (S at N = 64 reads its 6 KB of operands per MMA at the shared
+// memory's 128 bytes a clock, 48 instead of 32; PV 64), 2 x 4 x 64 x 32
+// exponentials 1024 at 16 lanes a clock (with what surrounds them 1174 under a
+// distance bias, 1466 under a cap), and 1750 to 2000 in all, the rest being the
+// hand-offs between the two (a step's weights to its next scores).  Six
+// 640-row chunks over up to 2048 cached keys, 32 heads, distance bias: 161 us,
+// 724 TFLOP/s; two 1024-row chunks over 4096 to 8192 keys in e4m3, cap: 343 us,
+// 765 TFLOP/s.
 // Every wait is bounded (2 s, then the error word); TMEM is freed on every path.
 #include <cuda_runtime.h>
 
@@ -810,138 +827,137 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
         }
         const int key0 = h * kHalf;
         const float dist = (float)(pos - key0);
-        {
-          // The first step of a unit, a step with hidden keys, or weights (a
-          // score) that left the fast form's range: the row max, then the
-          // weights, 16 keys at a time over scores already read.  Rolled loops:
-          // this path is taken a few times per unit, and what it costs is
-          // above all fetching its instructions.
-          // The row sees keys [wlo, hi) and [0, pl) of the half tile, a bit each.
-          const int hi = valid ? min(pos + 1, u.len) - key0 : 0;
-          const int wlo = tl.window > 0 ? pos - tl.window + 1 - key0 : 0;
-          const int pl = valid ? u.pfx - key0 : 0;
-          auto below = [](int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull; };
-          const uint64_t vis = below(pl) | (below(hi) & ~below(wlo));
-          // 16 scores -> exponents s - rf in log2 units: masks, keys past the
-          // row's position (their distance has the other sign), and with
-          // `exact` the cap's exact form
-          // the capped pair (y P(y^2)) of two raw scores
-          auto cap2 = [&](float x0, float x1, uint64_t& z) {
-            const uint64_t y = dev::mul2(dev::f2(x0, x1), dev::f2(y_in, y_in));
-            z = dev::mul2(y, y);
-            uint64_t q = dev::fma2(z, poly2[4], poly2[3]);
-            q = dev::fma2(z, q, poly2[2]);
-            q = dev::fma2(z, q, poly2[1]);
-            q = dev::fma2(z, q, poly2[0]);
-            return dev::mul2(y, q);
-          };
-          auto args = [&](int c, float (&a)[16], float rf, bool exact, float& zmax) {
+        // The first step of a unit, a step with hidden keys, or weights (a
+        // score) that left the fast form's range: the row max, then the
+        // weights, 16 keys at a time over scores already read.  Rolled loops:
+        // this path is taken a few times per unit, and what it costs is
+        // above all fetching its instructions.
+        // The row sees keys [wlo, hi) and [0, pl) of the half tile, a bit each.
+        const int hi = valid ? min(pos + 1, u.len) - key0 : 0;
+        const int wlo = tl.window > 0 ? pos - tl.window + 1 - key0 : 0;
+        const int pl = valid ? u.pfx - key0 : 0;
+        auto below = [](int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull; };
+        const uint64_t vis = below(pl) | (below(hi) & ~below(wlo));
+        // 16 scores -> exponents s - rf in log2 units: masks, keys past the
+        // row's position (their distance has the other sign), and with
+        // `exact` the cap's exact form
+        // the capped pair (y P(y^2)) of two raw scores
+        auto cap2 = [&](float x0, float x1, uint64_t& z) {
+          const uint64_t y = dev::mul2(dev::f2(x0, x1), dev::f2(y_in, y_in));
+          z = dev::mul2(y, y);
+          uint64_t q = dev::fma2(z, poly2[4], poly2[3]);
+          q = dev::fma2(z, q, poly2[2]);
+          q = dev::fma2(z, q, poly2[1]);
+          q = dev::fma2(z, q, poly2[0]);
+          return dev::mul2(y, q);
+        };
+        auto args = [&](int c, float (&a)[16], float rf, bool exact, float& zmax) {
+          uint32_t w[16];
+          dev::tmem_ld16(ts + 16 * c, w);
+          const uint32_t v = (uint32_t)(vis >> (16 * c));
+          const float d = dist - (float)(16 * c);
+#pragma unroll
+          for (int i = 0; i < 16; ++i)  // (what a hidden key holds must not choose the cap's form)
+            a[i] = !CAPS || (v & (1u << i)) ? __uint_as_float(w[i]) : 0.f;
+          if constexpr (CAPS) {
+            if (exact) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) a[i] = dev::capped(a[i], cap_in, p.mod.cap_out);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; i += 2) {
+                uint64_t z;
+                const uint64_t y = cap2(a[i], a[i + 1], z);
+                if (SLOPES) {  // (without slopes the raw maximum has decided)
+                  float z0, z1;
+                  dev::f2_split(z, z0, z1);
+                  zmax = dev::max3(zmax, z0, z1);
+                }
+                dev::f2_split(y, a[i], a[i + 1]);
+              }
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float off = SLOPES ? fmaf(-slope, fabsf(d - (float)i), -rf) : -rf;
+            a[i] = (v & (1u << i)) ? (CAPS ? a[i] + off : fmaf(a[i], scale, off)) : -INFINITY;
+          }
+        };
+        bool exact = false;
+        float m, zmax = 0.f;
+        if constexpr (!SLOPES) {
+          // scale and cap are monotone: the raw maximum decides (and with the
+          // raw minimum whether the cap's polynomial serves)
+          float hi_raw = -INFINITY, lo_raw = INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < kHalf / 16; ++c) {
             uint32_t w[16];
             dev::tmem_ld16(ts + 16 * c, w);
             const uint32_t v = (uint32_t)(vis >> (16 * c));
-            const float d = dist - (float)(16 * c);
-#pragma unroll
-            for (int i = 0; i < 16; ++i)  // (what a hidden key holds must not choose the cap's form)
-              a[i] = !CAPS || (v & (1u << i)) ? __uint_as_float(w[i]) : 0.f;
-            if constexpr (CAPS) {
-              if (exact) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) a[i] = dev::capped(a[i], cap_in, p.mod.cap_out);
-              } else {
-#pragma unroll
-                for (int i = 0; i < 16; i += 2) {
-                  uint64_t z;
-                  const uint64_t y = cap2(a[i], a[i + 1], z);
-                  if (SLOPES) {  // (without slopes the raw maximum has decided)
-                    float z0, z1;
-                    dev::f2_split(z, z0, z1);
-                    zmax = dev::max3(zmax, z0, z1);
-                  }
-                  dev::f2_split(y, a[i], a[i + 1]);
-                }
-              }
-            }
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const float off = SLOPES ? fmaf(-slope, fabsf(d - (float)i), -rf) : -rf;
-              a[i] = (v & (1u << i)) ? (CAPS ? a[i] + off : fmaf(a[i], scale, off)) : -INFINITY;
+              const float x = __uint_as_float(w[i]);
+              hi_raw = fmaxf(hi_raw, (v & (1u << i)) ? x : -INFINITY);
+              if (CAPS) lo_raw = fminf(lo_raw, (v & (1u << i)) ? x : INFINITY);
             }
-          };
-          bool exact = false;
-          float m, zmax = 0.f;
-          if constexpr (!SLOPES) {
-            // scale and cap are monotone: the raw maximum decides (and with the
-            // raw minimum whether the cap's polynomial serves)
-            float hi_raw = -INFINITY, lo_raw = INFINITY;
+          }
+          if constexpr (CAPS) {
+            const float most = vis ? fmaxf(fabsf(hi_raw), fabsf(lo_raw)) * y_in : 0.f;
+            exact = __any_sync(0xffffffffu, !(most <= kCapFast));
+            uint64_t z;
+            float capped, other;
+            dev::f2_split(cap2(hi_raw, 0.f, z), capped, other);
+            m = !vis ? -INFINITY : exact ? dev::capped(hi_raw, cap_in, p.mod.cap_out) : capped;
+          } else {
+            m = hi_raw * scale;
+          }
+        } else {
+          for (;;) {
+            m = -INFINITY;
+            zmax = 0.f;
 #pragma unroll 1
             for (int c = 0; c < kHalf / 16; ++c) {
-              uint32_t w[16];
-              dev::tmem_ld16(ts + 16 * c, w);
-              const uint32_t v = (uint32_t)(vis >> (16 * c));
+              float a[16];
+              args(c, a, 0.f, exact, zmax);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float x = __uint_as_float(w[i]);
-                hi_raw = fmaxf(hi_raw, (v & (1u << i)) ? x : -INFINITY);
-                if (CAPS) lo_raw = fminf(lo_raw, (v & (1u << i)) ? x : INFINITY);
-              }
+              for (int i = 0; i < 16; i += 2) m = dev::max3(m, a[i], a[i + 1]);
             }
-            if constexpr (CAPS) {
-              const float most = vis ? fmaxf(fabsf(hi_raw), fabsf(lo_raw)) * y_in : 0.f;
-              exact = __any_sync(0xffffffffu, !(most <= kCapFast));
-              uint64_t z;
-              float capped, other;
-              dev::f2_split(cap2(hi_raw, 0.f, z), capped, other);
-              m = !vis ? -INFINITY : exact ? dev::capped(hi_raw, cap_in, p.mod.cap_out) : capped;
-            } else {
-              m = hi_raw * scale;
-            }
-          } else {
-            for (;;) {
-              m = -INFINITY;
-              zmax = 0.f;
-#pragma unroll 1
-              for (int c = 0; c < kHalf / 16; ++c) {
-                float a[16];
-                args(c, a, 0.f, exact, zmax);
-#pragma unroll
-                for (int i = 0; i < 16; i += 2) m = dev::max3(m, a[i], a[i + 1]);
-              }
-              if (!CAPS || exact || !__any_sync(0xffffffffu, !(zmax <= kCapFast * kCapFast))) break;
-              exact = true;
-            }
+            if (!CAPS || exact || !__any_sync(0xffffffffu, !(zmax <= kCapFast * kCapFast))) break;
+            exact = true;
           }
-          // the reference moves where the weights would grow past 2^8; O is
-          // rescaled once the previous PV is complete
-          const bool move = m > ref + 8.f;
-          const float alpha = move ? dev::ex2(ref - m) : 1.f;
-          if (move) ref = m;
-          lsum *= alpha;
-          if (!first && __any_sync(0xffffffffu, move)) {
-            wait_ok(&pv_done[2 * x + (b ^ 1)], ((sc - 1) >> 1) & 1);
-            dev::tc_fence_after();
+        }
+        // the reference moves where the weights would grow past 2^8; O is
+        // rescaled once the previous PV is complete
+        const bool move = m > ref + 8.f;
+        const float alpha = move ? dev::ex2(ref - m) : 1.f;
+        if (move) ref = m;
+        lsum *= alpha;
+        if (!first && __any_sync(0xffffffffu, move)) {
+          wait_ok(&pv_done[2 * x + (b ^ 1)], ((sc - 1) >> 1) & 1);
+          dev::tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
-              uint32_t w[16];
-              dev::tmem_ld16(to + 16 * c, w);
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t w[16];
+            dev::tmem_ld16(to + 16 * c, w);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * alpha);
-              dev::tmem_st16(to + 16 * c, w);
-            }
+            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * alpha);
+            dev::tmem_st16(to + 16 * c, w);
           }
+        }
 #pragma unroll 1
-          for (int c = 0; c < kHalf / 16; ++c) {
-            float a[16], s2[2] = {0.f, 0.f};
-            args(c, a, ref, exact, zmax);
-            uint32_t pk[8];
+        for (int c = 0; c < kHalf / 16; ++c) {
+          float a[16], s2[2] = {0.f, 0.f};
+          args(c, a, ref, exact, zmax);
+          uint32_t pk[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float e0 = dev::ex2(a[2 * i]), e1 = dev::ex2(a[2 * i + 1]);
-              s2[i & 1] += e0 + e1;
-              pk[i] = T::FP8 ? dev::pack_f16(e0, e1) : dev::pack_bf16(e0, e1);
-            }
-            lsum += s2[0] + s2[1];
-            dev::tmem_st8(ts + 8 * c, pk);
+          for (int i = 0; i < 8; ++i) {
+            const float e0 = dev::ex2(a[2 * i]), e1 = dev::ex2(a[2 * i + 1]);
+            s2[i & 1] += e0 + e1;
+            pk[i] = T::FP8 ? dev::pack_f16(e0, e1) : dev::pack_bf16(e0, e1);
           }
+          lsum += s2[0] + s2[1];
+          dev::tmem_st8(ts + 8 * c, pk);
+        }
         if constexpr (!T::FP8) {
           // V rows that no row of the unit sees may hold anything (0 * NaN):
           // each query tile zeroes them before its own PV (neither waits for
@@ -960,7 +976,6 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
           };
           zero_v(max(0, max(u.len, u.pfx) - key0), min(kHalf, tl.nb * BS - key0));
           zero_v(max(u.pfx, key0) - key0, min(tl.lo, key0 + kHalf) - key0);
-        }
         }
         first = false;
         dev::tc_fence_before();
