@@ -522,8 +522,8 @@ int run_prefill_biased(const pa_cache_desc* d, const pa_score_mod* mod, const vo
 
 int run_biased_simt(const pa_cache_desc* d, const pa_score_mod* mod, const void* q, const void* k_cache,
                     const void* v_cache, const int32_t* block_tables, int32_t max_blocks, const int32_t* seq_lens,
-                    const int32_t* qsl, int32_t num_seqs, int32_t num_rows, float scale, void* out, void* workspace,
-                    cudaStream_t stream, const char* who) {
+                    const int32_t* qsl, int32_t num_seqs, int32_t num_rows, bool singles, bool chunks, float scale,
+                    void* out, void* workspace, cudaStream_t stream, const char* who) {
   BiasedSimtParams b = {};
   SimtParams& p = b.a;
   p.num_blocks = d->num_blocks;
@@ -550,7 +550,7 @@ int run_biased_simt(const pa_cache_desc* d, const pa_score_mod* mod, const void*
     p.v_head = d->v_head_scales;
   }
   b.mod = kernel_mod(mod, scale, 1.f);
-  cudaError_t e = launch_attn_biased_simt(b, d->kv_dtype, stream);
+  cudaError_t e = launch_attn_biased_simt(b, d->kv_dtype, singles, chunks, stream);
   if (e == cudaErrorNotSupported)
     return fail(PA_ERR_UNSUPPORTED, "%s: q dtype %d with kv dtype %d, %d rows", who, d->q_dtype, d->kv_dtype, num_rows);
   return cuda_status(e, who);
@@ -995,7 +995,7 @@ int pa_decode_biased(const pa_cache_desc* d, const pa_score_mod* mod, const void
                              num_seqs, scale, out, workspace, workspace_bytes, st, who);
   if (workspace_bytes < 256) return fail(PA_ERR_INVALID_ARG, "%s: workspace < 256 bytes", who);
   return run_biased_simt(d, mod, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, nullptr, num_seqs,
-                         num_seqs, scale, out, workspace, st, who);
+                         num_seqs, true, false, scale, out, workspace, st, who);
 }
 
 int pa_decode_chunked_prefill_biased(const pa_cache_desc* d, const pa_score_mod* mod, const void* q,
@@ -1015,14 +1015,14 @@ int pa_decode_chunked_prefill_biased(const pa_cache_desc* d, const pa_score_mod*
   if (num_tokens == 0) return PA_OK;
   if (max_q_len == 0) return fail(PA_ERR_INVALID_ARG, "%s: max_q_len 0 with %d tokens", who, num_tokens);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (!biased_tc(d)) {
-    if (workspace_bytes < 256) return fail(PA_ERR_INVALID_ARG, "%s: workspace < 256 bytes", who);
-    return run_biased_simt(d, mod, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, query_start_loc,
-                           num_seqs, num_tokens, scale, out, workspace, st, who);
-  }
   // single-token rows on the decode kernel (there are none when the rows fill
   // every sequence up to max_q_len), the others on the chunk kernel
   const bool decodes = max_q_len == 1 || (int64_t)num_seqs * max_q_len != num_tokens;
+  if (!biased_tc(d)) {
+    if (workspace_bytes < 256) return fail(PA_ERR_INVALID_ARG, "%s: workspace < 256 bytes", who);
+    return run_biased_simt(d, mod, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, query_start_loc,
+                           num_seqs, num_tokens, decodes, max_q_len > 1, scale, out, workspace, st, who);
+  }
   int sms = 0;
   if ((rc = num_sms(&sms))) return rc;
   size_t parts_at = 0;

@@ -1,15 +1,16 @@
 // Biased paged attention on CUDA cores: fp32 queries, whose 1e-4 rules out
-// tensor-core inputs of fewer bits, over an fp32 or e4m3 pool; decode rows and
-// chunks of new tokens alike.
+// tensor-core inputs of fewer bits, over an fp32 or e4m3 pool.
 //
 // Row i of a sequence sees key j if j < prefix, or j <= i and (window) i - j <
 // window; its score is cap * tanh(scale q k / cap) - slope |i - j|, all in
-// fp32.  A CTA takes NP (position, head) pairs of one sequence and kv head, so
-// that a key row read serves several queries; its warps take the visible
-// 16-key tiles in turn, each with its own online softmax, and merge at the
-// end.  With one pair per CTA (few rows: a chain of loads per tile is what
-// bounds it) there are 16 warps and a tile's K and V are loaded together.
-// Bound: latency for short contexts, FMA issue for long.
+// fp32.
+//
+// Row kernel: a CTA takes one (row, head); its warps take the visible 16-key
+// tiles in turn, each with its own online softmax, and merge at the end.  A
+// chain of loads per tile bounds it for short contexts, so there are up to 16
+// warps and a tile's K and V are loaded together (4 sequences of up to 301
+// keys: 9.4 us a call; 16.4 with eight warps and V loaded behind the softmax).
+// Tile kernel, further down: chunks with rows enough to fill it.
 #include <cuda_runtime.h>
 
 #include "pa_device.cuh"
@@ -22,9 +23,10 @@ constexpr int kTile = 16;  // keys of a tile: block sizes are multiples of it
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kHalfLn2 = 0.34657359027997264f;  // cap_in holds 2 log2(e) times what tanh takes
 
-template <typename T, int E>
+// E elements of a key row as fp32: fp32, or e4m3 codes (exact).
+template <int KV, int E>
 __device__ __forceinline__ void load_elems(const uint8_t* base, int64_t idx, float (&x)[E]) {
-  if constexpr (sizeof(T) == 4) {
+  if constexpr (KV == kF32) {
     const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(base) + idx);
 #pragma unroll
     for (int i = 0; i < E / 4; ++i) {
@@ -45,73 +47,57 @@ __device__ __forceinline__ void load_elems(const uint8_t* base, int64_t idx, flo
   }
 }
 
-template <int KV> struct KElem { using T = float; };
-template <> struct KElem<kFP8> { using T = uint8_t; };
-
 // (fp32 rows of 128 elements ahead need the registers of eight warps)
-template <int KV, int D, int NP>
-constexpr int warps_of() { return NP == 1 && (D == 64 || KV == kFP8) ? 16 : 8; }
+template <int KV, int D>
+constexpr int row_warps() { return D == 64 || KV == kFP8 ? 16 : 8; }
 
-template <int KV, int D, int NP>
-__global__ void __launch_bounds__(warps_of<KV, D, NP>() * 32) attn_biased_simt_kernel(const BiasedSimtParams bp) {
+template <int KV, int D>
+__global__ void __launch_bounds__(row_warps<KV, D>() * 32)
+    attn_biased_row_kernel(const BiasedSimtParams bp, bool singles, bool chunks) {
   dev::grid_dep_wait();
   const SimtParams& p = bp.a;
-  constexpr int kWarps = warps_of<KV, D, NP>();
+  constexpr int kWarps = row_warps<KV, D>();
   constexpr int E = D / 8;    // elements of a key row per lane (8 lanes a key, 4 keys a pass)
   constexpr int DV = D / 32;  // elements of the output per lane
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int hq = p.num_q_heads, hkv = p.num_kv_heads, G = hq / hkv, bs = p.block_size;
-  const int kvh = blockIdx.y;
-  // the CTA's pairs: block x of the batch, sequence s's blocks from
-  // floor(first row * G / NP) + s on (at least as many as it needs)
-  auto row0 = [&](int s) { return p.rows.qsl ? p.rows.qsl[s] : s; };
-  auto base = [&](int s) { return (int64_t)row0(s) * G / NP + s; };
-  int lo = 0, hi = p.rows.num_seqs - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (base(mid) <= (int64_t)blockIdx.x) lo = mid; else hi = mid - 1;
+  const int hq = p.num_q_heads, hkv = p.num_kv_heads, bs = p.block_size;
+  const int row = blockIdx.x, h = blockIdx.y, kvh = h / (hq / hkv);
+  int s = row, first = row, qlen = 1;
+  if (p.rows.qsl) {  // the last s with qsl[s] <= row
+    int lo = 0, hi = p.rows.num_seqs - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (p.rows.qsl[mid] <= row) lo = mid; else hi = mid - 1;
+    }
+    s = lo;
+    first = p.rows.qsl[s];
+    qlen = p.rows.qsl[s + 1] - first;
+    if (row < first || row >= first + qlen || !(qlen > 1 ? chunks : singles)) return;
   }
-  const int s = lo, first = row0(s), qlen = row0(s + 1) - first;
-  const int64_t pair0 = ((int64_t)blockIdx.x - base(s)) * NP;
-  const int64_t pairs = (int64_t)qlen * G;
-  if (pair0 >= pairs) return;
-  const int np = (int)min((int64_t)NP, pairs - pair0);
   int len = p.rows.seq_lens[s];
+  const int pos = len - qlen + row - first;
   if ((int64_t)len > (int64_t)p.max_blocks * bs) {  // longer than its table row: flag, clamp
     if (threadIdx.x == 0) atomicCAS(p.err, 0, 3);
     len = p.max_blocks * bs;
   }
-  const int at0 = p.rows.seq_lens[s] - qlen;  // position of the sequence's first query row
   const int W = bp.mod.window;
   const int pfx = bp.mod.prefix ? max(0, min(len, bp.mod.prefix[s])) : 0;
-  const float ks = p.k_head ? __ldg(p.k_head + kvh) : p.k_scale, vs = p.v_head ? __ldg(p.v_head + kvh) : p.v_scale;
-  const float kmul = KV == kFP8 ? ks : 1.f;
-
-  float q[NP][E], acc[NP][DV], m[NP], l[NP], slope[NP];
-  int pos[NP];
+  const float vs = KV != kFP8 ? 1.f : p.v_head ? __ldg(p.v_head + kvh) : p.v_scale;
+  const float kmul = KV != kFP8 ? 1.f : p.k_head ? __ldg(p.k_head + kvh) : p.k_scale;
+  const float slope = bp.mod.slopes ? __ldg(bp.mod.slopes + h) * kLog2e : 0.f;
   const int sub = lane & 7, kg = lane >> 3;
+  float q[E], acc[DV], m = -1e30f, l = 0.f;
+  load_elems<kF32, E>(p.q, ((int64_t)row * hq + h) * D + sub * E, q);
 #pragma unroll
-  for (int n = 0; n < NP; ++n) {
-    const int64_t pr = pair0 + (n < np ? n : 0);
-    const int row = (int)(pr / G), h = kvh * G + (int)(pr % G);
-    pos[n] = at0 + row;
-    slope[n] = bp.mod.slopes ? __ldg(bp.mod.slopes + h) * kLog2e : 0.f;
-    load_elems<float, E>(p.q, ((int64_t)(first + row) * hq + h) * D + sub * E, q[n]);
-    m[n] = -1e30f;
-    l[n] = 0.f;
-#pragma unroll
-    for (int e = 0; e < DV; ++e) acc[n][e] = 0.f;
-  }
-  // tiles with a key that some pair sees: [0, tp) of the prefix and [tl, te)
-  const int plo = at0 + (int)(pair0 / G), phi = at0 + (int)((pair0 + np - 1) / G);
-  const int end = min(len, max(phi + 1, pfx));
-  const int wlo = W > 0 ? max(0, plo - W + 1) : 0;
+  for (int e = 0; e < DV; ++e) acc[e] = 0.f;
+  // tiles with a visible key: [0, tp) of the prefix and [tl, te)
+  const int end = min(len, max(pos + 1, pfx)), wlo = W > 0 ? max(0, pos - W + 1) : 0;
   const int tp = (pfx + kTile - 1) / kTile, tl = max(tp, wlo / kTile), te = (end + kTile - 1) / kTile;
   const int ntiles = tp + max(0, te - tl);
+  auto seen = [&](int key) { return key < len && (key < pfx || (key <= pos && key >= wlo)); };
   const int32_t* table = p.block_tables + (int64_t)s * p.max_blocks;
   for (int i = warp; i < ntiles; i += kWarps) {
-    const int tile = i < tp ? i : i - tp + tl;
-    const int key0 = tile * kTile;
+    const int key0 = (i < tp ? i : i - tp + tl) * kTile;
     int64_t blk = __ldg(table + key0 / bs);
     if (blk < 0 || blk >= p.num_blocks) {  // bad table entry: flag it, read block 0
       if (lane == 0) atomicCAS(p.err, 0, 2);
@@ -119,175 +105,355 @@ __global__ void __launch_bounds__(warps_of<KV, D, NP>() * 32) attn_biased_simt_k
     }
     const int off = key0 % bs;
     const int64_t kb = ((blk * hkv + kvh) * bs + off) * D;
-    // key 4 j + kg of the tile, and this lane's V elements (with several pairs
-    // loaded where they are used: registers)
-    constexpr bool kAhead = NP == 1;
-    float kall[kAhead ? 4 : 1][E];
-    float2 vall[kAhead && KV != kFP8 ? kTile : 1][DV / 2];
-    uint4 raw[KV == kFP8 ? DV : 1];
-    if constexpr (kAhead) {
+    float kx[4][E];  // keys 4 j + kg
+    float2 vx[KV == kF32 ? kTile : 1][DV / 2];
+    uint4 raw[KV == kFP8 ? DV : 1];  // d-major: 16 keys of an element are contiguous
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        load_elems<typename KElem<KV>::T, E>(p.k_cache, kb + (4 * j + kg) * D + sub * E, kall[j]);
-      if constexpr (KV != kFP8) {
+    for (int j = 0; j < 4; ++j) load_elems<KV, E>(p.k_cache, kb + (4 * j + kg) * D + sub * E, kx[j]);
+    if constexpr (KV == kF32) {
 #pragma unroll
-        for (int k = 0; k < kTile; ++k)
+      for (int k = 0; k < kTile; ++k)
 #pragma unroll
-          for (int e = 0; e < DV / 2; ++e)
-            vall[k][e] = __ldg(reinterpret_cast<const float2*>(p.v_cache) + (kb + k * D + lane * DV) / 2 + e);
-      }
-    }
-    if constexpr (KV == kFP8) {
+        for (int e = 0; e < DV / 2; ++e)
+          vx[k][e] = __ldg(reinterpret_cast<const float2*>(p.v_cache) + (kb + k * D + lane * DV) / 2 + e);
+    } else {
 #pragma unroll
       for (int e = 0; e < DV; ++e)
         raw[e] = __ldg(reinterpret_cast<const uint4*>(p.v_cache + ((blk * hkv + kvh) * D + lane * DV + e) * bs + off));
     }
-    float sc[NP][4];
+    float sc[4], w[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      float kx[E];
-      if constexpr (kAhead) {
+      float dot = 0.f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) kx[e] = kall[j][e];
-      } else {
-        load_elems<typename KElem<KV>::T, E>(p.k_cache, kb + (4 * j + kg) * D + sub * E, kx);
-      }
+      for (int e = 0; e < E; ++e) dot = fmaf(q[e], kx[j][e], dot);
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
       const int key = key0 + 4 * j + kg;
-#pragma unroll
-      for (int n = 0; n < NP; ++n) {
-        float dot = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) dot = fmaf(q[n][e], kx[e], dot);
-#pragma unroll
-        for (int o = 4; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        const bool seen = key < len && (key < pfx || (key <= pos[n] && (W <= 0 || pos[n] - key < W)));
-        // (tanhf: fp32 rows are held to fp32's rounding, and latency bounds)
-        const float x = bp.mod.cap_out > 0.f ? bp.mod.cap_out * tanhf(dot * (bp.mod.cap_in * kmul * kHalfLn2))
-                                             : dot * (p.scale * kLog2e * kmul);
-        sc[n][j] = seen ? fmaf(-slope[n], fabsf((float)(pos[n] - key)), x) : -INFINITY;
-      }
+      // (tanhf: fp32 rows are held to fp32's rounding, and latency bounds)
+      const float x = bp.mod.cap_out > 0.f ? bp.mod.cap_out * tanhf(dot * (bp.mod.cap_in * kmul * kHalfLn2))
+                                           : dot * (p.scale * kLog2e * kmul);
+      sc[j] = seen(key) ? fmaf(-slope, fabsf((float)(pos - key)), x) : -INFINITY;
     }
-    float pr[NP][4];
+    float mx = fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3]));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+    const float mn = fmaxf(m, mx), al = dev::ex2(m - mn);
+    m = mn;
+    l *= al;
 #pragma unroll
-    for (int n = 0; n < NP; ++n) {
-      float mx = fmaxf(fmaxf(sc[n][0], sc[n][1]), fmaxf(sc[n][2], sc[n][3]));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-      const float mn = fmaxf(m[n], mx), al = dev::ex2(m[n] - mn);
-      m[n] = mn;
-      l[n] *= al;
+    for (int e = 0; e < DV; ++e) acc[e] *= al;
 #pragma unroll
-      for (int e = 0; e < DV; ++e) acc[n][e] *= al;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        pr[n][j] = dev::ex2(sc[n][j] - mn);
-        l[n] += pr[n][j];  // per key group: the groups are added at the end
-      }
+    for (int j = 0; j < 4; ++j) {
+      w[j] = dev::ex2(sc[j] - mn);
+      l += w[j];  // per key group: the groups are added at the end
     }
-    // O += P V, key by key; a key that no pair sees is skipped (its V may be
-    // anything: 0 * NaN)
-    if constexpr (KV != kFP8) {
+    // O += P V, key by key; a hidden key is skipped (its V may be anything: 0 * NaN)
 #pragma unroll
-      for (int k = 0; k < kTile; ++k) {
-        const int key = key0 + k;
-        const bool any = key < len && (key < pfx || (key <= phi && key >= wlo));
-        if (!any) continue;
-        float vx[DV];
-        const int64_t vb = kb + (int64_t)k * D + lane * DV;
+    for (int k = 0; k < kTile; ++k) {
+      if (!seen(key0 + k)) continue;
+      const float wk = __shfl_sync(0xffffffffu, w[k >> 2], (k & 3) * 8);
 #pragma unroll
-        for (int e = 0; e < DV; e += 2) {
-          float2 v;
-          if constexpr (kAhead) v = vall[k][e / 2];
-          else v = __ldg(reinterpret_cast<const float2*>(reinterpret_cast<const float*>(p.v_cache) + vb + e));
-          vx[e] = v.x;
-          vx[e + 1] = v.y;
-        }
-#pragma unroll
-        for (int n = 0; n < NP; ++n) {
-          const float w = __shfl_sync(0xffffffffu, pr[n][k >> 2], (k & 3) * 8);
-#pragma unroll
-          for (int e = 0; e < DV; ++e) acc[n][e] = fmaf(w, vx[e], acc[n][e]);
-        }
-      }
-    } else {  // d-major: 16 keys of an element are contiguous
-#pragma unroll
-      for (int k = 0; k < kTile; ++k) {
-        const int key = key0 + k;
-        const bool any = key < len && (key < pfx || (key <= phi && key >= wlo));
-        if (!any) continue;
-        float w[NP];
-#pragma unroll
-        for (int n = 0; n < NP; ++n) w[n] = __shfl_sync(0xffffffffu, pr[n][k >> 2], (k & 3) * 8);
-#pragma unroll
-        for (int e = 0; e < DV; ++e) {
+      for (int e = 0; e < DV; ++e) {
+        float v;
+        if constexpr (KV == kF32) {
+          v = e & 1 ? vx[k][e / 2].y : vx[k][e / 2].x;
+        } else {
           const uint32_t r[4] = {raw[e].x, raw[e].y, raw[e].z, raw[e].w};
-          const float v = dev::e4m3_to_f32((r[k >> 2] >> (8 * (k & 3))) & 0xFFu);
-#pragma unroll
-          for (int n = 0; n < NP; ++n) acc[n][e] = fmaf(w[n], v, acc[n][e]);
+          v = dev::e4m3_to_f32((r[k >> 2] >> (8 * (k & 3))) & 0xFFu);
         }
+        acc[e] = fmaf(wk, v, acc[e]);
       }
     }
   }
   // ---- merge the warps ----
-  __shared__ float sm[kWarps][NP], sl[kWarps][NP], sa[kWarps][NP][D];
-#pragma unroll
-  for (int n = 0; n < NP; ++n) {
-    float t = l[n];  // lanes of a key group hold the same sum
-    t += __shfl_xor_sync(0xffffffffu, t, 8);
-    t += __shfl_xor_sync(0xffffffffu, t, 16);
-    if (lane == 0) {
-      sm[warp][n] = m[n];
-      sl[warp][n] = t;
-    }
-#pragma unroll
-    for (int e = 0; e < DV; ++e) sa[warp][n][lane * DV + e] = acc[n][e];
+  __shared__ float sm[kWarps], sl[kWarps], sa[kWarps][D];
+  l += __shfl_xor_sync(0xffffffffu, l, 8);  // (the lanes of a key group hold the same sum)
+  l += __shfl_xor_sync(0xffffffffu, l, 16);
+  if (lane == 0) {
+    sm[warp] = m;
+    sl[warp] = l;
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < np * D; i += kWarps * 32) {
-    const int n = i / D, d = i % D;
-    float M = sm[0][n];
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) M = fmaxf(M, sm[w][n]);
+  for (int e = 0; e < DV; ++e) sa[warp][lane * DV + e] = acc[e];
+  __syncthreads();
+  if (threadIdx.x < D) {
+    float M = sm[0];
+#pragma unroll
+    for (int i = 1; i < kWarps; ++i) M = fmaxf(M, sm[i]);
     float L = 0.f, o = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float a = dev::ex2(sm[w][n] - M);
-      L = fmaf(sl[w][n], a, L);
-      o = fmaf(sa[w][n][d], a, o);
+    for (int i = 0; i < kWarps; ++i) {
+      const float a = dev::ex2(sm[i] - M);
+      L = fmaf(sl[i], a, L);
+      o = fmaf(sa[i][threadIdx.x], a, o);
     }
-    const int64_t pr = pair0 + n;
-    const int64_t at = ((int64_t)(first + pr / G) * hq + kvh * G + pr % G) * D + d;
-    const float x = L > 0.f ? o / L * (KV == kFP8 ? vs : 1.f) : 0.f;  // an empty context: a zero row
-    reinterpret_cast<float*>(p.out)[at] = x;
+    // nothing visible: a zero row; NaN stays
+    reinterpret_cast<float*>(p.out)[((int64_t)row * hq + h) * D + threadIdx.x] =
+        L > 0.f ? o / L * vs : (L == 0.f ? 0.f : L);
   }
 }
 
-template <int KV, int D, int NP>
-cudaError_t launch(const BiasedSimtParams& p, cudaStream_t stream) {
+// ---- chunks ----------------------------------------------------------------
+// The rows of sequences with more than one: 64 (position, head) pairs of one
+// sequence and kv head against tiles of 64 keys, both products in registers:
+// a thread has 4 x 4 scores and 4 x D / 16 outputs, so that eight (then ten)
+// shared-memory vectors feed 64 (128) FMAs.  Bound: FMA issue and the shared
+// memory's loads (256 rows of 32 heads over 4000 keys, twice: 1.85 ms, 18
+// TFLOP/s; the row kernel with four pairs per CTA took 6.7 ms).
+constexpr int kR = 64;   // pairs of a CTA
+constexpr int kKT = 64;  // keys of a tile
+constexpr int kTileThreads = 256;
+template <int D>
+constexpr int tile_smem() { return (kR * (D + 4) + 2 * kKT * (D + 4) + kR * (kKT + 4)) * 4; }
+
+template <int KV, int D>
+__global__ void __launch_bounds__(kTileThreads, 2) attn_biased_tile_kernel(const BiasedSimtParams bp) {
+  dev::grid_dep_wait();
+  extern __shared__ float4 smem4[];
+  constexpr int LD = D + 4, LP = kKT + 4, DC = D / 64;  // padded rows; 64-column groups of the outputs
+  float* qs = reinterpret_cast<float*>(smem4);
+  float* ks = qs + kR * LD;
+  float* vs = ks + kKT * LD;
+  float* ps = vs + kKT * LD;
+  const SimtParams& p = bp.a;
+  const int hq = p.num_q_heads, hkv = p.num_kv_heads, G = hq / hkv, bs = p.block_size, kvh = blockIdx.y;
+  auto base = [&](int s) { return (int64_t)p.rows.qsl[s] * G / kR + s; };
+  int lo = 0, hi = p.rows.num_seqs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (base(mid) <= (int64_t)blockIdx.x) lo = mid; else hi = mid - 1;
+  }
+  const int s = lo, first = p.rows.qsl[s], qlen = p.rows.qsl[s + 1] - first;
+  if (qlen <= 1) return;  // single rows are the other kernel's
+  const int64_t pair0 = ((int64_t)blockIdx.x - base(s)) * kR, pairs = (int64_t)qlen * G;
+  if (pair0 >= pairs) return;
+  const int np = (int)min((int64_t)kR, pairs - pair0);
+  int len = p.rows.seq_lens[s];
+  const int at0 = len - qlen;  // position of the sequence's first query row
+  if ((int64_t)len > (int64_t)p.max_blocks * bs) {  // longer than its table row: flag, clamp
+    if (threadIdx.x == 0) atomicCAS(p.err, 0, 3);
+    len = p.max_blocks * bs;
+  }
+  const int W = bp.mod.window;
+  const int pfx = bp.mod.prefix ? max(0, min(len, bp.mod.prefix[s])) : 0;
+  const float kmul = KV != kFP8 ? 1.f : p.k_head ? __ldg(p.k_head + kvh) : p.k_scale;
+  const float vmul = KV != kFP8 ? 1.f : p.v_head ? __ldg(p.v_head + kvh) : p.v_scale;
+  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+
+  for (int i = tid; i < kR * (D / 4); i += kTileThreads) {
+    const int r = i / (D / 4), c = i % (D / 4);
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < np) {
+      const int64_t pr = pair0 + r;
+      x = __ldg(reinterpret_cast<const float4*>(p.q) + (((int64_t)(first + pr / G)) * hq + kvh * G + pr % G) * (D / 4) + c);
+    }
+    *reinterpret_cast<float4*>(qs + r * LD + 4 * c) = x;
+  }
+  float acc[4][4 * DC], m[4], l[4], slope[4];
+  int pos[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t pr = pair0 + min(4 * ty + i, np - 1);
+    pos[i] = at0 + (int)(pr / G);
+    slope[i] = bp.mod.slopes ? __ldg(bp.mod.slopes + kvh * G + pr % G) * kLog2e : 0.f;
+    m[i] = -1e30f;
+    l[i] = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4 * DC; ++e) acc[i][e] = 0.f;
+  }
+  // tiles with a key that some pair sees: [0, tp) of the prefix and [tl, te)
+  const int plo = at0 + (int)(pair0 / G), phi = at0 + (int)((pair0 + np - 1) / G);
+  const int end = min(len, max(phi + 1, pfx)), wlo = W > 0 ? max(0, plo - W + 1) : 0;
+  const int tp = (pfx + kKT - 1) / kKT, tl = max(tp, wlo / kKT), te = (end + kKT - 1) / kKT;
+  const int ntiles = tp + max(0, te - tl);
+  const int32_t* table = p.block_tables + (int64_t)s * p.max_blocks;
+  auto seen_by_some = [&](int key) { return key < end && (key < pfx || (key >= wlo && key <= phi)); };
+  auto block_of = [&](int key) {
+    int64_t blk = __ldg(table + key / bs);
+    if (blk < 0 || blk >= p.num_blocks) {  // bad table entry: flag it, read block 0
+      atomicCAS(p.err, 0, 2);
+      blk = 0;
+    }
+    return blk;
+  };
+  const float scale2 = p.scale * kLog2e * kmul;
+  for (int t = 0; t < ntiles; ++t) {
+    const int key0 = (t < tp ? t : t - tp + tl) * kKT;
+    __syncthreads();  // the previous tile has been read
+    // K and V rows; those that no pair sees are 0 (their V may be anything: 0 * NaN)
+    for (int i = tid; i < kKT * (D / 4); i += kTileThreads) {
+      const int k = i / (D / 4), c = i % (D / 4), key = key0 + k;
+      float4 kx = make_float4(0.f, 0.f, 0.f, 0.f), vx = kx;
+      if (seen_by_some(key)) {
+        const int64_t at = ((block_of(key) * hkv + kvh) * bs + key % bs) * D + 4 * c;
+        if constexpr (KV == kF32) {
+          kx = __ldg(reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p.k_cache) + at));
+          vx = __ldg(reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p.v_cache) + at));
+        } else {
+          const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(p.k_cache + at));
+          kx = make_float4(dev::e4m3_to_f32(w & 0xFFu), dev::e4m3_to_f32((w >> 8) & 0xFFu),
+                           dev::e4m3_to_f32((w >> 16) & 0xFFu), dev::e4m3_to_f32(w >> 24));
+        }
+      }
+      *reinterpret_cast<float4*>(ks + k * LD + 4 * c) = kx;
+      if constexpr (KV == kF32) *reinterpret_cast<float4*>(vs + k * LD + 4 * c) = vx;
+    }
+    if constexpr (KV == kFP8) {  // d-major: 16 keys of an element are contiguous
+      for (int i = tid; i < D * (kKT / 16); i += kTileThreads) {
+        const int d = i % D, k0 = i / D * 16, key = key0 + k0;
+        bool any = false;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) any = any || seen_by_some(key + k);
+        uint4 raw = make_uint4(0, 0, 0, 0);
+        if (any)
+          raw = __ldg(reinterpret_cast<const uint4*>(p.v_cache + ((block_of(key) * hkv + kvh) * D + d) * bs + key % bs));
+        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          vs[(k0 + k) * LD + d] = seen_by_some(key + k) ? dev::e4m3_to_f32((w[k >> 2] >> (8 * (k & 3))) & 0xFFu) : 0.f;
+      }
+    }
+    __syncthreads();
+    // ---- scores of rows 4 ty + i and keys tx + 16 j ----
+    float sc[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sc[i][j] = 0.f;
+#pragma unroll 4
+    for (int c = 0; c < D; c += 4) {
+      float4 a[4], b[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        a[i] = *reinterpret_cast<const float4*>(qs + (4 * ty + i) * LD + c);
+        b[i] = *reinterpret_cast<const float4*>(ks + (tx + 16 * i) * LD + c);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          sc[i][j] = fmaf(a[i].x, b[j].x, sc[i][j]);
+          sc[i][j] = fmaf(a[i].y, b[j].y, sc[i][j]);
+          sc[i][j] = fmaf(a[i].z, b[j].z, sc[i][j]);
+          sc[i][j] = fmaf(a[i].w, b[j].w, sc[i][j]);
+        }
+    }
+    // ---- cap, bias, masks, online softmax per row (16 lanes) ----
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float mx = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int key = key0 + tx + 16 * j;
+        const bool seen = key < len && (key < pfx || (key <= pos[i] && (W <= 0 || pos[i] - key < W)));
+        const float x = bp.mod.cap_out > 0.f ? bp.mod.cap_out * tanhf(sc[i][j] * (bp.mod.cap_in * kmul * kHalfLn2))
+                                             : sc[i][j] * scale2;
+        sc[i][j] = seen ? fmaf(-slope[i], fabsf((float)(pos[i] - key)), x) : -INFINITY;
+        mx = fmaxf(mx, sc[i][j]);
+      }
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const float mn = fmaxf(m[i], mx), al = dev::ex2(m[i] - mn);
+      m[i] = mn;
+      l[i] *= al;
+#pragma unroll
+      for (int e = 0; e < 4 * DC; ++e) acc[i][e] *= al;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float w = dev::ex2(sc[i][j] - mn);
+        l[i] += w;  // this lane's keys: the lanes are added at the end
+        ps[(4 * ty + i) * LP + tx + 16 * j] = w;
+      }
+    }
+    __syncwarp();  // a row's weights are written and read by the same half warp
+    // ---- O += P V: rows 4 ty + i, columns 64 c + 4 tx .. + 3 ----
+#pragma unroll 2
+    for (int k = 0; k < kKT; k += 4) {
+      float4 w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(ps + (4 * ty + i) * LP + k);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+        for (int c = 0; c < DC; ++c) {
+          const float4 v = *reinterpret_cast<const float4*>(vs + (k + kk) * LD + 64 * c + 4 * tx);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float x = kk == 0 ? w[i].x : kk == 1 ? w[i].y : kk == 2 ? w[i].z : w[i].w;
+            acc[i][4 * c] = fmaf(x, v.x, acc[i][4 * c]);
+            acc[i][4 * c + 1] = fmaf(x, v.y, acc[i][4 * c + 1]);
+            acc[i][4 * c + 2] = fmaf(x, v.z, acc[i][4 * c + 2]);
+            acc[i][4 * c + 3] = fmaf(x, v.w, acc[i][4 * c + 3]);
+          }
+        }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float sum = l[i];
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (4 * ty + i >= np) continue;
+    const float inv = sum > 0.f ? vmul / sum : (sum == 0.f ? 0.f : sum);  // nothing visible: 0; NaN stays
+    const int64_t pr = pair0 + 4 * ty + i;
+    float4* out = reinterpret_cast<float4*>(p.out) + ((int64_t)(first + pr / G) * hq + kvh * G + pr % G) * (D / 4);
+#pragma unroll
+    for (int c = 0; c < DC; ++c)
+      out[16 * c + tx] = make_float4(acc[i][4 * c] * inv, acc[i][4 * c + 1] * inv, acc[i][4 * c + 2] * inv,
+                                     acc[i][4 * c + 3] * inv);
+  }
+}
+
+template <int KV, int D>
+cudaError_t launch_tiles(const BiasedSimtParams& p, cudaStream_t stream) {
   const int G = p.a.num_q_heads / p.a.num_kv_heads;
-  const int64_t blocks = (int64_t)p.a.rows.num_rows * G / NP + p.a.rows.num_seqs;
+  const int64_t blocks = (int64_t)p.a.rows.num_rows * G / kR + p.a.rows.num_seqs;
   if (blocks > INT32_MAX || p.a.num_kv_heads > 65535) return cudaErrorNotSupported;
-  attn_biased_simt_kernel<KV, D, NP><<<dim3((unsigned)blocks, (unsigned)p.a.num_kv_heads),
-                                             warps_of<KV, D, NP>() * 32, 0, stream>>>(p);
+  auto kern = attn_biased_tile_kernel<KV, D>;
+  static int set_for[64] = {0};  // the shared memory limit is raised once per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !set_for[dev]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, tile_smem<D>());
+    if (e != cudaSuccess) return e;
+    if (dev < 64) set_for[dev] = 1;
+  }
+  kern<<<dim3((unsigned)blocks, (unsigned)p.a.num_kv_heads), kTileThreads, tile_smem<D>(), stream>>>(p);
   return cudaGetLastError();
 }
 
-// Pairs per CTA: one where there are few (a decode batch: short chains per
-// warp count), else four.
+// The tile kernel where the chunks' pairs make 32 CTAs of it or more (below
+// that the row kernel's many short CTAs are faster: 33 rows of 8 heads over 500
+// keys 33 us against 120, 512 over 1000 580 against 309).
+template <int KV, int D>
+cudaError_t launch_rows(const BiasedSimtParams& p, bool singles, bool chunks, cudaStream_t stream) {
+  const bool tiles = chunks && (int64_t)p.a.rows.num_rows * p.a.num_q_heads >= 32 * kR;
+  const bool rows = singles || (chunks && !tiles);
+  if (p.a.num_q_heads > 65535) return cudaErrorNotSupported;
+  if (rows) {
+    attn_biased_row_kernel<KV, D><<<dim3((unsigned)p.a.rows.num_rows, (unsigned)p.a.num_q_heads),
+                                    row_warps<KV, D>() * 32, 0, stream>>>(p, singles, chunks && !tiles);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || !tiles) return e;
+  }
+  return tiles ? launch_tiles<KV, D>(p, stream) : cudaSuccess;
+}
+
 template <int KV>
-cudaError_t launch_d(const BiasedSimtParams& p, cudaStream_t stream) {
-  const int64_t pairs = (int64_t)p.a.rows.num_rows * p.a.num_q_heads;
-  const bool few = pairs <= 1024 || (p.a.num_q_heads == p.a.num_kv_heads && !p.a.rows.qsl);
-  if (p.a.head_dim == 64) return few ? launch<KV, 64, 1>(p, stream) : launch<KV, 64, 4>(p, stream);
-  if (p.a.head_dim == 128) return few ? launch<KV, 128, 1>(p, stream) : launch<KV, 128, 4>(p, stream);
+cudaError_t launch_d(const BiasedSimtParams& p, bool singles, bool chunks, cudaStream_t stream) {
+  if (p.a.head_dim == 64) return launch_rows<KV, 64>(p, singles, chunks, stream);
+  if (p.a.head_dim == 128) return launch_rows<KV, 128>(p, singles, chunks, stream);
   return cudaErrorNotSupported;
 }
 
 }  // namespace
 
-cudaError_t launch_attn_biased_simt(const BiasedSimtParams& p, int kv_dtype, cudaStream_t stream) {
-  if (kv_dtype == kF32) return launch_d<kF32>(p, stream);
-  if (kv_dtype == kFP8) return launch_d<kFP8>(p, stream);
+cudaError_t launch_attn_biased_simt(const BiasedSimtParams& p, int kv_dtype, bool singles, bool chunks,
+                                    cudaStream_t stream) {
+  if (kv_dtype == kF32) return launch_d<kF32>(p, singles, chunks, stream);
+  if (kv_dtype == kFP8) return launch_d<kFP8>(p, singles, chunks, stream);
   return cudaErrorNotSupported;
 }
 

@@ -275,12 +275,14 @@ struct SimtParams {
   int32_t num_blocks;      // table entries outside [0, num_blocks) are flagged and read as block 0
   int32_t* err;            // error word of the caller's workspace
 };
-// Biased attention of every row of a step on CUDA cores (fp32 queries).
+// Biased attention on CUDA cores (fp32 queries): of the sequences with one row
+// (`singles`; qsl nullptr: every sequence) and of those with more (`chunks`).
 struct BiasedSimtParams {
   SimtParams a;
   ScoreMod mod;
 };
-cudaError_t launch_attn_biased_simt(const BiasedSimtParams& p, int kv_dtype, cudaStream_t stream);
+cudaError_t launch_attn_biased_simt(const BiasedSimtParams& p, int kv_dtype, bool singles, bool chunks,
+                                    cudaStream_t stream);
 cudaError_t launch_attn_simt(const SimtParams& p, int q_dtype, int kv_dtype, cudaStream_t stream);
 
 }  // namespace pa

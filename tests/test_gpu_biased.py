@@ -224,6 +224,19 @@ def test_few_rows_over_long_contexts(hq, hkv, d, bs, kv, mod, cuda_device):
         b.check()
 
 
+@pytest.mark.parametrize("mod", [dict(cap=30.0), dict(window=77, prefix="some", slopes=True)], ids=str)
+@pytest.mark.parametrize("hq,hkv,d,bs,kv", [(8, 2, 128, 16, "f32"), (6, 2, 64, 32, "f32"), (16, 1, 128, 32, "e4m3"),
+                                            (8, 8, 64, 16, "e4m3")])
+def test_fp32_chunks_in_tiles(hq, hkv, d, bs, kv, mod, cuda_device):
+    """fp32 chunks with rows enough for the tile kernel, a single row and an empty sequence among them."""
+    lens = [400, 9, 300, 65]
+    b = Batch(cuda_device, [290, 0, 100, 1], lens, hq, hkv, d, bs, kv, "f32", **prefix_of(mod, lens), seed=d,
+              head_scales=kv == "e4m3")
+    assert 391 * hq >= 2048
+    b.run(decode=False)
+    b.check()
+
+
 def test_many_chunks(cuda_device):
     """More chunks than are put in order, between decode rows and empty sequences."""
     rng = np.random.default_rng(2)
