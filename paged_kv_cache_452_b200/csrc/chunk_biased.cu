@@ -85,7 +85,9 @@ struct C {
   static constexpr int NK = FP8 ? 2 : D == 64 ? 4 : 3, NV = FP8 || D == 128 ? 2 : 4;  // K and V tiles in shared memory
   static constexpr int NR = FP8 ? 2 : 0;            // raw tiles
   static constexpr int THREADS = FP8 ? 512 : 384;
-  static constexpr int READERS = FP8 ? 14 : 10;     // roles that read a queue entry
+  // warps that read a queue entry: the V loader, the two MMA warps, the eight
+  // softmax warps, in e4m3 the four converters
+  static constexpr int READERS = 1 + 2 + 8 + (FP8 ? 4 : 0);
   // weights stay at most this in a tile's sum before the reference moves:
   // bf16 has fp32's range, f16 ends at 65504
   static constexpr float BIG = FP8 ? 16384.f : 18446744073709551616.f;

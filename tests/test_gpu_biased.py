@@ -247,6 +247,16 @@ def test_many_chunks(cuda_device):
     b.check()
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_many_units_per_sm(kv, cuda_device):
+    """Every CTA takes its queue entries many times over: 330 two-row chunks of 32 kv heads."""
+    rng = np.random.default_rng(4)
+    lens = [int(n) for n in rng.integers(2, 60, 330)]
+    b = Batch(cuda_device, [2] * 330, lens, 32, 32, 64, 16, kv, "bf16", cap=20.0, seed=4, spoil=False)
+    b.run(decode=False)
+    b.check()
+
+
 def test_rows_of_others_stay(cuda_device):
     """A row past the last sequence's, as in a padded batch, keeps what it held."""
     for kv in ("bf16", "e4m3"):
