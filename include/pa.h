@@ -397,7 +397,11 @@ int pa_decode_biased(const pa_cache_desc* desc, const pa_score_mod* mod, const v
 /* pa_decode_chunked_prefill_biased: pa_decode_chunked_prefill under `mod`, for
  * a mixed step.  A prefix may reach past a row's own position, up to the
  * sequence's last token (whose K/V are in the pool).  Arguments, errors and
- * the workspace as for pa_decode_chunked_prefill and pa_decode_biased. */
+ * the workspace as for pa_decode_chunked_prefill and pa_decode_biased, but
+ * num_tokens may be above query_start_loc[num_seqs] (a step padded to a fixed
+ * size): the rows past it are left as they were.  A V row that some rows of a
+ * sequence see has to be finite: the weight 0 of a row that does not see it
+ * still multiplies it. */
 int pa_decode_chunked_prefill_biased(const pa_cache_desc* desc, const pa_score_mod* mod, const void* q,
                                      const void* k_cache, const void* v_cache, const int32_t* block_tables,
                                      int32_t max_blocks_per_seq, const int32_t* query_start_loc,

@@ -1015,13 +1015,14 @@ int pa_decode_chunked_prefill_biased(const pa_cache_desc* d, const pa_score_mod*
   if (num_tokens == 0) return PA_OK;
   if (max_q_len == 0) return fail(PA_ERR_INVALID_ARG, "%s: max_q_len 0 with %d tokens", who, num_tokens);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // single-token rows on the decode kernel (there are none when the rows fill
-  // every sequence up to max_q_len), the others on the chunk kernel
+  // single-token rows on the decode kernel, the others on the chunk kernel.
+  // Rows that would fill every sequence up to max_q_len leave no single ones,
+  // unless some of them lie past the last sequence's: the chunk kernel has all.
   const bool decodes = max_q_len == 1 || (int64_t)num_seqs * max_q_len != num_tokens;
   if (!biased_tc(d)) {
     if (workspace_bytes < 256) return fail(PA_ERR_INVALID_ARG, "%s: workspace < 256 bytes", who);
     return run_biased_simt(d, mod, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, query_start_loc,
-                           num_seqs, num_tokens, decodes, max_q_len > 1, scale, out, workspace, st, who);
+                           num_seqs, num_tokens, true, max_q_len > 1, scale, out, workspace, st, who);
   }
   int sms = 0;
   if ((rc = num_sms(&sms))) return rc;

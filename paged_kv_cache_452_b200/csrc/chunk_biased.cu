@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
   // ---- unit blocks of each group of sequences, exclusive prefix --------------
   auto blocks_of = [&](int s) {
     const int q = s < S ? p.rows.qsl[s + 1] - p.rows.qsl[s] : 0;
-    return q > 1 ? (q + QB2 - 1) / QB2 : 0;  // single rows are the decode kernel's
+    return q > p.after_decode ? (q + QB2 - 1) / QB2 : 0;  // (single rows are the decode kernel's, if it ran)
   };
   const int groups = (S + kGroup - 1) / kGroup;
   // The chunks by falling context where there are few (long units first leave

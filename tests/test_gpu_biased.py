@@ -272,6 +272,31 @@ def test_rows_of_others_stay(cuda_device):
         b.check()
 
 
+@pytest.mark.parametrize("kv,q", [("bf16", "bf16"), ("e4m3", "bf16"), ("f32", "f32"), ("e4m3", "f32")])
+def test_padding_that_looks_like_full_chunks(kv, q, cuda_device):
+    """num_seqs * max_q_len rows of which the last lie past every sequence's: the single rows are still computed."""
+    b = Batch(cuda_device, [1, 7, 1, 0], [90, 33, 200, 12], 8, 2, 64, 16, kv, q, cap=30.0, window=50, seed=6)
+    rows, full = b.q.shape[0], 28
+    kept = b.q
+    b.q = torch.cat([kept, torch.full((full - rows, 8, 64), float("nan"), dtype=kept.dtype, device=cuda_device)])
+    b.out = torch.full((full, 8, 64), 3.0, dtype=kept.dtype, device=cuda_device)
+    b.ws = pa.alloc_workspace(pa.pa_biased_workspace_size(b.desc, 4, full), cuda_device)
+    b.run(decode=False)
+    torch.cuda.synchronize()
+    assert bool((b.out[rows:] == 3).all())
+    b.q, b.out = kept, b.out[:rows].contiguous()
+    b.check()
+
+
+@pytest.mark.parametrize("kv,q", [("bf16", "bf16"), ("e4m3", "bf16"), ("f32", "f32")])
+def test_a_window_past_every_context(kv, q, cuda_device):
+    """The largest window hides nothing, whatever the prefix: its arithmetic does not wrap."""
+    b = Batch(cuda_device, [1, 300, 1, 70], [900, 1300, 64, 70], 8, 2, 64, 16, kv, q, window=2**31 - 1,
+              prefix=[1000, 1300, 0, 33], slopes=True, seed=7)
+    b.run(decode=False)
+    b.check()
+
+
 def test_capped_fp32_keeps_fp32(cuda_device):
     """The cap in fp32 rows: within 1e-5 of the fp64 result in the 2-norm."""
     b = Batch(cuda_device, [1] * 5, [40, 128, 300, 64, 511], 4, 2, 64, 16, "f32", "f32", cap=50.0, slopes=True, seed=1)
