@@ -212,7 +212,9 @@ size_t pa_decode_workspace_size(const pa_cache_desc* desc, int32_t num_seqs);
  *   out         device, [num_seqs][num_q_heads][head_dim], q_dtype
  *   workspace   device, >= pa_decode_workspace_size bytes, 256-byte aligned,
  *               zero-filled once before its first use; every call leaves it
- *               ready for the next (also when replayed from a CUDA graph).
+ *               ready for the next (also when replayed from a CUDA graph) of
+ *               the same desc and num_seqs, which its layout follows: zero it
+ *               again for others.
  *               Its first 4 bytes are an error word the kernels set (never
  *               clear): 1 = a bounded internal wait timed out, 2 = a block
  *               table entry outside [0, num_blocks) (read as block 0),
@@ -376,9 +378,12 @@ typedef struct {
 } pa_score_mod;
 
 /* Scratch bytes pa_decode_biased (num_tokens = num_seqs) and
- * pa_decode_chunked_prefill_biased need.  With num_tokens > num_seqs that
- * includes room for the partial results of chunks whose keys are split over
- * several SMs (39 MB at head_dim 128 on a B200, half of it at 64). */
+ * pa_decode_chunked_prefill_biased need: for fp32 queries the 256-byte header,
+ * else that and the decode's partial results, and with num_tokens > num_seqs
+ * room for those of chunks whose keys are split over several SMs (39 MB at
+ * head_dim 128 on a B200, half of it at 64).  A workspace that is large enough
+ * for each of them serves biased calls of any descs and sizes one after
+ * another; the other calls (pa_decode and its kind) take one of their own. */
 size_t pa_biased_workspace_size(const pa_cache_desc* desc, int32_t num_seqs, int32_t num_tokens);
 
 /* pa_decode_biased: pa_decode under `mod`: sequence s's query row sits at

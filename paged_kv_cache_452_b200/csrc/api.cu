@@ -393,39 +393,52 @@ int check_mod(const pa_score_mod* m, float scale, const pa_cache_desc* d, int32_
   return PA_OK;
 }
 
-// The tensor-core paths' workspace: the decode's, and for a step of more rows
-// than sequences (some of them chunks) the cut units' from *parts_at on.
-size_t biased_workspace(const pa_cache_desc* d, int32_t num_seqs, int32_t num_tokens, int sms, size_t* parts_at) {
-  const int cut = cut_group(d->num_q_heads / d->num_kv_heads, 8);
-  size_t n = decode_tc_workspace_bytes(num_seqs, d->num_q_heads / cut, cut, d->head_dim, sms);
-  if (parts_at) *parts_at = 0;
+// The tensor-core paths' workspace.  What is zero between calls (the header
+// and both kernels' counters) lies in front, at places that follow from the
+// SMs alone, so that calls of any sizes can share one workspace; behind it
+// the decode's partials and, for a step of more rows than sequences (some of
+// them chunks), those of cut units: (reference, sum) and O rows.
+struct BiasedWs {
+  size_t cnt, part_cnt, ml, o, part_ml, part_o, bytes;
+  int part_slots;
+};
+
+BiasedWs biased_workspace(const pa_cache_desc* d, int32_t num_seqs, int32_t num_tokens, int sms) {
+  const size_t P = (size_t)decode_tc_workers(sms), cut = (size_t)cut_group(d->num_q_heads / d->num_kv_heads, 8);
+  const size_t slots = (size_t)kPartSlots * sms, dim = (size_t)d->head_dim;
+  size_t off = 256;  // header
+  auto take = [&](size_t n) {
+    const size_t at = off;
+    off += (n + 255) / 256 * 256;
+    return at;
+  };
+  BiasedWs w = {};
+  w.cnt = take(P * 4);
+  w.part_cnt = take(slots * 8 * 4);
+  w.ml = take(P * cut * 2 * 4);
+  w.o = take(P * cut * dim * 4);
   if (num_tokens > num_seqs) {
-    n = (n + 255) / 256 * 256;
-    if (parts_at) *parts_at = n;
-    size_t ml_at, o_at;
-    n += chunk_biased_scratch(d->head_dim, sms, &ml_at, &o_at);
+    w.part_slots = (int)slots;
+    w.part_ml = take(slots * 256 * 2 * 4);
+    w.part_o = take(slots * 256 * dim * 4);
   }
-  return n;
+  w.bytes = off;
+  return w;
 }
 
 bool biased_tc(const pa_cache_desc* d) { return d->q_dtype == kBF16 && d->kv_dtype != kF32; }
 
 // Single-token rows of a biased step on the tensor-core decode (qsl null:
-// every row).
+// every row), on all SMs but the `beside` that chunk CTAs launched before it hold.
 int run_decode_biased(const pa_cache_desc* d, const pa_score_mod* mod, const void* q, const void* k_cache,
                       const void* v_cache, const int32_t* block_tables, int32_t max_blocks, const int32_t* seq_lens,
-                      const int32_t* qsl, int32_t num_seqs, int32_t num_rows, float scale, void* out, void* workspace,
-                      size_t workspace_bytes, cudaStream_t stream, const char* who) {
-  int sms = 0;
-  int rc = num_sms(&sms);
-  if (rc) return rc;
+                      const int32_t* qsl, int32_t num_seqs, int32_t num_rows, float scale, int beside, void* out,
+                      void* workspace, const BiasedWs& w, int sms, cudaStream_t stream, const char* who) {
+  int rc;
   const int group = d->num_q_heads / d->num_kv_heads, cut = cut_group(group, 8);
   const int heads = d->num_q_heads / cut;
   if ((int64_t)num_seqs * max_blocks * heads >= (int64_t)INT32_MAX)
     return fail(PA_ERR_UNSUPPORTED, "%s: num_seqs * max_blocks_per_seq * heads reaches 2^31", who);
-  WsCarve c = carve(workspace, num_seqs, heads, cut, d->head_dim, sms);
-  if (workspace_bytes < c.bytes)
-    return fail(PA_ERR_INVALID_ARG, "%s: workspace %zu < %zu bytes", who, workspace_bytes, c.bytes);
   CUtensorMap tm_k, tm_v;
   if ((rc = make_kv_map(&tm_k, k_cache, d->kv_dtype, d))) return rc;
   if (d->kv_dtype == kBF16) {
@@ -455,32 +468,40 @@ int run_decode_biased(const pa_cache_desc* d, const pa_score_mod* mod, const voi
   p.v_head = fp8 ? d->v_head_scales : nullptr;
   p.mod = kernel_mod(mod, scale, k_scale);
   p.mod.sub = group / cut;
-  p.ws = c.ws;
-  cudaError_t e = launch_decode_biased(p, tm_k, tm_v, d->kv_dtype, d->head_dim, d->block_size, sms, stream);
+  p.beside_chunks = beside > 0;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.ws.err = reinterpret_cast<int32_t*>(ws);
+  p.ws.cnt = reinterpret_cast<unsigned int*>(ws + w.cnt);
+  p.ws.ml = reinterpret_cast<float*>(ws + w.ml);
+  p.ws.o = reinterpret_cast<float*>(ws + w.o);
+  cudaError_t e = launch_decode_biased(p, tm_k, tm_v, d->kv_dtype, d->head_dim, d->block_size, sms - beside, stream);
   if (e == cudaErrorNotSupported) return fail(PA_ERR_UNSUPPORTED, "%s: too many sequences for one launch", who);
   return cuda_status(e, who);
 }
 
 // Chunk rows (more than one per sequence) of a biased step on tcgen05.
-int run_prefill_biased(const pa_cache_desc* d, const pa_score_mod* mod, const void* q, const void* k_cache,
-                       const void* v_cache, const int32_t* block_tables, int32_t max_blocks, const int32_t* qsl,
-                       const int32_t* seq_lens, int32_t num_seqs, int32_t num_tokens, float scale, bool after_decode,
-                       void* out, void* workspace, size_t parts_at, cudaStream_t stream, const char* who) {
-  int sms = 0;
-  int rc = num_sms(&sms);
-  if (rc) return rc;
+struct Chunks {
+  PrefillParams p;
+  CUtensorMap tm_k, tm_v, tm_q;
+};
+
+int make_chunks(const pa_cache_desc* d, const pa_score_mod* mod, const void* q, const void* k_cache,
+                const void* v_cache, const int32_t* block_tables, int32_t max_blocks, const int32_t* qsl,
+                const int32_t* seq_lens, int32_t num_seqs, int32_t num_tokens, float scale, bool decodes,
+                void* out, void* workspace, const BiasedWs& w, Chunks* c) {
+  int rc;
   const int group = d->num_q_heads / d->num_kv_heads, cut = cut_group(group, 128);
   const bool fp8 = d->kv_dtype == kFP8;
   const float k_scale = fp8 && !d->k_head_scales ? d->k_scale : 1.f;
-  CUtensorMap tm_k, tm_v, tm_q;
-  if ((rc = encode_q_map(&tm_q, q, num_tokens, d, cut))) return rc;
+  if ((rc = encode_q_map(&c->tm_q, q, num_tokens, d, cut))) return rc;
   if (fp8) {
-    tm_k = tm_v = tm_q;  // e4m3 blocks come by bulk copies
+    c->tm_k = c->tm_v = c->tm_q;  // e4m3 blocks come by bulk copies
   } else {
-    if ((rc = make_kv_map(&tm_k, k_cache, d->kv_dtype, d))) return rc;
-    if ((rc = make_kv_map(&tm_v, v_cache, d->kv_dtype, d))) return rc;
+    if ((rc = make_kv_map(&c->tm_k, k_cache, d->kv_dtype, d))) return rc;
+    if ((rc = make_kv_map(&c->tm_v, v_cache, d->kv_dtype, d))) return rc;
   }
-  PrefillParams p = {};
+  PrefillParams& p = c->p;
+  p = {};
   p.k_raw = static_cast<const uint8_t*>(k_cache);
   p.v_raw = static_cast<const uint8_t*>(v_cache);
   p.k_head = fp8 ? d->k_head_scales : nullptr;
@@ -504,20 +525,38 @@ int run_prefill_biased(const pa_cache_desc* d, const pa_score_mod* mod, const vo
   p.err = static_cast<int32_t*>(workspace);
   p.unit_ctr = static_cast<int32_t*>(workspace) + 2;
   p.unit_exit = static_cast<int32_t*>(workspace) + 3;
-  p.after_decode = after_decode;
-  if (parts_at) {  // the workspace has room for cut units
-    size_t ml_at = 0, o_at = 0;
-    chunk_biased_scratch(d->head_dim, sms, &ml_at, &o_at);
-    uint8_t* at = static_cast<uint8_t*>(workspace) + parts_at;
-    p.part_slots = kPartSlots * sms;
-    p.part_cnt = reinterpret_cast<unsigned int*>(at);
-    p.part_ml = reinterpret_cast<float*>(at + ml_at);
-    p.part_o = reinterpret_cast<float*>(at + o_at);
+  p.after_decode = decodes;
+  p.singles = !decodes;
+  if (w.part_slots > 0) {  // the workspace has room for cut units
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.part_slots = w.part_slots;
+    p.part_cnt = reinterpret_cast<unsigned int*>(ws + w.part_cnt);
+    p.part_ml = reinterpret_cast<float*>(ws + w.part_ml);
+    p.part_o = reinterpret_cast<float*>(ws + w.part_o);
   }
-  cudaError_t e = launch_chunk_biased(p, tm_k, tm_v, tm_q, d->kv_dtype, d->head_dim, d->block_size, num_tokens, sms,
-                                      stream);
+  return PA_OK;
+}
+
+int launch_chunks(const pa_cache_desc* d, const Chunks& c, int num_tokens, int sms, int ahead, bool front,
+                  cudaStream_t stream, const char* who) {
+  cudaError_t e = launch_chunk_biased(c.p, c.tm_k, c.tm_v, c.tm_q, d->kv_dtype, d->head_dim, d->block_size, num_tokens,
+                                      sms, ahead, front, stream);
   if (e == cudaErrorNotSupported) return fail(PA_ERR_UNSUPPORTED, "%s: too many sequences for one launch", who);
   return cuda_status(e, who);
+}
+
+// CTAs of the chunk kernel (an SM each) that a mixed step launches before its
+// decode rows, to run beside them: the decode kernel streams a bf16 pool at the
+// full rate from some 90 of 148 SMs on, and the chunks' products use the others
+// meanwhile.  248 decode rows of up to 4096 keys with 8, 4 or 1 chunks of 512
+// rows, capped: 419, 361, 324 us without, 357, 298, 292 with 3/8 of the SMs,
+// 341, 304, 303 with 7/16 (blocks of 32, 8 chunks: 437, 411, 445).  The decode
+// of an e4m3 pool is bound by its instructions and gains from every SM (one
+// chunk: 255 without, 284 with 3/8): none there.
+int chunks_ahead(const pa_cache_desc* d, int num_seqs, int num_tokens, int sms) {
+  if (d->kv_dtype != kBF16) return 0;
+  const bool many = d->block_size == 16 && (int64_t)num_tokens >= 12LL * num_seqs;  // rows per sequence
+  return many ? sms * 7 / 16 : sms * 3 / 8;
 }
 
 int run_biased_simt(const pa_cache_desc* d, const pa_score_mod* mod, const void* q, const void* k_cache,
@@ -976,7 +1015,7 @@ size_t pa_biased_workspace_size(const pa_cache_desc* d, int32_t num_seqs, int32_
   if (!biased_tc(d)) return 256;
   int sms = 0;
   if (num_sms(&sms)) return 0;
-  return biased_workspace(d, num_seqs, num_tokens, sms, nullptr);
+  return biased_workspace(d, num_seqs, num_tokens, sms).bytes;
 }
 
 int pa_decode_biased(const pa_cache_desc* d, const pa_score_mod* mod, const void* q, const void* k_cache,
@@ -990,9 +1029,15 @@ int pa_decode_biased(const pa_cache_desc* d, const pa_score_mod* mod, const void
   if (rc) return rc;
   if ((rc = check_mod(mod, scale, d, max_blocks_per_seq, who)) || num_seqs == 0) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (biased_tc(d))
+  if (biased_tc(d)) {
+    int sms = 0;
+    if ((rc = num_sms(&sms))) return rc;
+    const BiasedWs w = biased_workspace(d, num_seqs, num_seqs, sms);
+    if (workspace_bytes < w.bytes)
+      return fail(PA_ERR_INVALID_ARG, "%s: workspace %zu < %zu bytes", who, workspace_bytes, w.bytes);
     return run_decode_biased(d, mod, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, nullptr, num_seqs,
-                             num_seqs, scale, out, workspace, workspace_bytes, st, who);
+                             num_seqs, scale, 0, out, workspace, w, sms, st, who);
+  }
   if (workspace_bytes < 256) return fail(PA_ERR_INVALID_ARG, "%s: workspace < 256 bytes", who);
   return run_biased_simt(d, mod, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, nullptr, num_seqs,
                          num_seqs, true, false, scale, out, workspace, st, who);
@@ -1026,17 +1071,25 @@ int pa_decode_chunked_prefill_biased(const pa_cache_desc* d, const pa_score_mod*
   }
   int sms = 0;
   if ((rc = num_sms(&sms))) return rc;
-  size_t parts_at = 0;
-  const size_t need = biased_workspace(d, num_seqs, num_tokens, sms, &parts_at);
-  if (workspace_bytes < need)
-    return fail(PA_ERR_INVALID_ARG, "%s: workspace %zu < %zu bytes", who, workspace_bytes, need);
-  if (decodes) {
-    rc = run_decode_biased(d, mod, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, query_start_loc,
-                           num_seqs, num_tokens, scale, out, workspace, workspace_bytes, st, who);
-    if (rc || max_q_len == 1) return rc;
-  }
-  return run_prefill_biased(d, mod, q, k_cache, v_cache, block_tables, max_blocks_per_seq, query_start_loc, seq_lens,
-                            num_seqs, num_tokens, scale, decodes, out, workspace, parts_at, st, who);
+  const BiasedWs w = biased_workspace(d, num_seqs, num_tokens, sms);
+  if (workspace_bytes < w.bytes)
+    return fail(PA_ERR_INVALID_ARG, "%s: workspace %zu < %zu bytes", who, workspace_bytes, w.bytes);
+  auto decode = [&](int beside) {
+    return run_decode_biased(d, mod, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, query_start_loc,
+                             num_seqs, num_tokens, scale, beside, out, workspace, w, sms, st, who);
+  };
+  if (max_q_len == 1) return decode(0);
+  Chunks c;
+  if ((rc = make_chunks(d, mod, q, k_cache, v_cache, block_tables, max_blocks_per_seq, query_start_loc, seq_lens,
+                        num_seqs, num_tokens, scale, decodes, out, workspace, w, &c)))
+    return rc;
+  const int ahead = decodes ? chunks_ahead(d, num_seqs, num_tokens, sms) : 0;
+  if (ahead > 0 && (rc = launch_chunks(d, c, num_tokens, sms, ahead, true, st, who))) return rc;
+  if (decodes) rc = decode(ahead);
+  if (!rc) rc = launch_chunks(d, c, num_tokens, sms, ahead, false, st, who);
+  // a step that got no further leaves the unit counters to the next one
+  if (rc && ahead > 0) cudaMemsetAsync(c.p.unit_ctr, 0, 8, st);
+  return rc;
 }
 
 }  // extern "C"

@@ -47,6 +47,10 @@
 // 640-row chunks over up to 2048 cached keys, 32 heads, distance bias: 161 us,
 // 724 TFLOP/s; two 1024-row chunks over 4096 to 8192 keys in e4m3, cap: 343 us,
 // 765 TFLOP/s.
+// A mixed step over a bf16 pool launches this kernel twice around its decode
+// kernel, which is bound by HBM: some CTAs before it, which run beside it on
+// SMs of their own, and CTAs behind it that take SMs as its CTAs leave.  All
+// claim units of one queue.
 // Every wait is bounded (2 s, then the error word); TMEM is freed on every path.
 #include <cuda_runtime.h>
 
@@ -209,7 +213,7 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
   // ---- unit blocks of each group of sequences, exclusive prefix --------------
   auto blocks_of = [&](int s) {
     const int q = s < S ? p.rows.qsl[s + 1] - p.rows.qsl[s] : 0;
-    return q > p.after_decode ? (q + QB2 - 1) / QB2 : 0;  // (single rows are the decode kernel's, if it ran)
+    return q > 1 || (q == 1 && p.singles) ? (q + QB2 - 1) / QB2 : 0;
   };
   const int groups = (S + kGroup - 1) / kGroup;
   // The chunks by falling context where there are few (long units first leave
@@ -329,10 +333,10 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
   const int whole = gsum[groups] * hkv;
   const int parts = whole > 0 ? max(1, min(kMaxParts, p.part_slots / whole)) : 1;
   const int nunits = whole * parts;
-  auto finish_queue = [&]() {  // the last CTA puts the claim counter back to zero
+  auto finish_queue = [&]() {  // the step's last CTA puts the claim counter back to zero
     if (tid == 0) {
       __threadfence();
-      if (atomicAdd(p.unit_exit, 1) == (int)gridDim.x - 1) {
+      if (atomicAdd(p.unit_exit, 1) == p.exits - 1) {
         atomicExch(p.unit_ctr, 0);
         atomicExch(p.unit_exit, 0);
       }
@@ -1258,7 +1262,7 @@ cudaError_t launch_kv(const PrefillParams& p, const CUtensorMap& tm_k, const CUt
 
 cudaError_t launch_chunk_biased(const PrefillParams& p_in, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                 const CUtensorMap& tm_q, int kv, int head_dim, int block_size, int num_tokens,
-                                int num_sms, cudaStream_t stream) {
+                                int num_sms, int ahead, bool front, cudaStream_t stream) {
   PrefillParams p = p_in;
   if (p.group < 1 || p.group > kRows || p.rows.num_seqs > kGroup * kMaxGroups) return cudaErrorNotSupported;
   for (int i = 0; i < 5; ++i) p.mod.poly[i] = kTanh[i] * p.mod.cap_out;
@@ -1268,19 +1272,12 @@ cudaError_t launch_chunk_biased(const PrefillParams& p_in, const CUtensorMap& tm
   if (bound >= INT32_MAX) return cudaErrorNotSupported;
   // units are cut into at most kMaxParts parts each
   const int64_t most = p.part_slots > 0 ? bound * kMaxParts : bound;
-  const int grid = (int)(most < num_sms ? most : num_sms);
+  const int rest = (int)(most < num_sms ? most : num_sms), first = (int)(most < ahead ? most : ahead);
+  const int grid = front ? first : rest;
+  p.exits = first + rest;
+  if (front) p.after_decode = 0;
   return kv == kBF16 ? launch_kv<kBF16>(p, tm_k, tm_v, tm_q, head_dim, block_size, grid, stream)
                      : launch_kv<kFP8>(p, tm_k, tm_v, tm_q, head_dim, block_size, grid, stream);
-}
-
-// Scratch of the cut units: arrival counters, (reference, sum) and O rows of
-// up to 2 slots per SM (a slot: one part of one unit, 256 rows; with 4 the 256
-// units of two long chunks were halved too, and took 415 us instead of 344).
-size_t chunk_biased_scratch(int head_dim, int num_sms, size_t* ml_at, size_t* o_at) {
-  const size_t slots = kPartSlots * (size_t)num_sms;
-  *ml_at = slots * 8 * 4;
-  *o_at = *ml_at + slots * 256 * 8;
-  return *o_at + slots * 256 * (size_t)head_dim * 4;
 }
 
 }  // namespace pa

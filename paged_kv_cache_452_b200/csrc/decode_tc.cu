@@ -338,7 +338,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<KV>())
   const int wk = blockIdx.x * kWarps + warp;
   // a decode row with an empty context attends nothing: zero output (the
   // biased form waits first: the kernel before this one may write the same rows)
-  if constexpr (MOD) dev::grid_dep_wait();
+  // Beside chunks this grid is launched by theirs, whose CTAs have waited for
+  // the kernel before them by then; one warp waits for that grid, last of all.
+  const bool waits = !MOD || !p.beside_chunks;
+  if (MOD && waits) dev::grid_dep_wait();
   for (int s = blockIdx.x; s < S; s += gridDim.x) {
     const int qlen = p.rows.qsl ? p.rows.qsl[s + 1] - p.rows.qsl[s] : 1;
     if (qlen == 1 && prefix[s + 1] == prefix[s]) {
@@ -352,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<KV>())
     // no tiles: leave once the step's cache write is complete, so that a
     // kernel launched behind this one (the step's prompt rows) can rely on
     // every CTA of this grid having waited for it
-    dev::grid_dep_wait();
+    if (waits || wk == 0) dev::grid_dep_wait();
     return;  // no CTA-wide synchronisation follows
   }
 
@@ -450,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<KV>())
     }
   };
   int issued = 0;
-  dev::grid_dep_wait();  // the pool rows this step wrote are visible from here on
+  if (waits) dev::grid_dep_wait();  // the pool rows this step wrote are visible from here on
   // only now may a dependent launch start (it relies on this wait, above)
   dev::grid_dep_launch();
   // Fault injection for tests (the workspace's second word, zero in normal
@@ -815,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<KV>())
         }
       }
       __syncwarp();
-      if (lane == 0 && !inject) count_in_release(p.ws.cnt + (int64_t)s * hkv + h);
+      if (lane == 0 && !inject) count_in_release(p.ws.cnt + (MOD ? cta_of(a, T, W) : (int64_t)s * hkv + h));
     } else {
       // the sequence's first piece: this warp finishes the (sequence, kv
       // head).  If the context was cut by the end of this warp's range, the
@@ -857,7 +860,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<KV>())
         M0 = n0;
         M1 = n1;
       };
-      unsigned int* cnt = p.ws.cnt + (int64_t)s * hkv + h;
+      // (the biased form counts by the merging warp, which has one cut context
+      // at most: its workspace then lies the same way for every batch)
+      unsigned int* cnt = p.ws.cnt + (MOD ? wk : (int64_t)s * hkv + h);
       bool ready = true;
       if (pe != b) {
         const int cf = wk, cl = cta_of(b - 1, T, W);
@@ -918,6 +923,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<KV>())
     // drain: let this warp's copies still in flight land before exiting
     for (int k = done; k < issued; ++k) dev::mbar_wait(&full[k % NSW], (uint32_t)((k / NSW) & 1), nullptr, 100000000ull);
   }
+  if (MOD && !waits && wk == 0) dev::grid_dep_wait();
 }
 
 // Forward progress: a merging warp waits for pieces held by later CTAs, so

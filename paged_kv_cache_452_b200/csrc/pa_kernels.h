@@ -160,6 +160,7 @@ struct DecodeParams {
   int32_t pfx_members;
   int32_t pfx_chunk_blocks;  // blocks per prefix chunk (prefix_chunk_keys / block_size)
   ScoreMod mod;              // the biased kernel's
+  int32_t beside_chunks;     // the biased kernel's: launched behind chunk CTAs that run beside it
   DecodeWorkspace ws;
 };
 
@@ -203,6 +204,8 @@ struct PrefillParams {
   float* pfx_ml;               // [chunks][M][Hq][2] (max reference, sum), log2 domain
   float* pfx_o;                // [chunks][M][Hq][D]
   ScoreMod mod;                // the biased kernel's
+  int32_t singles;             // the biased kernel's: 1: single rows are units too (no decode kernel has them)
+  int32_t exits;               // the biased kernel's: CTAs of this step that unit_exit counts
   // the biased kernel's cut units (part_slots 0: none are cut): counters, zero
   // between calls, [slots][8]; (reference, sum) [slots][256][2]; O [slots][256][D]
   int32_t part_slots;
@@ -250,11 +253,14 @@ cudaError_t launch_prefill_umma(const PrefillParams& p, const CUtensorMap& tm_k,
                                 cudaStream_t stream);
 // Rows of more than one per sequence with p.mod applied, any group up to 128;
 // an e4m3 pool comes through k_raw and v_raw, a bf16 one through the maps.
+// ahead > 0: the step launches its chunks twice, `ahead` CTAs (front) before
+// its decode kernel and the rest behind it.
 cudaError_t launch_chunk_biased(const PrefillParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                 const CUtensorMap& tm_q, int kv, int head_dim, int block_size, int num_tokens,
-                                int num_sms, cudaStream_t stream);
-constexpr int kPartSlots = 2;  // slots per SM
-size_t chunk_biased_scratch(int head_dim, int num_sms, size_t* ml_at, size_t* o_at);
+                                int num_sms, int ahead, bool front, cudaStream_t stream);
+// Slots per SM for cut units (a slot: one part of one unit, 256 rows; with 4
+// the 256 units of two long chunks were halved too, and took 415 us, not 344).
+constexpr int kPartSlots = 2;
 cudaError_t launch_prefill_tc(const PrefillParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                               int head_dim, int block_size, int num_tokens, cudaStream_t stream);
 

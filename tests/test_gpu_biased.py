@@ -319,6 +319,35 @@ def test_decode_behind_a_chunk_on_the_same_output(cuda_device):
         assert bool((small.out[[0, 2, 4]] == 0).all())
 
 
+@pytest.mark.parametrize("bs", [16, 32])
+def test_mixed_steps_back_to_back(bs, cuda_device):
+    """Mixed steps of different sizes over one workspace, without a gap: each one's chunks run beside its single rows
+    and partly behind them, and its results stay the same bits."""
+    big = Batch(cuda_device, [300, 1, 1, 200, 1, 1, 1, 450], [900, 3000, 40, 1500, 2, 700, 5, 450], 16, 4, 128, bs, "bf16",
+                "bf16", cap=40.0, window=800, prefix=[16] * 8, seed=1)
+    many = Batch(cuda_device, [1] * 90 + [70] + [1] * 60, list(range(7, 157 * 9, 9))[:151], 8, 2, 64, bs, "bf16", "bf16",
+                 slopes=True, seed=2)
+    none = Batch(cuda_device, [3, 5, 0, 4], [60, 5, 9, 400], 8, 2, 128, bs, "bf16", "bf16", cap=9.0, seed=3)
+    rows = Batch(cuda_device, [1] * 7, [5000, 1, 0, 4000, 300, 9000, 17], 32, 2, 64, bs, "bf16", "bf16", cap=9.0, seed=4)
+    codes = Batch(cuda_device, [1, 1, 90], [6000, 2500, 90], 8, 1, 128, bs, "e4m3", "bf16", slopes=True, seed=5)
+    batches = (big, many, none, rows, codes)
+    ws = max((b.ws for b in batches), key=lambda t: t.numel())
+    first = []
+    for b in batches:
+        b.ws = ws
+        b.run(decode=False)
+        b.check()
+        first.append(b.out.clone())
+        b.out.zero_()
+    for _ in range(20):
+        for b in batches:
+            b.run(decode=False)
+    torch.cuda.synchronize()
+    for b, was in zip(batches, first):
+        assert torch.equal(b.out, was)
+        b.check()
+
+
 def test_a_group_of_more_than_128(cuda_device):
     b = Batch(cuda_device, [3, 1], [40, 90], 130, 1, 64, 16, "bf16", "bf16", cap=10.0, seed=3)
     b.run(decode=False)
