@@ -549,15 +549,12 @@ int launch_chunks(const pa_cache_desc* d, const Chunks& c, int num_tokens, int s
 // decode rows, to run beside them: the decode kernel streams a bf16 pool at the
 // full rate from some 90 of 148 SMs on, and the chunks' products use the others
 // meanwhile.  248 decode rows of up to 4096 keys with 8, 4 or 1 chunks of 512
-// rows, capped: 419, 361, 324 us without, 357, 298, 292 with 3/8 of the SMs,
-// 341, 304, 303 with 7/16 (blocks of 32, 8 chunks: 437, 411, 445).  The decode
-// of an e4m3 pool is bound by its instructions and gains from every SM (one
-// chunk: 255 without, 284 with 3/8): none there.
-int chunks_ahead(const pa_cache_desc* d, int num_seqs, int num_tokens, int sms) {
-  if (d->kv_dtype != kBF16) return 0;
-  const bool many = d->block_size == 16 && (int64_t)num_tokens >= 12LL * num_seqs;  // rows per sequence
-  return many ? sms * 7 / 16 : sms * 3 / 8;
-}
+// rows, capped, us: 419, 361, 324 without, 374, 296, 290 with a third of the
+// SMs, 357, 298, 292 with 3/8, 341, 304, 303 with 7/16; called back to back,
+// under the power cap, 426, 351, 318; 395, 331, 294; 392, 327, 303; 408, 341,
+// 314.  The decode of an e4m3 pool is bound by its instructions and gains from
+// every SM (one chunk: 255 without, 284 with 3/8): none there.
+int chunks_ahead(const pa_cache_desc* d, int sms) { return d->kv_dtype == kBF16 ? sms * 3 / 8 : 0; }
 
 int run_biased_simt(const pa_cache_desc* d, const pa_score_mod* mod, const void* q, const void* k_cache,
                     const void* v_cache, const int32_t* block_tables, int32_t max_blocks, const int32_t* seq_lens,
@@ -1083,7 +1080,7 @@ int pa_decode_chunked_prefill_biased(const pa_cache_desc* d, const pa_score_mod*
   if ((rc = make_chunks(d, mod, q, k_cache, v_cache, block_tables, max_blocks_per_seq, query_start_loc, seq_lens,
                         num_seqs, num_tokens, scale, decodes, out, workspace, w, &c)))
     return rc;
-  const int ahead = decodes ? chunks_ahead(d, num_seqs, num_tokens, sms) : 0;
+  const int ahead = decodes ? chunks_ahead(d, sms) : 0;
   if (ahead > 0 && (rc = launch_chunks(d, c, num_tokens, sms, ahead, true, st, who))) return rc;
   if (decodes) rc = decode(ahead);
   if (!rc) rc = launch_chunks(d, c, num_tokens, sms, ahead, false, st, who);
