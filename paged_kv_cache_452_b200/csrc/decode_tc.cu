@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<KV>())
   const int pool_heads = MOD ? hkv / p.mod.sub : hkv;  // kv heads of the pool
   const SmemLayout L = smem_layout(STAGE, NSW, S);
   int32_t* prefix = reinterpret_cast<int32_t*>(smem + L.prefix);
-  __shared__ int32_t warp_tot[kWarps];
+  __shared__ int32_t warp_tot[kWarps], warp_most[kWarps];
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5, lane = tid & 31;
@@ -307,8 +307,15 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<KV>())
   {
     const int ipt = (S + kThreads - 1) / kThreads;
     const int lo = min(S, tid * ipt), hi = min(S, lo + ipt);
-    int sum = 0;
-    for (int i = lo; i < hi; ++i) sum += prefix[i];
+    int sum = 0, most = 0;
+    for (int i = lo; i < hi; ++i) {
+      sum += prefix[i];
+      if (MOD) most = max(most, prefix[i]);
+    }
+    if constexpr (MOD) {
+      most = __reduce_max_sync(0xffffffffu, most);
+      if (lane == 0) warp_most[warp] = most;
+    }
     int x = sum;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -334,8 +341,20 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<KV>())
   __syncthreads();
 
   const int T = hkv * prefix[S];
-  const int W = gridDim.x * kWarps;  // warps of the grid: the workers
-  const int wk = blockIdx.x * kWarps + warp;
+  int W = gridDim.x * kWarps;  // warps of the grid: the workers
+  int wk = blockIdx.x * kWarps + warp;
+  if constexpr (MOD) {
+    // A context of n tiles takes its worker n / pieces steps and as many folds
+    // as it has pieces, one after another: of few tiles, ranges are at least
+    // sqrt(n) of the longest context.  (1 sequence, 1 kv head, 13 273 keys: 360
+    // us in single tiles, 37 us.)  Warps of the same CTA are far apart, so that
+    // few workers still spread over the SMs.
+    int longest = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) longest = max(longest, warp_most[w]);
+    W = max(1, min(W, T / max(1, (int)sqrtf((float)longest))));
+    wk = warp * gridDim.x + blockIdx.x;
+  }
   // a decode row with an empty context attends nothing: zero output (the
   // biased form waits first: the kernel before this one may write the same rows)
   // Beside chunks this grid is launched by theirs, whose CTAs have waited for
@@ -350,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<KV>())
         reinterpret_cast<__nv_bfloat16*>(p.out)[(int64_t)row * hq * D + i] = __float2bfloat16_rn(0.f);
     }
   }
-  const int wbeg = range_start(wk, T, W), wend = range_start(wk + 1, T, W);
+  const int wbeg = MOD && wk >= W ? T : range_start(wk, T, W), wend = MOD && wk >= W ? T : range_start(wk + 1, T, W);
   if (wbeg >= wend) {
     // no tiles: leave once the step's cache write is complete, so that a
     // kernel launched behind this one (the step's prompt rows) can rely on
@@ -867,7 +886,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<KV>())
       if (pe != b) {
         const int cf = wk, cl = cta_of(b - 1, T, W);
         int others = 0;
-        for (int c = cf + 1; c <= cl; ++c) others += range_start(c, T, W) < range_start(c + 1, T, W);
+        if (MOD) others = cl - cf;  // (no range is empty)
+        for (int c = cf + 1; c <= cl && !MOD; ++c) others += range_start(c, T, W) < range_start(c + 1, T, W);
         if (lane == 0) {
           const uint64_t t_start = dev::globaltimer_ns();
           const uint64_t limit = inject ? 1000000ull : 2000000000ull;
@@ -881,9 +901,59 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<KV>())
         }
         ready = __shfl_sync(0xffffffffu, ready, 0);
         __syncwarp();
-        for (int c = cf + 1; c <= cl && ready; ++c) {
-          if (range_start(c, T, W) >= range_start(c + 1, T, W)) continue;
-          fold(p.ws.ml + (int64_t)c * G * 2, p.ws.o + (int64_t)c * G * D);
+        if constexpr (MOD) {
+          // All pieces' references first (a piece per row group of the
+          // fragments), so that their O rows fold without a chain of rescales
+          // and their loads overlap.
+          float n0 = M0, n1 = M1;
+          for (int c = cf + 1 + g; c <= cl && ready; c += 8) {
+            const float* pml = p.ws.ml + (int64_t)c * G * 2;
+            if (c0 < G) n0 = fmaxf(n0, __ldcg(pml + c0 * 2));
+            if (c1 < G) n1 = fmaxf(n1, __ldcg(pml + c1 * 2));
+          }
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) {
+            n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, x));
+            n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, x));
+          }
+          const float a0 = dev::ex2(M0 - n0), a1 = dev::ex2(M1 - n1);
+          L0 *= a0;
+          L1 *= a1;
+#pragma unroll
+          for (int mt = 0; mt < C::DM; ++mt) {
+            o[mt][0] *= a0;
+            o[mt][2] *= a0;
+            o[mt][1] *= a1;
+            o[mt][3] *= a1;
+          }
+#pragma unroll 2
+          for (int c = cf + 1; c <= (ready ? cl : cf); ++c) {
+            const float* pml = p.ws.ml + (int64_t)c * G * 2;
+            const float* po = p.ws.o + (int64_t)c * G * D;
+            const float w0 = c0 < G ? dev::ex2(__ldcg(pml + c0 * 2) - n0) : 0.f;
+            const float w1 = c1 < G ? dev::ex2(__ldcg(pml + c1 * 2) - n1) : 0.f;
+            if (c0 < G) L0 = fmaf(__ldcg(pml + c0 * 2 + 1), w0, L0);
+            if (c1 < G) L1 = fmaf(__ldcg(pml + c1 * 2 + 1), w1, L1);
+#pragma unroll
+            for (int mt = 0; mt < C::DM; ++mt) {
+              const int d0 = 16 * mt + g;
+              if (c0 < G) {
+                o[mt][0] = fmaf(__ldcg(po + c0 * D + d0), w0, o[mt][0]);
+                o[mt][2] = fmaf(__ldcg(po + c0 * D + d0 + 8), w0, o[mt][2]);
+              }
+              if (c1 < G) {
+                o[mt][1] = fmaf(__ldcg(po + c1 * D + d0), w1, o[mt][1]);
+                o[mt][3] = fmaf(__ldcg(po + c1 * D + d0 + 8), w1, o[mt][3]);
+              }
+            }
+          }
+          M0 = n0;
+          M1 = n1;
+        } else {
+          for (int c = cf + 1; c <= cl && ready; ++c) {
+            if (range_start(c, T, W) >= range_start(c + 1, T, W)) continue;
+            fold(p.ws.ml + (int64_t)c * G * 2, p.ws.o + (int64_t)c * G * D);
+          }
         }
       }
       if (skip > 0) {

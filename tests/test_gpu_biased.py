@@ -363,14 +363,18 @@ def test_scores_that_fill_the_cap(cuda_device):
 
 
 def test_without_mod_as_plain_attention(cuda_device):
-    """With nothing set the biased decode's outputs are pa_decode's, to the bit."""
+    """With nothing set the biased decode computes what pa_decode does.  The two cut contexts into different pieces,
+    and a weight is rounded to bf16 relative to its piece's reference, so a weight may differ by two roundings of
+    2^-9 and a result by two of its own: each of the two is within the tolerance of the fp64 result, which counts
+    2^-8 per weight and per result, and so within twice that of the other."""
     b = Batch(cuda_device, [1] * 12, LENS, 8, 2, 128, 16, "bf16", "bf16", seed=4, spoil=False)
     b.run(decode=True)
     out = torch.empty_like(b.out)
     ws = pa.alloc_workspace(pa.pa_decode_workspace_size(b.desc, 12), cuda_device)
     pa.pa_decode(b.desc, b.q, b.k, b.v, b.tables, b.sl, b.scale, out, ws)
-    torch.cuda.synchronize()
-    assert torch.equal(out, b.out)
+    b.check()
+    _, tol = b.expected()
+    assert bool(((out.double() - b.out.double()).abs() <= 2 * tol).all())
 
 
 def test_bad_table_entries_and_long_contexts_are_flagged(cuda_device):
