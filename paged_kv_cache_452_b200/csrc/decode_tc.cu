@@ -344,15 +344,17 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<KV>())
   int W = gridDim.x * kWarps;  // warps of the grid: the workers
   int wk = blockIdx.x * kWarps + warp;
   if constexpr (MOD) {
-    // A context of n tiles takes its worker n / pieces steps and as many folds
-    // as it has pieces, one after another: of few tiles, ranges are at least
-    // sqrt(n) of the longest context.  (1 sequence, 1 kv head, 13 273 keys: 360
-    // us in single tiles, 37 us.)  Warps of the same CTA are far apart, so that
-    // few workers still spread over the SMs.
+    // A piece of m tiles takes its worker m steps, and the warp that joins a
+    // context of n tiles n / m folds, one after another (a fold costs half a
+    // step): ranges are at least sqrt(n / 2) of the longest context.  (1
+    // sequence of 13 273 keys, 1 kv head, blocks of 32: 360 us in single
+    // tiles, 32 with 0.5 sqrt(n), 34 with 0.7, 38 with 1, 60 with 2; 8 of up to
+    // 1000 keys, 8 kv heads: 19, 17, 18, 24.)  Warps of a CTA are far apart, so
+    // that few workers still spread over the SMs.
     int longest = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) longest = max(longest, warp_most[w]);
-    W = max(1, min(W, T / max(1, (int)sqrtf((float)longest))));
+    W = max(1, min(W, T / max(1, (int)sqrtf(0.5f * (float)longest))));
     wk = warp * gridDim.x + blockIdx.x;
   }
   // a decode row with an empty context attends nothing: zero output (the
