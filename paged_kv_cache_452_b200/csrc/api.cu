@@ -554,7 +554,12 @@ int launch_chunks(const pa_cache_desc* d, const Chunks& c, int num_tokens, int s
 // under the power cap, 426, 351, 318; 395, 331, 294; 392, 327, 303; 408, 341,
 // 314.  The decode of an e4m3 pool is bound by its instructions and gains from
 // every SM (one chunk: 255 without, 284 with 3/8): none there.
-int chunks_ahead(const pa_cache_desc* d, int sms) { return d->kv_dtype == kBF16 ? sms * 3 / 8 : 0; }
+// Nor where decode rows are too few to keep HBM busy for long (up to 17 with 2
+// chunks of 710 rows, by 2 kv heads 49 against 60, by 8 79 against 89; 60 of
+// them by 8 kv heads 119 against 103).
+int chunks_ahead(const pa_cache_desc* d, int num_seqs, int sms) {
+  return d->kv_dtype == kBF16 && (int64_t)num_seqs * d->num_kv_heads >= 2LL * sms ? sms * 3 / 8 : 0;
+}
 
 int run_biased_simt(const pa_cache_desc* d, const pa_score_mod* mod, const void* q, const void* k_cache,
                     const void* v_cache, const int32_t* block_tables, int32_t max_blocks, const int32_t* seq_lens,
@@ -1080,7 +1085,7 @@ int pa_decode_chunked_prefill_biased(const pa_cache_desc* d, const pa_score_mod*
   if ((rc = make_chunks(d, mod, q, k_cache, v_cache, block_tables, max_blocks_per_seq, query_start_loc, seq_lens,
                         num_seqs, num_tokens, scale, decodes, out, workspace, w, &c)))
     return rc;
-  const int ahead = decodes ? chunks_ahead(d, sms) : 0;
+  const int ahead = decodes ? chunks_ahead(d, num_seqs, sms) : 0;
   if (ahead > 0 && (rc = launch_chunks(d, c, num_tokens, sms, ahead, true, st, who))) return rc;
   if (decodes) rc = decode(ahead);
   if (!rc) rc = launch_chunks(d, c, num_tokens, sms, ahead, false, st, who);

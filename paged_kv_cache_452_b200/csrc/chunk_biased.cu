@@ -47,8 +47,8 @@
 // 640-row chunks over up to 2048 cached keys, 32 heads, distance bias: 161 us,
 // 724 TFLOP/s; two 1024-row chunks over 4096 to 8192 keys in e4m3, cap: 343 us,
 // 765 TFLOP/s.
-// A mixed step over a bf16 pool launches this kernel twice around its decode
-// kernel, which is bound by HBM: some CTAs before it, which run beside it on
+// A mixed step of many sequences over a bf16 pool launches this kernel twice
+// around its decode kernel, which is bound by HBM: some CTAs before it, which run beside it on
 // SMs of their own, and CTAs behind it that take SMs as its CTAs leave.  All
 // claim units of one queue.
 // Every wait is bounded (2 s, then the error word); TMEM is freed on every path.

@@ -348,6 +348,42 @@ def test_mixed_steps_back_to_back(bs, cuda_device):
         b.check()
 
 
+@pytest.mark.parametrize("bs", [16, 32])
+def test_many_single_rows_beside_chunks(bs, cuda_device):
+    """Enough single rows that chunks start before them: every row is right, and again the same bits when the step is
+    repeated without a gap, captured, and followed by a step without chunks."""
+    rng = np.random.default_rng(bs)
+    qlens = [1] * 70
+    lens = [int(n) for n in rng.integers(1, 900, 70)]
+    for s, n in ((3, 260), (40, 33), (69, 500)):
+        qlens[s], lens[s] = n, n + 77 * s
+    b = Batch(cuda_device, qlens, lens, 16, 8, 128, bs, "bf16", "bf16", cap=30.0, window=700, prefix=[9] * 70, seed=bs)
+    one = Batch(cuda_device, [1] * 70, lens, 16, 8, 128, bs, "bf16", "bf16", cap=30.0, seed=bs + 1)
+    b.run(decode=False)
+    b.check()
+    was = b.out.clone()
+    b.out.zero_()
+    for _ in range(15):
+        b.run(decode=False)
+        one.run(decode=True)
+    torch.cuda.synchronize()
+    assert torch.equal(b.out, was)
+    one.check()
+    b.out.zero_()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            b.run(decode=False)
+            b.run(decode=False)
+        g.replay()
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(b.out, was)
+    b.check()
+
+
 def test_a_group_of_more_than_128(cuda_device):
     b = Batch(cuda_device, [3, 1], [40, 90], 130, 1, 64, 16, "bf16", "bf16", cap=10.0, seed=3)
     b.run(decode=False)
