@@ -33,7 +33,7 @@
 //    each a unit of the queue that leaves (reference, sum, O) per row; for each
 //    warp's rows the part that arrives last joins them in the order of the
 //    parts.  Nobody waits for another, and results do not depend on the order
-//    of arrival.  (One 512-row chunk over 8300 keys: 155 -> 112 us.)
+//    of arrival.  (One 512-row chunk over 8300 keys, 32 heads: 155 -> 90 us.)
 //  * e4m3 pools: blocks land raw (bulk copies), four converter warps write them
 //    as f16 (exact) into the swizzled K and V tiles, V as rows of d with
 //    their keys contiguous (what its d-major blocks give), and the queries are rounded to f16; P is f16.
@@ -66,6 +66,8 @@ constexpr int kHalf = 64;    // keys of a step: half a tile
 constexpr int kTileRow = 128 * 128;  // bytes of a 64-element-wide chunk of a 128-row tile
 constexpr int kUQ = 4;       // unit queue entries
 constexpr int kMaxParts = 8;
+constexpr float kPartCost = 6.f;  // tiles (3 and 10 choose the same almost everywhere)
+static_assert(kMaxParts == 8, "a candidate per lane of eight");
 constexpr int kGroup = 64;   // sequences of a group in the unit search
 constexpr int kMaxGroups = 256;  // groups: 16384 sequences
 constexpr int kMaxOrder = 64;    // up to so many chunks are taken longest context first
@@ -222,6 +224,7 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
   int32_t* obase = reinterpret_cast<int32_t*>(smem + T::ORDER);
   int16_t* oseq = reinterpret_cast<int16_t*>(obase + kMaxOrder + 1);
   int32_t* found = reinterpret_cast<int32_t*>(tmem_slot + 1);
+  int32_t* longest = found + 1;  // context of the first
   if (tid == 0) *found = 0;
   __syncthreads();
   for (int g = warp; g < groups; g += T::THREADS / 32) {
@@ -291,17 +294,18 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
   const bool ordered = chunks <= kMaxOrder;
   {
     // rank by (context, sequence): the same whatever order they were found in
-    int mine = -1, rank = 0, nb = 0;
+    int mine = -1, rank = 0, nb = 0, len = 0;
     if (ordered && tid < chunks) {
       mine = oseq[tid];
       nb = blocks_of(mine);
-      const int len = obase[tid];
+      len = obase[tid];
       for (int j = 0; j < chunks; ++j) rank += obase[j] > len || (obase[j] == len && oseq[j] < mine);
     }
     __syncthreads();
     if (mine >= 0) {
       oseq[rank] = (int16_t)mine;
       obase[rank] = nb;
+      if (rank == 0) *longest = len;
     }
     __syncthreads();
     if (ordered && warp == 1) {
@@ -331,7 +335,30 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
   // and the last ones are short; a unit's parts leave (reference, sum, O) per
   // row, and for each warp's rows the part that arrives last joins them.
   const int whole = gsum[groups] * hkv;
-  const int parts = whole > 0 ? max(1, min(kMaxParts, p.part_slots / whole)) : 1;
+  // A part costs its tiles and about kPartCost more (start, first step, join);
+  // parts are as many as make the rounds over the SMs shortest (as many as
+  // there are slots for: 6 chunks of 27 rows over 3200 keys 45 us, so 30; one of
+  // 512 over 8500, 32 heads, 106 and 90).
+  int parts = 1;
+  if (!ordered && whole > 0) {  // (contexts not at hand: one round)
+    parts = max(1, min(kMaxParts, p.part_slots / (kPartSlots * whole)));
+  } else if (whole > 0 && p.part_slots >= 2 * whole) {
+    int tiles = (min(*longest, p.max_blocks * BS) + kKeys - 1) / kKeys;
+    if (p.mod.window > 0) tiles = min(tiles, (p.mod.window - 1) / kKeys + QB2 / kKeys + 2);
+    const int sms = p.part_slots / kPartSlots;
+    parts = (lane & 7) + 1;  // a candidate per lane, then the best of them
+    float cost = parts * whole > p.part_slots ? 1e30f
+                                              : (float)((whole * parts + sms - 1) / sms) * ((float)tiles / (float)parts + kPartCost);
+#pragma unroll
+    for (int x = 1; x < 8; x <<= 1) {
+      const float c = __shfl_xor_sync(0xffffffffu, cost, x);
+      const int n = __shfl_xor_sync(0xffffffffu, parts, x);
+      if (c < cost || (c == cost && n < parts)) {
+        cost = c;
+        parts = n;
+      }
+    }
+  }
   const int nunits = whole * parts;
   auto finish_queue = [&]() {  // the step's last CTA puts the claim counter back to zero
     if (tid == 0) {

@@ -384,6 +384,19 @@ def test_many_single_rows_beside_chunks(bs, cuda_device):
     b.check()
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_cut_units_of_many_chunks(kv, cuda_device):
+    """More chunks than are taken in order, but few enough units that their keys are cut."""
+    lens = [2 + 11 * s for s in range(70)]
+    b = Batch(cuda_device, [2] * 70, lens, 4, 1, 64, 16, kv, "bf16", cap=20.0, window=400, prefix=[20] * 70, seed=11)
+    b.run(decode=False)
+    b.check()
+    was = b.out.clone()
+    b.run(decode=False)
+    b.check()
+    assert torch.equal(b.out, was)
+
+
 def test_a_group_of_more_than_128(cuda_device):
     b = Batch(cuda_device, [3, 1], [40, 90], 130, 1, 64, 16, "bf16", "bf16", cap=10.0, seed=3)
     b.run(decode=False)
