@@ -392,7 +392,8 @@ size_t pa_biased_workspace_size(const pa_cache_desc* desc, int32_t num_seqs, int
  * Arguments, errors, the workspace (sized by pa_biased_workspace_size) and its
  * error word as for pa_decode; `scale` positive and finite.  bf16 queries over
  * a bf16 or e4m3 pool run on the tensor cores for every group and head_dim,
- * fp32 queries on CUDA cores.  V rows that no query of the sequence sees may
+ * fp32 queries over an fp32 or e4m3 pool on CUDA cores; other pairs are
+ * PA_ERR_UNSUPPORTED (their workspace size is 0).  V rows that no query of the sequence sees may
  * hold anything, NaN included. */
 int pa_decode_biased(const pa_cache_desc* desc, const pa_score_mod* mod, const void* q, const void* k_cache,
                      const void* v_cache, const int32_t* block_tables, int32_t max_blocks_per_seq,

@@ -375,6 +375,15 @@ ScoreMod kernel_mod(const pa_score_mod* m, float scale, float k_scale) {
   return k;
 }
 
+// The pairs the biased kernels are built for: bf16 queries over a bf16 or e4m3
+// pool (tensor cores), fp32 queries over an fp32 or e4m3 pool (CUDA cores).
+// The fp32 kernels take the query type from here: nothing else may pass.
+int check_biased_dtypes(const pa_cache_desc* d, const char* who) {
+  if (d->kv_dtype != kFP8 && d->kv_dtype != d->q_dtype)
+    return fail(PA_ERR_UNSUPPORTED, "%s: q dtype %d with kv dtype %d", who, d->q_dtype, d->kv_dtype);
+  return PA_OK;
+}
+
 int check_mod(const pa_score_mod* m, float scale, const pa_cache_desc* d, int32_t max_blocks, const char* who) {
   if (!m) return fail(PA_ERR_INVALID_ARG, "%s: mod is NULL", who);
   if (!(m->softcap >= 0.f) || !std::isfinite(m->softcap))
@@ -390,7 +399,7 @@ int check_mod(const pa_score_mod* m, float scale, const pa_cache_desc* d, int32_
     return fail(PA_ERR_INVALID_ARG, "%s: misaligned slopes or prefix_lens", who);
   if ((int64_t)max_blocks * d->block_size >= (int64_t)INT32_MAX)
     return fail(PA_ERR_UNSUPPORTED, "%s: table rows of 2^31 tokens", who);
-  return PA_OK;
+  return check_biased_dtypes(d, who);
 }
 
 // The tensor-core paths' workspace.  What is zero between calls (the header
@@ -426,7 +435,7 @@ BiasedWs biased_workspace(const pa_cache_desc* d, int32_t num_seqs, int32_t num_
   return w;
 }
 
-bool biased_tc(const pa_cache_desc* d) { return d->q_dtype == kBF16 && d->kv_dtype != kF32; }
+bool biased_tc(const pa_cache_desc* d) { return d->q_dtype == kBF16; }
 
 // Single-token rows of a biased step on the tensor-core decode (qsl null:
 // every row), on all SMs but the `beside` that chunk CTAs launched before it hold.
@@ -1009,7 +1018,7 @@ int pa_decode_chunked_prefill(const pa_cache_desc* d, const void* q, const void*
 
 size_t pa_biased_workspace_size(const pa_cache_desc* d, int32_t num_seqs, int32_t num_tokens) {
   clear_error();
-  if (check_desc(d, "pa_biased_workspace_size")) return 0;
+  if (check_desc(d, "pa_biased_workspace_size") || check_biased_dtypes(d, "pa_biased_workspace_size")) return 0;
   if (num_seqs < 0 || num_tokens < 0) {
     fail(PA_ERR_INVALID_ARG, "pa_biased_workspace_size: negative size");
     return 0;

@@ -122,6 +122,21 @@ def test_biased_attention_refusals():
     assert pa.pa_biased_workspace_size(f32, 4, 4) == 256
 
 
+@pytest.mark.parametrize("kv,q", [("f32", "bf16"), ("bf16", "f32")])
+def test_biased_attention_refuses_pairs_that_are_not_built(kv, q):
+    """bf16 queries over an fp32 pool, or fp32 queries over a bf16 pool: no kernel reads them, and none is launched."""
+    desc = pa.CacheDesc.make(16, 16, 2, 8, 64, kv, q)
+    L, d, m = pa.lib(), ctypes.byref(desc), ctypes.byref(pa.ScoreMod(30.0, 10, None, None))
+    assert L.pa_decode_biased(d, m, P, P, P, P, 4, P, 2, 0.125, P, P, 1 << 30, None) == 2
+    assert b"kv dtype" in L.pa_last_error()
+    for max_q_len in (1, 4):
+        assert L.pa_decode_chunked_prefill_biased(d, m, P, P, P, P, 4, P, P, 2, 5, max_q_len, 0.125, P, P, 1 << 30,
+                                                  None) == 2
+    assert L.pa_biased_workspace_size(d, 2, 5) == 0
+    with pytest.raises(pa.PaError, match="kv dtype"):
+        pa.pa_biased_workspace_size(desc, 2, 5)
+
+
 def test_biased_bindings_refuse_wrong_tensors():
     bf, i32 = torch.bfloat16, torch.int32
     desc = pa.CacheDesc.make(4, 16, 2, 8, 64, "bf16", "bf16")
