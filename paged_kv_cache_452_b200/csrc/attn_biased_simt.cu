@@ -225,8 +225,9 @@ __global__ void __launch_bounds__(kTileThreads, 2) attn_biased_tile_kernel(const
     if (base(mid) <= (int64_t)blockIdx.x) lo = mid; else hi = mid - 1;
   }
   const int s = lo, first = p.rows.qsl[s], qlen = p.rows.qsl[s + 1] - first;
-  if (qlen <= 1) return;  // single rows are the other kernel's
-  const int64_t pair0 = ((int64_t)blockIdx.x - base(s)) * kR, pairs = (int64_t)qlen * G;
+  if (qlen <= 1 || first < 0) return;  // single rows are the other kernel's
+  // (never past the rows that q and out have, whatever query_start_loc says)
+  const int64_t pair0 = ((int64_t)blockIdx.x - base(s)) * kR, pairs = (int64_t)min(qlen, p.rows.num_rows - first) * G;
   if (pair0 >= pairs) return;
   const int np = (int)min((int64_t)kR, pairs - pair0);
   int len = p.rows.seq_lens[s];

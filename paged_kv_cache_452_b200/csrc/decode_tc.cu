@@ -141,6 +141,12 @@ __device__ __forceinline__ int seq_skip(const DecodeParams& p, bool pfx, int s) 
   return pf >= 0 ? __ldg(p.pfx_blocks + pf) : 0;
 }
 
+// Whether the query row of sequence s is one of the rows that q and out have,
+// whatever query_start_loc says.
+__device__ __forceinline__ bool has_row(const DecodeParams& p, int s) {
+  return !p.rows.qsl || (unsigned)p.rows.qsl[s] < (unsigned)p.rows.num_rows;
+}
+
 // The biased decode's view of sequence s (its query at position len - 1): a
 // row's blocks [0, np) hold visible prefix keys, blocks [np + gap, end) the
 // window's; the gap between them is not read.
@@ -277,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<KV>())
   for (int s = tid; s < S; s += kThreads) {
     const int len = p.rows.seq_lens[s];
     const int qlen = p.rows.qsl ? p.rows.qsl[s + 1] - p.rows.qsl[s] : 1;
-    int nb = (qlen == 1 && len > 0) ? (len + BS - 1) / BS : 0;
+    int nb = (qlen == 1 && len > 0 && (!MOD || has_row(p, s))) ? (len + BS - 1) / BS : 0;
     if (nb > p.max_blocks) {  // context longer than its table row: flag, clamp
       atomicCAS(p.ws.err, 0, 3);
       nb = p.max_blocks;
@@ -365,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<KV>())
   if (MOD && waits) dev::grid_dep_wait();
   for (int s = blockIdx.x; s < S; s += gridDim.x) {
     const int qlen = p.rows.qsl ? p.rows.qsl[s + 1] - p.rows.qsl[s] : 1;
-    if (qlen == 1 && prefix[s + 1] == prefix[s]) {
+    if (qlen == 1 && prefix[s + 1] == prefix[s] && (!MOD || has_row(p, s))) {
       const int row = p.rows.qsl ? p.rows.qsl[s] : s;
       for (int i = tid; i < hq * D; i += kThreads)
         reinterpret_cast<__nv_bfloat16*>(p.out)[(int64_t)row * hq * D + i] = __float2bfloat16_rn(0.f);

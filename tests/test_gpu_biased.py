@@ -288,6 +288,24 @@ def test_padding_that_looks_like_full_chunks(kv, q, cuda_device):
     b.check()
 
 
+@pytest.mark.parametrize("kv,q,hq", [("bf16", "bf16", 8), ("e4m3", "bf16", 8), ("f32", "f32", 8), ("f32", "f32", 2)])
+@pytest.mark.parametrize("rows", [1, 200, 362])
+def test_rows_past_the_queries_are_left_out(rows, kv, q, hq, cuda_device):
+    """query_start_loc that goes on past the rows of q and out (a step cut to fewer rows): the rows there are are right,
+    what lies behind them stays.  The cut falls behind a single row, inside the first chunk and before the last single
+    rows, one of them with an empty context; the buffers go on behind the cut."""
+    b = Batch(cuda_device, [1, 260, 1, 100, 1, 1], [90, 333, 40, 100, 200, 0], hq, 2, 64, 16, kv, q, cap=30.0, window=150,
+              seed=13)
+    exp, tol = b.expected()
+    whole = torch.full_like(b.out, 3.0)
+    b.q, b.out = b.q[:rows], whole[:rows]
+    b.run(decode=False)
+    torch.cuda.synchronize()
+    assert pa.workspace_error(b.ws) == 0
+    assert bool((whole[rows:] == 3).all())
+    assert bool(((b.out.double() - exp[:rows]).abs() <= tol[:rows]).all())
+
+
 @pytest.mark.parametrize("kv,q", [("bf16", "bf16"), ("e4m3", "bf16"), ("f32", "f32")])
 def test_a_window_past_every_context(kv, q, cuda_device):
     """The largest window hides nothing, whatever the prefix: its arithmetic does not wrap."""
