@@ -437,27 +437,47 @@ BiasedWs biased_workspace(const pa_cache_desc* d, int32_t num_seqs, int32_t num_
 
 bool biased_tc(const pa_cache_desc* d) { return d->q_dtype == kBF16; }
 
+// Sizes that the kernels of a biased step index in 32 bits; asked before
+// anything of the step is launched.
+int check_biased_sizes(const pa_cache_desc* d, int32_t num_seqs, int32_t num_tokens, int32_t max_blocks, bool chunks,
+                       const char* who) {
+  const int group = d->num_q_heads / d->num_kv_heads;
+  if (!biased_tc(d)) {
+    if (!biased_simt_fits(num_tokens, num_seqs, d->num_q_heads, d->num_kv_heads))
+      return fail(PA_ERR_UNSUPPORTED, "%s: %d rows of %d heads", who, num_tokens, d->num_q_heads);
+    return PA_OK;
+  }
+  if ((int64_t)num_seqs * max_blocks * (d->num_q_heads / cut_group(group, 8)) >= (int64_t)INT32_MAX)
+    return fail(PA_ERR_UNSUPPORTED, "%s: num_seqs * max_blocks_per_seq * heads reaches 2^31", who);
+  const int cut = cut_group(group, 128);
+  if (chunks && chunk_biased_units(num_tokens, num_seqs, cut, d->num_q_heads / cut) >= (int64_t)INT32_MAX)
+    return fail(PA_ERR_UNSUPPORTED, "%s: %d rows of %d heads in chunks", who, num_tokens, d->num_q_heads);
+  return PA_OK;
+}
+
 // Single-token rows of a biased step on the tensor-core decode (qsl null:
-// every row), on all SMs but the `beside` that chunk CTAs launched before it hold.
-int run_decode_biased(const pa_cache_desc* d, const pa_score_mod* mod, const void* q, const void* k_cache,
-                      const void* v_cache, const int32_t* block_tables, int32_t max_blocks, const int32_t* seq_lens,
-                      const int32_t* qsl, int32_t num_seqs, int32_t num_rows, float scale, int beside, void* out,
-                      void* workspace, const BiasedWs& w, int sms, cudaStream_t stream, const char* who) {
+// every row).
+struct Singles {
+  DecodeParams p;
+  CUtensorMap tm_k, tm_v;
+};
+
+int make_singles(const pa_cache_desc* d, const pa_score_mod* mod, const void* q, const void* k_cache,
+                 const void* v_cache, const int32_t* block_tables, int32_t max_blocks, const int32_t* seq_lens,
+                 const int32_t* qsl, int32_t num_seqs, int32_t num_rows, float scale, void* out, void* workspace,
+                 const BiasedWs& w, Singles* c) {
   int rc;
   const int group = d->num_q_heads / d->num_kv_heads, cut = cut_group(group, 8);
-  const int heads = d->num_q_heads / cut;
-  if ((int64_t)num_seqs * max_blocks * heads >= (int64_t)INT32_MAX)
-    return fail(PA_ERR_UNSUPPORTED, "%s: num_seqs * max_blocks_per_seq * heads reaches 2^31", who);
-  CUtensorMap tm_k, tm_v;
-  if ((rc = make_kv_map(&tm_k, k_cache, d->kv_dtype, d))) return rc;
+  if ((rc = make_kv_map(&c->tm_k, k_cache, d->kv_dtype, d))) return rc;
   if (d->kv_dtype == kBF16) {
-    if ((rc = make_kv_map(&tm_v, v_cache, d->kv_dtype, d))) return rc;
+    if ((rc = make_kv_map(&c->tm_v, v_cache, d->kv_dtype, d))) return rc;
   } else {
-    tm_v = tm_k;  // e4m3 V tiles are contiguous and come by bulk copy
+    c->tm_v = c->tm_k;  // e4m3 V tiles are contiguous and come by bulk copy
   }
   const bool fp8 = d->kv_dtype == kFP8;
   const float k_scale = fp8 && !d->k_head_scales ? d->k_scale : 1.f;
-  DecodeParams p = {};
+  DecodeParams& p = c->p;
+  p = {};
   p.q = static_cast<const uint8_t*>(q);
   p.out = static_cast<uint8_t*>(out);
   p.v_cache = static_cast<const uint8_t*>(v_cache);
@@ -468,7 +488,7 @@ int run_decode_biased(const pa_cache_desc* d, const pa_score_mod* mod, const voi
   p.rows.num_seqs = num_seqs;
   p.rows.num_rows = num_rows;
   p.num_q_heads = d->num_q_heads;
-  p.num_kv_heads = heads;
+  p.num_kv_heads = d->num_q_heads / cut;
   p.num_blocks = d->num_blocks;
   p.group = cut;
   p.scale_log2 = scale * kLog2e * k_scale;
@@ -477,13 +497,18 @@ int run_decode_biased(const pa_cache_desc* d, const pa_score_mod* mod, const voi
   p.v_head = fp8 ? d->v_head_scales : nullptr;
   p.mod = kernel_mod(mod, scale, k_scale);
   p.mod.sub = group / cut;
-  p.beside_chunks = beside > 0;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.ws.err = reinterpret_cast<int32_t*>(ws);
   p.ws.cnt = reinterpret_cast<unsigned int*>(ws + w.cnt);
   p.ws.ml = reinterpret_cast<float*>(ws + w.ml);
   p.ws.o = reinterpret_cast<float*>(ws + w.o);
-  cudaError_t e = launch_decode_biased(p, tm_k, tm_v, d->kv_dtype, d->head_dim, d->block_size, sms - beside, stream);
+  return PA_OK;
+}
+
+// ... on all SMs but the `beside` that chunk CTAs launched before it hold.
+int launch_singles(const pa_cache_desc* d, Singles& c, int sms, int beside, cudaStream_t stream, const char* who) {
+  c.p.beside_chunks = beside > 0;
+  cudaError_t e = launch_decode_biased(c.p, c.tm_k, c.tm_v, d->kv_dtype, d->head_dim, d->block_size, sms - beside, stream);
   if (e == cudaErrorNotSupported) return fail(PA_ERR_UNSUPPORTED, "%s: too many sequences for one launch", who);
   return cuda_status(e, who);
 }
@@ -1039,6 +1064,7 @@ int pa_decode_biased(const pa_cache_desc* d, const pa_score_mod* mod, const void
                            workspace, who);
   if (rc) return rc;
   if ((rc = check_mod(mod, scale, d, max_blocks_per_seq, who)) || num_seqs == 0) return rc;
+  if ((rc = check_biased_sizes(d, num_seqs, num_seqs, max_blocks_per_seq, false, who))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (biased_tc(d)) {
     int sms = 0;
@@ -1046,8 +1072,11 @@ int pa_decode_biased(const pa_cache_desc* d, const pa_score_mod* mod, const void
     const BiasedWs w = biased_workspace(d, num_seqs, num_seqs, sms);
     if (workspace_bytes < w.bytes)
       return fail(PA_ERR_INVALID_ARG, "%s: workspace %zu < %zu bytes", who, workspace_bytes, w.bytes);
-    return run_decode_biased(d, mod, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, nullptr, num_seqs,
-                             num_seqs, scale, 0, out, workspace, w, sms, st, who);
+    Singles c;
+    if ((rc = make_singles(d, mod, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, nullptr, num_seqs,
+                           num_seqs, scale, out, workspace, w, &c)))
+      return rc;
+    return launch_singles(d, c, sms, 0, st, who);
   }
   if (workspace_bytes < 256) return fail(PA_ERR_INVALID_ARG, "%s: workspace < 256 bytes", who);
   return run_biased_simt(d, mod, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, nullptr, num_seqs,
@@ -1070,6 +1099,7 @@ int pa_decode_chunked_prefill_biased(const pa_cache_desc* d, const pa_score_mod*
   if (num_tokens < 0 || max_q_len < 0) return fail(PA_ERR_INVALID_ARG, "%s: negative size", who);
   if (num_tokens == 0) return PA_OK;
   if (max_q_len == 0) return fail(PA_ERR_INVALID_ARG, "%s: max_q_len 0 with %d tokens", who, num_tokens);
+  if ((rc = check_biased_sizes(d, num_seqs, num_tokens, max_blocks_per_seq, max_q_len > 1, who))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   // single-token rows on the decode kernel, the others on the chunk kernel.
   // Rows that would fill every sequence up to max_q_len leave no single ones,
@@ -1085,20 +1115,21 @@ int pa_decode_chunked_prefill_biased(const pa_cache_desc* d, const pa_score_mod*
   const BiasedWs w = biased_workspace(d, num_seqs, num_tokens, sms);
   if (workspace_bytes < w.bytes)
     return fail(PA_ERR_INVALID_ARG, "%s: workspace %zu < %zu bytes", who, workspace_bytes, w.bytes);
-  auto decode = [&](int beside) {
-    return run_decode_biased(d, mod, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, query_start_loc,
-                             num_seqs, num_tokens, scale, beside, out, workspace, w, sms, st, who);
-  };
-  if (max_q_len == 1) return decode(0);
+  // every check is made and every map encoded before the first launch
+  Singles one;
   Chunks c;
+  if (decodes && (rc = make_singles(d, mod, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens,
+                                    query_start_loc, num_seqs, num_tokens, scale, out, workspace, w, &one)))
+    return rc;
+  if (max_q_len == 1) return launch_singles(d, one, sms, 0, st, who);
   if ((rc = make_chunks(d, mod, q, k_cache, v_cache, block_tables, max_blocks_per_seq, query_start_loc, seq_lens,
                         num_seqs, num_tokens, scale, decodes, out, workspace, w, &c)))
     return rc;
   const int ahead = decodes ? chunks_ahead(d, num_seqs, sms) : 0;
   if (ahead > 0 && (rc = launch_chunks(d, c, num_tokens, sms, ahead, true, st, who))) return rc;
-  if (decodes) rc = decode(ahead);
+  if (decodes) rc = launch_singles(d, one, sms, ahead, st, who);
   if (!rc) rc = launch_chunks(d, c, num_tokens, sms, ahead, false, st, who);
-  // a step that got no further leaves the unit counters to the next one
+  // a step whose later launch failed leaves the unit counters to the next one
   if (rc && ahead > 0) cudaMemsetAsync(c.p.unit_ctr, 0, 8, st);
   return rc;
 }

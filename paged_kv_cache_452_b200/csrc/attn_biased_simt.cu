@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(row_warps<KV, D>() * 32)
 // shared-memory vectors feed 64 (128) FMAs.  Bound: FMA issue and the shared
 // memory's loads (256 rows of 32 heads over 4000 keys, twice: 1.85 ms, 18
 // TFLOP/s; the row kernel with four pairs per CTA took 6.7 ms).
-constexpr int kR = 64;   // pairs of a CTA
+constexpr int kR = kBiasedTileRows;  // pairs of a CTA
 constexpr int kKT = 64;  // keys of a tile
 constexpr int kTileThreads = 256;
 template <int D>
@@ -410,7 +410,6 @@ template <int KV, int D>
 cudaError_t launch_tiles(const BiasedSimtParams& p, cudaStream_t stream) {
   const int G = p.a.num_q_heads / p.a.num_kv_heads;
   const int64_t blocks = (int64_t)p.a.rows.num_rows * G / kR + p.a.rows.num_seqs;
-  if (blocks > INT32_MAX || p.a.num_kv_heads > 65535) return cudaErrorNotSupported;
   auto kern = attn_biased_tile_kernel<KV, D>;
   static int set_for[64] = {0};  // the shared memory limit is raised once per device
   int dev = 0;
@@ -432,7 +431,8 @@ template <int KV, int D>
 cudaError_t launch_rows(const BiasedSimtParams& p, bool singles, bool chunks, cudaStream_t stream) {
   const bool tiles = chunks && (int64_t)p.a.rows.num_rows * p.a.num_q_heads >= 32 * kR;
   const bool rows = singles || (chunks && !tiles);
-  if (p.a.num_q_heads > 65535) return cudaErrorNotSupported;
+  if (!biased_simt_fits(p.a.rows.num_rows, p.a.rows.num_seqs, p.a.num_q_heads, p.a.num_kv_heads))
+    return cudaErrorNotSupported;  // (before either launch)
   if (rows) {
     attn_biased_row_kernel<KV, D><<<dim3((unsigned)p.a.rows.num_rows, (unsigned)p.a.num_q_heads),
                                     row_warps<KV, D>() * 32, 0, stream>>>(p, singles, chunks && !tiles);

@@ -1293,8 +1293,8 @@ cudaError_t launch_chunk_biased(const PrefillParams& p_in, const CUtensorMap& tm
   PrefillParams p = p_in;
   if (p.group < 1 || p.group > kRows || p.rows.num_seqs > kGroup * kMaxGroups) return cudaErrorNotSupported;
   for (int i = 0; i < 5; ++i) p.mod.poly[i] = kTanh[i] * p.mod.cap_out;
-  const int qb2 = 2 * (kRows / p.group);
-  const int64_t bound = ((int64_t)num_tokens / qb2 + p.rows.num_seqs) * p.num_kv_heads;  // units, at most
+  static_assert(kRows == 128, "chunk_biased_units counts query tiles of 128 rows");
+  const int64_t bound = chunk_biased_units(num_tokens, p.rows.num_seqs, p.group, p.num_kv_heads);
   if (bound <= 0) return cudaSuccess;
   if (bound >= INT32_MAX) return cudaErrorNotSupported;
   // units are cut into at most kMaxParts parts each

@@ -258,6 +258,11 @@ cudaError_t launch_prefill_umma(const PrefillParams& p, const CUtensorMap& tm_k,
 cudaError_t launch_chunk_biased(const PrefillParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                 const CUtensorMap& tm_q, int kv, int head_dim, int block_size, int num_tokens,
                                 int num_sms, int ahead, bool front, cudaStream_t stream);
+// Its units, at most: two query tiles of 128 / group positions each, per
+// kernel kv head.
+inline int64_t chunk_biased_units(int num_tokens, int num_seqs, int group, int heads) {
+  return ((int64_t)num_tokens / (2 * (128 / group)) + num_seqs) * heads;
+}
 // Slots per SM for cut units (a slot: one part of one unit, 256 rows; with 4
 // the 256 units of two long chunks were halved too, and took 415 us, not 344).
 constexpr int kPartSlots = 2;
@@ -283,10 +288,16 @@ struct SimtParams {
 };
 // Biased attention on CUDA cores (fp32 queries): of the sequences with one row
 // (`singles`; qsl nullptr: every sequence) and of those with more (`chunks`).
+constexpr int kBiasedTileRows = 64;  // (row, head) pairs of a tile kernel's CTA
 struct BiasedSimtParams {
   SimtParams a;
   ScoreMod mod;
 };
+// Whether both kernels' grids hold the step.
+inline bool biased_simt_fits(int num_rows, int num_seqs, int num_q_heads, int num_kv_heads) {
+  return num_q_heads <= 65535 &&
+         (int64_t)num_rows * (num_q_heads / num_kv_heads) / kBiasedTileRows + num_seqs <= INT32_MAX;
+}
 cudaError_t launch_attn_biased_simt(const BiasedSimtParams& p, int kv_dtype, bool singles, bool chunks,
                                     cudaStream_t stream);
 cudaError_t launch_attn_simt(const SimtParams& p, int q_dtype, int kv_dtype, cudaStream_t stream);

@@ -137,6 +137,27 @@ def test_biased_attention_refuses_pairs_that_are_not_built(kv, q):
         pa.pa_biased_workspace_size(desc, 2, 5)
 
 
+def test_biased_steps_check_sizes_before_the_first_launch():
+    """Sizes that a later kernel of a step could not take are turned down with the arguments, ahead of the device."""
+    mod = ctypes.byref(pa.ScoreMod(30.0, 10, None, None))
+
+    def chunk(desc, n, mb, t, mq):
+        return pa.lib().pa_decode_chunked_prefill_biased(ctypes.byref(desc), mod, P, P, P, P, mb, P, P, n, t, mq, 0.125, P,
+                                                         P, 1 << 40, None)
+    # a group of 16 is two kernel heads per kv head: 2^31 tiles although num_seqs * max_blocks * kv heads is below
+    wide = pa.CacheDesc.make(64, 16, 8, 128, 64, "bf16", "bf16")
+    assert chunk(wide, 16000, 10000, 20000, 300) == 2 and b"2^31" in pa.lib().pa_last_error()
+    assert pa.lib().pa_decode_biased(ctypes.byref(wide), mod, P, P, P, P, 10000, P, 16000, 0.125, P, P, 1 << 40, None) == 2
+    # 2^31 units of chunk rows
+    many = pa.CacheDesc.make(64, 16, 512, 512, 64, "bf16", "bf16")
+    assert chunk(many, 2, 4, 2**30 + 2**21, 2**30) == 2 and b"chunks" in pa.lib().pa_last_error()
+    # fp32: the grids of the row kernel and of the tile kernel
+    f32 = pa.CacheDesc.make(64, 16, 1, 70000, 64, "f32", "f32")
+    assert chunk(f32, 2, 4, 100, 50) == 2
+    f32 = pa.CacheDesc.make(64, 16, 1, 1024, 64, "f32", "f32")
+    assert chunk(f32, 2, 4, 2**28, 2**27) == 2
+
+
 def test_biased_bindings_refuse_wrong_tensors():
     bf, i32 = torch.bfloat16, torch.int32
     desc = pa.CacheDesc.make(4, 16, 2, 8, 64, "bf16", "bf16")
