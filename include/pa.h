@@ -206,7 +206,9 @@ size_t pa_decode_workspace_size(const pa_cache_desc* desc, int32_t num_seqs);
  * «Идея и механизм»); the result is the one dense attention gives over the
  * same keys ("PagedAttention：KV cache 即虚拟内存（block manager & 碎片）",
  * the follow-up "分页改变输出或加速 kernel 吗？").
- *   q           device, [num_seqs][num_q_heads][head_dim], q_dtype
+ *   q           device, [num_seqs][num_q_heads][head_dim], q_dtype; bf16
+ *               queries over an e4m3 pool are taken as f16 on the tensor
+ *               cores: keep them within 65504
  *   block_tables device, int32 [num_seqs][max_blocks_per_seq]
  *   seq_lens    device, int32 [num_seqs]; 0 gives a zero output row
  *   out         device, [num_seqs][num_q_heads][head_dim], q_dtype
@@ -393,7 +395,9 @@ size_t pa_biased_workspace_size(const pa_cache_desc* desc, int32_t num_seqs, int
  * error word as for pa_decode; `scale` positive and finite.  bf16 queries over
  * a bf16 or e4m3 pool run on the tensor cores for every group and head_dim,
  * fp32 queries over an fp32 or e4m3 pool on CUDA cores; other pairs are
- * PA_ERR_UNSUPPORTED (their workspace size is 0).  V rows that no query of the sequence sees may
+ * PA_ERR_UNSUPPORTED (their workspace size is 0).  Over an e4m3 pool a bf16
+ * query row is brought into f16's range by a power of two, exactly but for
+ * elements below 2^-28 of its largest.  V rows that no query of the sequence sees may
  * hold anything, NaN included. */
 int pa_decode_biased(const pa_cache_desc* desc, const pa_score_mod* mod, const void* q, const void* k_cache,
                      const void* v_cache, const int32_t* block_tables, int32_t max_blocks_per_seq,

@@ -36,7 +36,8 @@
 //    of arrival.  (One 512-row chunk over 8300 keys, 32 heads: 155 -> 90 us.)
 //  * e4m3 pools: blocks land raw (bulk copies), four converter warps write them
 //    as f16 (exact) into the swizzled K and V tiles, V as rows of d with
-//    their keys contiguous (what its d-major blocks give), and the queries are rounded to f16; P is f16.
+//    their keys contiguous (what its d-major blocks give), and the queries
+//    become f16, each row times a power of two that keeps it in range; P is f16.
 //
 // What bounds it (measured on B200, clocks per step of both query tiles): the
 // products 1280 (S at N = 64 reads its 6 KB of operands per MMA at the shared
@@ -742,8 +743,20 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
           cap_in *= ks;
         }
         if (p.v_head) osc *= __ldg(p.v_head + head);
-        // the queries as f16, in place
+        // the queries as f16, in place, each row by a power of two that keeps
+        // it in f16's range (its scores' factors take it back)
         wait_ok(q_raw, (uint32_t)(n & 1));
+        uint32_t most = 0;
+#pragma unroll
+        for (int v = 0; v < T::NCH * 8; ++v) {
+          const uint4 b = *reinterpret_cast<const uint4*>(qs + (v >> 3) * kTileRow + r * 128 + (v & 7) * 16);
+          most = dev::max_bf16_bits(dev::max_bf16_bits(most, b.x), b.y);
+          most = dev::max_bf16_bits(dev::max_bf16_bits(most, b.z), b.w);
+        }
+        float up, down;
+        dev::f16_row_scale(most, up, down);
+        scale *= down;
+        cap_in *= down;
 #pragma unroll
         for (int v = 0; v < T::NCH * 8; ++v) {
           uint4* w = reinterpret_cast<uint4*>(qs + (v >> 3) * kTileRow + r * 128 + (v & 7) * 16);
@@ -751,7 +764,7 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
           uint32_t* e = &b.x;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            e[i] = dev::pack_f16(dev::bf16_bits_to_f32(e[i] & 0xFFFFu), dev::bf16_bits_to_f32(e[i] >> 16));
+            e[i] = dev::pack_f16(dev::bf16_bits_to_f32(e[i] & 0xFFFFu) * up, dev::bf16_bits_to_f32(e[i] >> 16) * up);
           *w = b;
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");

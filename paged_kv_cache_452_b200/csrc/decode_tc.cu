@@ -516,10 +516,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<KV>())
     const float osc = p.v_head ? p.out_scale * __ldg(p.v_head + ph) : p.out_scale;
     Span span{0, 0, 0, 0};
     const float kf0 = (float)(C::FP8 ? kperm(g) : g), kf1 = (float)(C::FP8 ? kperm(g + 8) : g + 8);  // this thread's keys of a tile
-    float cap_in = 0.f, sp0 = 0.f, sp1 = 0.f;  // the piece's cap factor and this thread's columns' slopes (log2 units)
+    // this thread's columns' score factors (the cap's, or without one the
+    // softmax scale) and slopes (log2 units)
+    float in0 = 0.f, in1 = 0.f, sp0 = 0.f, sp1 = 0.f;
     if constexpr (MOD) {
       span = seq_span<BS>(p, s, min(__ldg(p.rows.seq_lens + s), p.max_blocks * BS));
-      cap_in = p.mod.cap_in * khs;
+      in0 = in1 = p.mod.cap_out > 0.f ? p.mod.cap_in * khs : sl2;
       if (p.mod.slopes) {
         const float log2e = 1.4426950408889634f;
         if (c0 < G) sp0 = __ldg(p.mod.slopes + h * G + c0) * log2e;
@@ -567,14 +569,33 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<KV>())
           // d order inside a 16-wide k-step follows the e4m3 byte pairs
           // (a thread's four bytes of a K row are d 4t..4t+3):
           // logical k (2t, 2t+1 | 2t+8, 2t+9) <-> d (4t, 4t+1 | 4t+2, 4t+3)
+          float up = 1.f;
+          if constexpr (MOD) {
+            // bf16 reaches past f16 at both ends: a power of two per row
+            // brings its largest element to f16's 2^14, the row's factor
+            // takes it back
+            uint32_t most = 0;
+#pragma unroll
+            for (int kk = 0; kk < C::KSTEPS; ++kk) {
+              const uint2 w = g < G ? *reinterpret_cast<const uint2*>(qs + (16 * kk + 4 * tq) * 2) : make_uint2(0u, 0u);
+              most = dev::max_bf16_bits(most, w.x);
+              most = dev::max_bf16_bits(most, w.y);
+            }
+            most = __vmaxu2(most, __shfl_xor_sync(0xffffffffu, most, 1));
+            most = __vmaxu2(most, __shfl_xor_sync(0xffffffffu, most, 2));
+            float down;
+            dev::f16_row_scale(most, up, down);
+            in0 *= __shfl_sync(0xffffffffu, down, 4 * c0);
+            in1 *= __shfl_sync(0xffffffffu, down, 4 * c1);
+          }
 #pragma unroll
           for (int kk = 0; kk < C::KSTEPS; ++kk) {
             uint2 w = make_uint2(0u, 0u);
             if (g < G) w = *reinterpret_cast<const uint2*>(qs + (16 * kk + 4 * tq) * 2);
             const float q0 = dev::bf16_bits_to_f32(w.x & 0xFFFFu), q1 = dev::bf16_bits_to_f32(w.x >> 16);
             const float q2 = dev::bf16_bits_to_f32(w.y & 0xFFFFu), q3 = dev::bf16_bits_to_f32(w.y >> 16);
-            qf[kk][0] = dev::pack_f16(q0, q1);
-            qf[kk][1] = dev::pack_f16(q2, q3);
+            qf[kk][0] = MOD ? dev::pack_f16(q0 * up, q1 * up) : dev::pack_f16(q0, q1);
+            qf[kk][1] = MOD ? dev::pack_f16(q2 * up, q3 * up) : dev::pack_f16(q2, q3);
           }
         }
       }
@@ -683,10 +704,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<KV>())
           float x[4] = {acc0[0] + acc1[0], acc0[1] + acc1[1], acc0[2] + acc1[2], acc0[3] + acc1[3]};
           if (p.mod.cap_out > 0.f) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = dev::capped(x[i], cap_in, p.mod.cap_out);
+            for (int i = 0; i < 4; ++i) x[i] = dev::capped(x[i], i & 1 ? in1 : in0, p.mod.cap_out);
           } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] *= sl2;
+            for (int i = 0; i < 4; ++i) x[i] *= i & 1 ? in1 : in0;
           }
           if (p.mod.slopes) {
             // minus slope times distance: the tile's first key's, and the

@@ -402,6 +402,19 @@ __device__ __forceinline__ float rcp(float x) {
 __device__ __forceinline__ float capped(float x, float in, float out) {
   return fmaf(-2.f * out, rcp(1.f + ex2(x * in)), out);
 }
+// The larger magnitudes of two bf16 pairs, as bits (they order as integers).
+__device__ __forceinline__ uint32_t max_bf16_bits(uint32_t most, uint32_t pair) {
+  return __vmaxu2(most, pair & 0x7FFF7FFFu);
+}
+// Powers of two for a bf16 row that becomes f16: `up` brings its largest
+// element (`most`: a pair of candidates, as bits) to [2^14, 2^15), so that
+// every element within 2^-28 of it stays exact; down = 1 / up.
+__device__ __forceinline__ void f16_row_scale(uint32_t most, float& up, float& down) {
+  const int e = (int)(max(most & 0xFFFFu, most >> 16) >> 7);  // biased exponent
+  const int k = min(126, 14 + 127 - e);                       // (e = 255: infinities stay, k = -114)
+  up = __int_as_float((127 + k) << 23);
+  down = __int_as_float((127 - k) << 23);
+}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);

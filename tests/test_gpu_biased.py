@@ -429,6 +429,29 @@ def test_scores_that_fill_the_cap(cuda_device):
         b.check()
 
 
+@pytest.mark.parametrize("cap", [0.0, 30.0])
+@pytest.mark.parametrize("size", [2.0**-60, 2.0**-30, 2.0**14, 2.0**20, 2.0**100])
+def test_queries_past_the_range_of_f16(size, cap, cuda_device):
+    """bf16 queries that f16 cannot hold, with a scale that brings their scores back: an e4m3 pool's products take them
+    as they are (a power of two changes nothing else in the arithmetic)."""
+    for qlens, lens in (([1] * 4, [300, 17, 64, 900]), ([70, 1, 130], [200, 90, 130])):
+        b = Batch(cuda_device, qlens, lens, 12, 2, 128, 16, "e4m3", "bf16", cap=cap, seed=14)
+        b.q, b.scale = (b.q.float() * size).to(torch.bfloat16), b.scale / size
+        b.run()
+        b.check()
+
+
+def test_queries_of_many_sizes_in_a_group(cuda_device):
+    """Heads of one group whose queries differ by powers of two, a row of zeros among them: every row by its own."""
+    for qlens, lens in (([1] * 3, [300, 17, 900]), ([70, 1, 20], [200, 90, 130])):
+        b = Batch(cuda_device, qlens, lens, 8, 1, 64, 32, "e4m3", "bf16", cap=0.0, slopes=True, seed=15)
+        size = 2.0 ** torch.tensor([0, -40, 1, -20, 0, 2, -100, 0], device=cuda_device)
+        b.q = (b.q.float() * size[None, :, None]).to(torch.bfloat16)
+        b.q[:, 4] = 0
+        b.run()
+        b.check()
+
+
 def test_without_mod_as_plain_attention(cuda_device):
     """With nothing set the biased decode computes what pa_decode does.  The two cut contexts into different pieces,
     and a weight is rounded to bf16 relative to its piece's reference, so a weight may differ by two roundings of
