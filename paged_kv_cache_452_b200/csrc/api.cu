@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdarg>
@@ -595,11 +596,22 @@ int chunks_ahead(const pa_cache_desc* d, int num_seqs, int sms) {
   return d->kv_dtype == kBF16 && (int64_t)num_seqs * d->num_kv_heads >= 2LL * sms ? sms * 3 / 8 : 0;
 }
 
+// Rows of a step that belong to chunks, as far as its sizes tell: the step's
+// rows without those of sequences with a single one, if no sequence is empty
+// and its chunks are as long as they may be; at least one of max_q_len rows.
+int32_t chunk_rows(int32_t num_seqs, int32_t num_tokens, int32_t max_q_len) {
+  if (max_q_len <= 1) return 0;
+  const int64_t more = num_tokens > num_seqs ? num_tokens - num_seqs : 0;
+  const int64_t rows = more + (more + max_q_len - 2) / (max_q_len - 1);
+  return (int32_t)std::min<int64_t>(num_tokens, std::max<int64_t>(max_q_len, rows));
+}
+
 int run_biased_simt(const pa_cache_desc* d, const pa_score_mod* mod, const void* q, const void* k_cache,
                     const void* v_cache, const int32_t* block_tables, int32_t max_blocks, const int32_t* seq_lens,
-                    const int32_t* qsl, int32_t num_seqs, int32_t num_rows, bool singles, bool chunks, float scale,
-                    void* out, void* workspace, cudaStream_t stream, const char* who) {
+                    const int32_t* qsl, int32_t num_seqs, int32_t num_rows, int32_t max_q_len, float scale, void* out,
+                    void* workspace, cudaStream_t stream, const char* who) {
   BiasedSimtParams b = {};
+  b.chunk_rows = chunk_rows(num_seqs, num_rows, max_q_len);
   SimtParams& p = b.a;
   p.num_blocks = d->num_blocks;
   p.err = static_cast<int32_t*>(workspace);
@@ -625,7 +637,7 @@ int run_biased_simt(const pa_cache_desc* d, const pa_score_mod* mod, const void*
     p.v_head = d->v_head_scales;
   }
   b.mod = kernel_mod(mod, scale, 1.f);
-  cudaError_t e = launch_attn_biased_simt(b, d->kv_dtype, singles, chunks, stream);
+  cudaError_t e = launch_attn_biased_simt(b, d->kv_dtype, stream);
   if (e == cudaErrorNotSupported)
     return fail(PA_ERR_UNSUPPORTED, "%s: q dtype %d with kv dtype %d, %d rows", who, d->q_dtype, d->kv_dtype, num_rows);
   return cuda_status(e, who);
@@ -1080,7 +1092,7 @@ int pa_decode_biased(const pa_cache_desc* d, const pa_score_mod* mod, const void
   }
   if (workspace_bytes < 256) return fail(PA_ERR_INVALID_ARG, "%s: workspace < 256 bytes", who);
   return run_biased_simt(d, mod, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, nullptr, num_seqs,
-                         num_seqs, true, false, scale, out, workspace, st, who);
+                         num_seqs, 1, scale, out, workspace, st, who);
 }
 
 int pa_decode_chunked_prefill_biased(const pa_cache_desc* d, const pa_score_mod* mod, const void* q,
@@ -1108,7 +1120,7 @@ int pa_decode_chunked_prefill_biased(const pa_cache_desc* d, const pa_score_mod*
   if (!biased_tc(d)) {
     if (workspace_bytes < 256) return fail(PA_ERR_INVALID_ARG, "%s: workspace < 256 bytes", who);
     return run_biased_simt(d, mod, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, query_start_loc,
-                           num_seqs, num_tokens, true, max_q_len > 1, scale, out, workspace, st, who);
+                           num_seqs, num_tokens, max_q_len, scale, out, workspace, st, who);
   }
   int sms = 0;
   if ((rc = num_sms(&sms))) return rc;

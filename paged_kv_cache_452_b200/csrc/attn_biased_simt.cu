@@ -53,7 +53,7 @@ constexpr int row_warps() { return D == 64 || KV == kFP8 ? 16 : 8; }
 
 template <int KV, int D>
 __global__ void __launch_bounds__(row_warps<KV, D>() * 32)
-    attn_biased_row_kernel(const BiasedSimtParams bp, bool singles, bool chunks) {
+    attn_biased_row_kernel(const BiasedSimtParams bp, bool chunks) {
   dev::grid_dep_wait();
   const SimtParams& p = bp.a;
   constexpr int kWarps = row_warps<KV, D>();
@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(row_warps<KV, D>() * 32)
     s = lo;
     first = p.rows.qsl[s];
     qlen = p.rows.qsl[s + 1] - first;
-    if (row < first || row >= first + qlen || !(qlen > 1 ? chunks : singles)) return;
+    if (row < first || row >= first + qlen || (qlen > 1 && !chunks)) return;
   }
   int len = p.rows.seq_lens[s];
   const int pos = len - qlen + row - first;
@@ -426,35 +426,31 @@ cudaError_t launch_tiles(const BiasedSimtParams& p, cudaStream_t stream) {
 
 // The tile kernel where the chunks' pairs make 32 CTAs of it or more (below
 // that the row kernel's many short CTAs are faster: 33 rows of 8 heads over 500
-// keys 33 us against 120, 512 over 1000 580 against 309).
+// keys 33 us against 120, 512 over 1000 580 against 309; beside 62 single rows
+// of 32 heads over 500 keys a 2-row chunk 181 us a step against 276).
 template <int KV, int D>
-cudaError_t launch_rows(const BiasedSimtParams& p, bool singles, bool chunks, cudaStream_t stream) {
-  const bool tiles = chunks && (int64_t)p.a.rows.num_rows * p.a.num_q_heads >= 32 * kR;
-  const bool rows = singles || (chunks && !tiles);
+cudaError_t launch_rows(const BiasedSimtParams& p, cudaStream_t stream) {
+  const bool tiles = (int64_t)p.chunk_rows * p.a.num_q_heads >= 32 * kR;
   if (!biased_simt_fits(p.a.rows.num_rows, p.a.rows.num_seqs, p.a.num_q_heads, p.a.num_kv_heads))
     return cudaErrorNotSupported;  // (before either launch)
-  if (rows) {
-    attn_biased_row_kernel<KV, D><<<dim3((unsigned)p.a.rows.num_rows, (unsigned)p.a.num_q_heads),
-                                    row_warps<KV, D>() * 32, 0, stream>>>(p, singles, chunks && !tiles);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || !tiles) return e;
-  }
-  return tiles ? launch_tiles<KV, D>(p, stream) : cudaSuccess;
+  attn_biased_row_kernel<KV, D><<<dim3((unsigned)p.a.rows.num_rows, (unsigned)p.a.num_q_heads),
+                                  row_warps<KV, D>() * 32, 0, stream>>>(p, !tiles);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess && tiles ? launch_tiles<KV, D>(p, stream) : e;
 }
 
 template <int KV>
-cudaError_t launch_d(const BiasedSimtParams& p, bool singles, bool chunks, cudaStream_t stream) {
-  if (p.a.head_dim == 64) return launch_rows<KV, 64>(p, singles, chunks, stream);
-  if (p.a.head_dim == 128) return launch_rows<KV, 128>(p, singles, chunks, stream);
+cudaError_t launch_d(const BiasedSimtParams& p, cudaStream_t stream) {
+  if (p.a.head_dim == 64) return launch_rows<KV, 64>(p, stream);
+  if (p.a.head_dim == 128) return launch_rows<KV, 128>(p, stream);
   return cudaErrorNotSupported;
 }
 
 }  // namespace
 
-cudaError_t launch_attn_biased_simt(const BiasedSimtParams& p, int kv_dtype, bool singles, bool chunks,
-                                    cudaStream_t stream) {
-  if (kv_dtype == kF32) return launch_d<kF32>(p, singles, chunks, stream);
-  if (kv_dtype == kFP8) return launch_d<kFP8>(p, singles, chunks, stream);
+cudaError_t launch_attn_biased_simt(const BiasedSimtParams& p, int kv_dtype, cudaStream_t stream) {
+  if (kv_dtype == kF32) return launch_d<kF32>(p, stream);
+  if (kv_dtype == kFP8) return launch_d<kFP8>(p, stream);
   return cudaErrorNotSupported;
 }
 

@@ -286,20 +286,20 @@ struct SimtParams {
   int32_t num_blocks;      // table entries outside [0, num_blocks) are flagged and read as block 0
   int32_t* err;            // error word of the caller's workspace
 };
-// Biased attention on CUDA cores (fp32 queries): of the sequences with one row
-// (`singles`; qsl nullptr: every sequence) and of those with more (`chunks`).
+// Biased attention on CUDA cores (fp32 queries), of every row (qsl nullptr: one
+// per sequence).
 constexpr int kBiasedTileRows = 64;  // (row, head) pairs of a tile kernel's CTA
 struct BiasedSimtParams {
   SimtParams a;
   ScoreMod mod;
+  int32_t chunk_rows;  // rows of sequences with more than one, about: chooses the kernel that takes those
 };
 // Whether both kernels' grids hold the step.
 inline bool biased_simt_fits(int num_rows, int num_seqs, int num_q_heads, int num_kv_heads) {
   return num_q_heads <= 65535 &&
          (int64_t)num_rows * (num_q_heads / num_kv_heads) / kBiasedTileRows + num_seqs <= INT32_MAX;
 }
-cudaError_t launch_attn_biased_simt(const BiasedSimtParams& p, int kv_dtype, bool singles, bool chunks,
-                                    cudaStream_t stream);
+cudaError_t launch_attn_biased_simt(const BiasedSimtParams& p, int kv_dtype, cudaStream_t stream);
 cudaError_t launch_attn_simt(const SimtParams& p, int q_dtype, int kv_dtype, cudaStream_t stream);
 
 }  // namespace pa

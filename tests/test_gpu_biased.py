@@ -237,6 +237,18 @@ def test_fp32_chunks_in_tiles(hq, hkv, d, bs, kv, mod, cuda_device):
     b.check()
 
 
+@pytest.mark.parametrize("kv", ["f32", "e4m3"])
+@pytest.mark.parametrize("qlens", [[1] * 30 + [2] + [1] * 32, [1] * 30 + [70] + [1] * 32, [0] * 90 + [80] + [0] * 30],
+                         ids=["a short chunk", "a long chunk", "empty sequences"])
+def test_fp32_chunks_among_single_rows(qlens, kv, cuda_device):
+    """fp32: many single rows beside one chunk, and a chunk among empty sequences."""
+    rng = np.random.default_rng(16)
+    lens = [q + int(rng.integers(0, 300)) for q in qlens]
+    b = Batch(cuda_device, qlens, lens, 32, 4, 64, 16, kv, "f32", cap=30.0, slopes=True, seed=16)
+    b.run(decode=False)
+    b.check()
+
+
 def test_many_chunks(cuda_device):
     """More chunks than are put in order, between decode rows and empty sequences."""
     rng = np.random.default_rng(2)
