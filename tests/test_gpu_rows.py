@@ -146,6 +146,61 @@ def test_norm_rope_write_matches_fp64(n, hq, hkv, d, bs, kv, q, rot, inter, how,
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
 
 
+def four_row_groups(n, hq, hkv, d):
+    """Whether a call has more lanes of work than one launch of the GPU holds: then a row group has four head rows."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    return n * (hq + 2 * hkv) * (d // 8) > sms * 2048
+
+
+@pytest.mark.parametrize("n,hq,hkv,d,bs,kv,q,rot,inter,how,head_scales", [
+    (2500, 7, 1, 128, 16, "bf16", "bf16", 128, False, "runs", False),
+    (2500, 9, 3, 128, 32, "e4m3", "bf16", 128, False, "runs", True),
+    (2500, 9, 1, 128, 16, "e4m3", "f32", 128, False, "runs", False),
+    (6000, 6, 3, 64, 16, "f32", "f32", 64, False, "any", False),
+    (6000, 5, 5, 64, 32, "e4m3", "bf16", 64, False, "any", False),
+    (2500, 6, 3, 128, 16, "e4m3", "bf16", 64, True, "runs", False),
+    (6000, 9, 3, 64, 32, "bf16", "bf16", 16, False, "any", False),
+    (2500, 10, 2, 128, 16, "f32", "f32", 40, True, "runs", False),
+    (2500, 7, 1, 128, 16, "bf16", "bf16", 0, False, "runs", False),
+])
+def test_norm_rope_write_in_groups_of_four_rows(n, hq, hkv, d, bs, kv, q, rot, inter, how, head_scales, cuda_device):
+    """Steps large enough for four head rows per group, head counts that leave a group unfilled, every form of the
+    rotation and every pool."""
+    assert four_row_groups(n, hq, hkv, d)
+    test_norm_rope_write_matches_fp64(n, hq, hkv, d, bs, kv, q, rot, inter, how, head_scales, cuda_device)
+
+
+@pytest.mark.parametrize("n,hq,hkv,d,bs,q,how,head_scales", [
+    (301, 5, 5, 128, 16, "bf16", "runs", True), (77, 6, 3, 64, 32, "bf16", "any", False),
+    (45, 3, 1, 64, 16, "f32", "runs", False), (16, 8, 2, 128, 32, "f32", "any", True)])
+def test_e4m3_keys_normed_and_rotated_over_the_whole_head(n, hq, hkv, d, bs, q, how, head_scales, cuda_device):
+    test_norm_rope_write_matches_fp64(n, hq, hkv, d, bs, "e4m3", q, d, False, how, head_scales, cuda_device)
+
+
+@pytest.mark.parametrize("n,hq,hkv,d", [(37, 6, 3, 128), (2500, 9, 3, 128), (6000, 6, 3, 64)])
+@pytest.mark.parametrize("kv,q", [("bf16", "bf16"), ("e4m3", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("inter,part", [(False, 1), (True, 1), (False, 2)])
+def test_rotation_without_a_norm_and_with_one_of_the_two(inter, part, kv, q, n, hq, hkv, d, cuda_device):
+    assert four_row_groups(n, hq, hkv, d) == (n > 1000)
+    desc, kc, vc, (xq, xk, xv), slots, _, rng, g = setup(n, hq, hkv, d, 16, kv, q, "runs", cuda_device, n + part)
+    rot = d // part
+    table = table_of(3000, rot, cuda_device)
+    pos = torch.from_numpy(rng.integers(0, 3000, n).astype(np.int32)).to(cuda_device)
+    kw = (1 + 0.3 * torch.randn(d, generator=g, device=cuda_device)).to(DT[q])
+    for w in (None, kw):
+        out = torch.full((n, hq, d), float("nan"), dtype=DT[q], device=cuda_device)
+        pa.pa_norm_rope_write(desc, pa.QkPrep.make(None, w, 1e-5, table, inter), xq, xk, xv, pos, slots, out, kc, vc)
+        close(out, fp64_rows(xq, None, 1e-5, table, pos, rot, inter), HALF[q])
+        gk, gv = pool_rows(desc, kc, vc, slots)
+        ek = fp64_rows(xk, w, 1e-5, table, pos, rot, inter)
+        if kv == "e4m3":
+            close_e4m3(gk, ek, KS)
+            close_e4m3(gv, xv.double(), VS)
+        else:
+            close(gk, ek, HALF[q])
+            assert torch.equal(gv, xv)
+
+
 def test_norm_rope_write_without_norm_is_a_rotation_and_a_copy(cuda_device):
     desc, kc, vc, (xq, xk, xv), slots, _, rng, g = setup(37, 8, 2, 128, 16, "bf16", "bf16", "runs", cuda_device, 3)
     out = torch.empty_like(xq, memory_format=torch.contiguous_format)
@@ -240,6 +295,17 @@ def test_cache_read_matches_the_pool(n, hkv, d, bs, kv, q, how, head_scales, cud
             assert torch.equal(got[~nan], exp[~nan])
         else:
             assert torch.equal(got.contiguous().view(torch.uint8), exp.contiguous().view(torch.uint8))
+
+
+@pytest.mark.parametrize("n,hkv,d,bs,kv,q,how,head_scales", [
+    (2500, 5, 128, 16, "e4m3", "bf16", "runs", True), (5000, 5, 64, 32, "e4m3", "bf16", "any", False),
+    (2500, 3, 128, 32, "e4m3", "f32", "runs", False), (3001, 7, 64, 16, "e4m3", "f32", "any", True),
+    (2500, 3, 128, 16, "f32", "f32", "any", False), (5003, 5, 64, 32, "bf16", "bf16", "runs", False)])
+def test_cache_read_of_many_rows(n, hkv, d, bs, kv, q, how, head_scales, cuda_device):
+    """Calls large enough for four vectors per thread."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert 2 * n * hkv * (d * (4 if q == "f32" else 2) // 16) > sms * 2048
+    test_cache_read_matches_the_pool(n, hkv, d, bs, kv, q, how, head_scales, cuda_device)
 
 
 def test_write_then_read_back(cuda_device):
