@@ -359,6 +359,8 @@ class ScoreMod(ctypes.Structure):
         device fp32 [num_q_heads], the score loses slope * distance; prefix_lens: device int32 [num_seqs], leading
         keys that every row sees."""
         who = "ScoreMod.make"
+        if not 0 <= int(window) < 2**31:  # (the struct's field would wrap)
+            raise PaError(1, f"{who}: window {window} (0, or keys up to 2^31 - 1)")
         devs = set()
         if slopes is not None:
             devs.add(_parameter(who, "slopes", slopes, (torch.float32,), 1))

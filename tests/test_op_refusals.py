@@ -158,6 +158,13 @@ def test_biased_steps_check_sizes_before_the_first_launch():
     assert chunk(f32, 2, 4, 2**28, 2**27) == 2
 
 
+def test_a_window_past_32_bits_is_refused():
+    for window in (2**31, 2**32 + 5, -1):
+        with pytest.raises(pa.PaError, match="window"):
+            pa.ScoreMod.make(window=window)
+    assert pa.ScoreMod.make(window=2**31 - 1).window == 2**31 - 1
+
+
 def test_biased_bindings_refuse_wrong_tensors():
     bf, i32 = torch.bfloat16, torch.int32
     desc = pa.CacheDesc.make(4, 16, 2, 8, 64, "bf16", "bf16")
