@@ -410,7 +410,8 @@ int pa_decode_biased(const pa_cache_desc* desc, const pa_score_mod* mod, const v
  * the workspace as for pa_decode_chunked_prefill and pa_decode_biased, but
  * num_tokens may be above query_start_loc[num_seqs] (a step padded to a fixed
  * size): the rows past it are left as they were.  Rows that query_start_loc
- * places past num_tokens are left out.  A V row that some rows of a
+ * places past num_tokens are left out; with num_tokens 0 nothing is done, and
+ * q and out may be NULL.  A V row that some rows of a
  * sequence see has to be finite: the weight 0 of a row that does not see it
  * still multiplies it. */
 int pa_decode_chunked_prefill_biased(const pa_cache_desc* desc, const pa_score_mod* mod, const void* q,

@@ -1103,6 +1103,10 @@ int pa_decode_chunked_prefill_biased(const pa_cache_desc* d, const pa_score_mod*
                                      size_t workspace_bytes, void* stream) {
   clear_error();
   const char* who = "pa_decode_chunked_prefill_biased";
+  if (num_tokens == 0) {  // no rows: q and out may be NULL, as empty tensors are
+    if (!q) q = workspace;
+    if (!out) out = workspace;
+  }
   int rc = check_attn_args(d, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, num_seqs, out,
                            workspace, who);
   if (rc) return rc;

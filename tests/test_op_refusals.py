@@ -158,6 +158,18 @@ def test_biased_steps_check_sizes_before_the_first_launch():
     assert chunk(f32, 2, 4, 2**28, 2**27) == 2
 
 
+def test_a_step_without_rows_needs_no_queries():
+    """A step of sequences that all have no new rows: its q and out are empty tensors, whose address is NULL."""
+    desc = pa.CacheDesc.make(16, 16, 2, 8, 64, "bf16", "bf16")
+    mod = pa.ScoreMod(30.0, 10, None, None)
+
+    def chunk(t, q, out, n=2):
+        return pa.lib().pa_decode_chunked_prefill_biased(ctypes.byref(desc), ctypes.byref(mod), q, P, P, P, 4, P, P, n, t, 1,
+                                                         0.125, out, P, 1 << 30, None)
+    assert chunk(0, None, None) == 0 and chunk(0, None, None, n=0) == 0
+    assert chunk(1, None, P) == 1 and chunk(1, P, None) == 1 and chunk(-1, None, None) == 1
+
+
 def test_a_window_past_32_bits_is_refused():
     for window in (2**31, 2**32 + 5, -1):
         with pytest.raises(pa.PaError, match="window"):
