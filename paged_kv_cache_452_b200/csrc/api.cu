@@ -101,6 +101,18 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
+// An encode by the driver, which asks for a context of the calling thread.  A
+// host thread that has made no call of its own yet has none bound: the
+// runtime binds the device's.
+template <class F>
+CUresult with_context(F encode) {
+  CUresult r = encode();
+  int dev = 0;
+  if (r == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess)
+    r = encode();
+  return r;
+}
+
 // 2-D map over a token-major pool viewed as rows of head_dim elements; one
 // box is [block_size rows][128 bytes] with 128-byte swizzle.
 int encode_kv_map(CUtensorMap* m, const void* base, int dt, const pa_cache_desc* d);
@@ -151,10 +163,12 @@ int encode_kv_map(CUtensorMap* m, const void* base, int dt, const pa_cache_desc*
   if (strides[0] < dims[0] * eb || strides[0] % 16 != 0)
     return fail(PA_ERR_INVALID_ARG, "tensor map: row stride %llu bytes for %llu-byte rows",
                 (unsigned long long)strides[0], (unsigned long long)(dims[0] * eb));
-  CUresult r = enc(m, dt == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
-                   const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   row < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUresult r = with_context([&] {
+    return enc(m, dt == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+               const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               row < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  });
   if (r != CUDA_SUCCESS) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   return PA_OK;
 }
@@ -172,9 +186,11 @@ int encode_q_map(CUtensorMap* m, const void* q, int num_tokens, const pa_cache_d
   cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)(128 / group)};
   cuuint32_t estr[3] = {1, 1, 1};
   if (!aligned(q, 16)) return fail(PA_ERR_INVALID_ARG, "q must be 16-byte aligned");
-  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUresult r = with_context([&] {
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  });
   if (r != CUDA_SUCCESS) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   return PA_OK;
 }

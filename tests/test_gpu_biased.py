@@ -497,6 +497,33 @@ def test_bad_table_entries_and_long_contexts_are_flagged(cuda_device):
         assert pa.workspace_error(b.ws) == 3
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("which", ["pa_decode_biased", "pa_decode_chunked_prefill_biased", "pa_decode"])
+def test_first_call_of_a_host_thread(which, kv, cuda_device):
+    """A call from a host thread that has made no CUDA call of its own (no context is bound to it yet), over pools and
+    queries whose maps are not known from an earlier call."""
+    import threading
+    qlens = [40, 1] if which == "pa_decode_chunked_prefill_biased" else [1, 1]
+    b = Batch(cuda_device, qlens, [200, 300], 8, 2, 128, 16, kv, "bf16", seed=17, spoil=False)
+    if which == "pa_decode":
+        b.ws = pa.alloc_workspace(pa.pa_decode_workspace_size(b.desc, 2), cuda_device)
+    stream, failed = torch.cuda.current_stream().cuda_stream, []
+
+    def call():
+        try:
+            if which == "pa_decode":
+                pa.pa_decode(b.desc, b.q, b.k, b.v, b.tables, b.sl, b.scale, b.out, b.ws, stream)
+            else:
+                b.run(stream=stream)
+        except pa.PaError as e:
+            failed.append(str(e))
+    t = threading.Thread(target=call)
+    t.start()
+    t.join()
+    assert not failed
+    b.check()
+
+
 def test_captured_and_replayed(cuda_device):
     """A mixed step captured into a graph and replayed on other inputs."""
     b = Batch(cuda_device, [40, 1, 1], [200, 300, 17], 8, 2, 128, 16, "bf16", "bf16", cap=30.0, window=60, seed=8)
