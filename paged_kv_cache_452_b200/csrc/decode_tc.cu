@@ -38,6 +38,8 @@
 //    scales are folded into the softmax scale and the output scale.
 #include <cuda_runtime.h>
 
+#include <mutex>
+
 #include "pa_device.cuh"
 #include "pa_kernels.h"
 
@@ -1037,11 +1039,16 @@ cudaError_t launch_instance(DecodeParams p, const CUtensorMap& tm_k, const CUten
   using C = Cfg<KV, D, BS>;
   const SmemLayout L = smem_layout(C::KVB + q_area_bytes(p.group, D), p.nstages, p.rows.num_seqs);
   auto kern = decode_tc_kernel<KV, D, BS, MOD>;
-  // raise the kernel's dynamic shared memory limit once per device
-  static int set_for[64] = {0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  // What is kept per device below changes together: calls of two host threads
+  // that saw it half changed could launch more CTAs than are resident, or
+  // find the limit lowered again.
+  static std::mutex mu;
+  std::unique_lock<std::mutex> lock(mu);
+  // raise the kernel's dynamic shared memory limit once per device
+  static int set_for[64] = {0};
   if (dev >= 64 || set_for[dev] < (int)L.total) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L.total);
     if (e != cudaSuccess) return e;
@@ -1059,6 +1066,7 @@ cudaError_t launch_instance(DecodeParams p, const CUtensorMap& tm_k, const CUten
       occ_ctas[dev] = resident;
     }
   }
+  lock.unlock();
   if (resident < 1) return cudaErrorNotSupported;
   if (p.grid > resident * num_sms) p.grid = resident * num_sms;
   cudaLaunchAttribute attr[1];

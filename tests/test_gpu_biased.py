@@ -524,6 +524,22 @@ def test_first_call_of_a_host_thread(which, kv, cuda_device):
     b.check()
 
 
+def test_host_threads_call_at_once(cuda_device):
+    """Host threads that call with batches of other sizes (other shared-memory sizes of one kernel) on one stream."""
+    from concurrent.futures import ThreadPoolExecutor
+    batches = [Batch(cuda_device, [1] * n, [1 + (37 * i + 11 * n) % 900 for i in range(n)], 8, 2, 128, 16, "bf16", "bf16",
+                     cap=30.0, seed=n, spoil=False) for n in (3, 60, 700, 1500)]
+    stream = torch.cuda.current_stream()
+
+    def calls(b):
+        for _ in range(60):
+            b.run(decode=True, stream=stream)
+    with ThreadPoolExecutor(len(batches)) as pool:
+        list(pool.map(calls, batches))
+    for b in batches:
+        b.check()
+
+
 def test_captured_and_replayed(cuda_device):
     """A mixed step captured into a graph and replayed on other inputs."""
     b = Batch(cuda_device, [40, 1, 1], [200, 300, 17], 8, 2, 128, 16, "bf16", "bf16", cap=30.0, window=60, seed=8)
