@@ -497,6 +497,27 @@ def test_bad_table_entries_and_long_contexts_are_flagged(cuda_device):
         assert pa.workspace_error(b.ws) == 3
 
 
+@pytest.mark.parametrize("qlens,lens", [([1] * 3, [300, 17, 900]), ([70, 1, 130], [200, 90, 130])], ids=["decode", "chunks"])
+@pytest.mark.parametrize("hq,hkv,d,kv,q", [(8, 8, 128, "bf16", "bf16"), (8, 4, 128, "e4m3", "bf16"),
+                                           (8, 8, 64, "e4m3", "bf16"), (8, 8, 64, "f32", "f32"),
+                                           (32, 8, 128, "e4m3", "f32")])
+def test_pools_past_32_bits(hq, hkv, d, kv, q, qlens, lens, cuda_device):
+    """Blocks whose bytes lie past 2^32 in each of the pools."""
+    b = Batch(cuda_device, qlens, lens, hq, hkv, d, 16, kv, q, cap=30.0, slopes=True, seed=18, spoil=False)
+    bytes_per_block = b.k[0].nbytes
+    blocks = 2**32 // bytes_per_block + b.desc.num_blocks + 1
+    first = blocks - b.desc.num_blocks
+    far = []
+    for t in (b.k, b.v):
+        far.append(torch.empty((blocks, *t.shape[1:]), dtype=t.dtype, device=cuda_device))
+        far[-1][first:] = t
+    b.k, b.v = far
+    b.tables = torch.where(b.tables >= 0, b.tables + first, b.tables)
+    b.desc = pa.CacheDesc.make(blocks, 16, hkv, hq, d, kv, q, KS, VS)
+    b.run()
+    b.check()
+
+
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 @pytest.mark.parametrize("which", ["pa_decode_biased", "pa_decode_chunked_prefill_biased", "pa_decode"])
 def test_first_call_of_a_host_thread(which, kv, cuda_device):

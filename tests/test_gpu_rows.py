@@ -308,6 +308,40 @@ def test_cache_read_of_many_rows(n, hkv, d, bs, kv, q, how, head_scales, cuda_de
     test_cache_read_matches_the_pool(n, hkv, d, bs, kv, q, how, head_scales, cuda_device)
 
 
+@pytest.mark.parametrize("n", [100, 3000])
+@pytest.mark.parametrize("d,kv,q", [(128, "bf16", "bf16"), (128, "e4m3", "bf16"), (64, "f32", "f32"), (64, "e4m3", "f32")])
+def test_pools_past_32_bits(d, kv, q, n, cuda_device):
+    """Slots whose bytes lie past 2^32 in each of the pools: written, and read back."""
+    hq, hkv, bs = 8, 8, 16
+    rng, g = np.random.default_rng(n), torch.Generator(device=cuda_device).manual_seed(n)
+    size = {"bf16": 2, "e4m3": 1, "f32": 4}[kv]
+    first, used = 2**32 // (hkv * bs * d * size) + 1, n // bs + 3
+    desc = pa.CacheDesc.make(first + used, bs, hkv, hq, d, kv, q, KS, VS)
+    kc, vc = pa.alloc_cache(desc, cuda_device)
+    assert kc.nbytes > 2**32
+    qkv = torch.randn((n, hq + 2 * hkv, d), generator=g, device=cuda_device).to(DT[q])
+    xq, xk, xv = qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:]
+    table = table_of(5000, d, cuda_device)
+    pos = torch.from_numpy(rng.integers(0, 5000, n).astype(np.int32)).to(cuda_device)
+    w = (1 + 0.3 * torch.randn(d, generator=g, device=cuda_device)).to(DT[q])
+    slots = torch.from_numpy(slots_of(n, used, bs, "runs", rng)).to(cuda_device) + first * bs
+    out = torch.empty((n, hq, d), dtype=DT[q], device=cuda_device)
+    pa.pa_norm_rope_write(desc, pa.QkPrep.make(w, w, 1e-5, table), xq, xk, xv, pos, slots, out, kc, vc)
+    close(out, fp64_rows(xq, w, 1e-5, table, pos, d, False), HALF[q])
+    gk, gv = pool_rows(desc, kc, vc, slots)
+    ek = fp64_rows(xk, w, 1e-5, table, pos, d, False)
+    k, v = (torch.empty((n, hkv, d), dtype=DT[q], device=cuda_device) for _ in range(2))
+    pa.pa_cache_read(desc, slots, kc, vc, k, v)
+    if kv == "e4m3":
+        close_e4m3(gk, ek, KS)
+        close_e4m3(gv, xv.double(), VS)
+        gk, gv = ((t.view(torch.float8_e4m3fn).float() * s).to(DT[q]) for t, s in ((gk, KS), (gv, VS)))
+    else:
+        close(gk, ek, HALF[q])
+        assert torch.equal(gv, xv)
+    assert torch.equal(k, gk) and torch.equal(v, gv)
+
+
 def test_write_then_read_back(cuda_device):
     """What pa_norm_rope_write stores comes back through pa_cache_read: the run a swap-out makes."""
     desc, kc, vc, (xq, xk, xv), slots, _, rng, g = setup(200, 8, 2, 128, 16, "bf16", "bf16", "runs", cuda_device, 23)
