@@ -151,8 +151,8 @@ int pa_norm_rope_write(const pa_cache_desc* desc, const pa_qk_prep* prep, const 
 /* pa_cache_read: pa_cache_write's inverse: row t of k_out and v_out becomes
  * what the pools hold at slot_mapping[t]; a slot outside the pool leaves its
  * rows as they were.  Rows of fp32 and bf16 pools are bit copies (query dtype =
- * pool dtype, else PA_ERR_UNSUPPORTED); e4m3 codes come back as code * scale,
- * rounded once to the query dtype (NaN codes as NaN).
+ * pool dtype, else PA_ERR_UNSUPPORTED); e4m3 codes come back as code * scale
+ * in fp32, rounded to bf16 where that is the query dtype (NaN codes as NaN).
  *   slot_mapping  device, int64 [num_tokens]; a slot may come more than once
  *   k_out, v_out  device, [num_tokens][num_kv_heads][head_dim], q_dtype, apart
  *                 from each other and from the pools */
@@ -370,7 +370,8 @@ int pa_decode_chunked_prefill(const pa_cache_desc* desc, const void* q, const vo
  * (softcap 0: scale * q_i k_j), and the output is the softmax over the visible
  * keys.  Without prefix and window that is pa_decode's causal attention. */
 typedef struct {
-  float softcap;              /* 0 (none), or 1e-4 to 1e4 */
+  float softcap;              /* 0 (none), or 1e-4 to 1e4; bf16 queries' capped scores are off by up to 5e-7 *
+                                 softcap (2.5e-5 at 50), fp32 queries' by fp32's rounding */
   int32_t window;             /* 0 (none), or the keys a row sees up to itself, itself included */
   const float* slopes;        /* NULL (none), or device fp32 [num_q_heads], finite */
   const int32_t* prefix_lens; /* NULL (none), or device int32 [num_seqs]: keys 0 .. prefix_lens[s] - 1 are
@@ -397,8 +398,14 @@ size_t pa_biased_workspace_size(const pa_cache_desc* desc, int32_t num_seqs, int
  * fp32 queries over an fp32 or e4m3 pool on CUDA cores; other pairs are
  * PA_ERR_UNSUPPORTED (their workspace size is 0).  Over an e4m3 pool a bf16
  * query row is brought into f16's range by a power of two, exactly but for
- * elements below 2^-28 of its largest.  V rows that no query of the sequence sees may
- * hold anything, NaN included. */
+ * elements below 2^-28 of its largest.  V rows that no query of the sequence
+ * sees may hold anything, NaN included.  A group of more than 8 query heads
+ * per kv head is read as equal parts, the largest divisor of it up to 8 each
+ * (16 as 8 + 8, 9 as 3 x 3, a prime group head by head), and every part reads
+ * its kv head's keys again.
+ * Limits (PA_ERR_UNSUPPORTED past them): 16384 sequences; num_seqs *
+ * max_blocks_per_seq * num_kv_heads * parts below 2^31; table rows below 2^31
+ * tokens. */
 int pa_decode_biased(const pa_cache_desc* desc, const pa_score_mod* mod, const void* q, const void* k_cache,
                      const void* v_cache, const int32_t* block_tables, int32_t max_blocks_per_seq,
                      const int32_t* seq_lens, int32_t num_seqs, float scale, void* out, void* workspace,

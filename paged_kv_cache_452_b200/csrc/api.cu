@@ -607,7 +607,8 @@ int launch_chunks(const pa_cache_desc* d, const Chunks& c, int num_tokens, int s
 // every SM (one chunk: 255 without, 284 with 3/8): none there.
 // Nor where decode rows are too few to keep HBM busy for long (up to 17 with 2
 // chunks of 710 rows, by 2 kv heads 49 against 60, by 8 79 against 89; 60 of
-// them by 8 kv heads 119 against 103).
+// them by 8 kv heads 119 against 103).  The rule knows sizes alone: it counts
+// chunks among the sequences, and keys that a window hides among the rows'.
 int chunks_ahead(const pa_cache_desc* d, int num_seqs, int sms) {
   return d->kv_dtype == kBF16 && (int64_t)num_seqs * d->num_kv_heads >= 2LL * sms ? sms * 3 / 8 : 0;
 }

@@ -24,8 +24,9 @@ struct CacheWriteParams {
 };
 cudaError_t launch_cache_write(const CacheWriteParams& p, int in_dtype, int kv_dtype, cudaStream_t stream);
 
-// Division of n < 2^31 by a fixed d >= 1 as a multiplication: the quotient is
-// (umulhi(n, mul) + n) >> shift (round-up method: mul = floor(2^32 (2^shift -
+// Division of n < 2^31 by a fixed d >= 1 as a multiplication (Granlund and
+// Montgomery, "Division by Invariant Integers using Multiplication", PLDI
+// 1994): the quotient is (umulhi(n, mul) + n) >> shift (mul = floor(2^32 (2^shift -
 // d) / d) + 1 with shift = ceil(log2 d)).
 struct FastDiv {
   uint32_t mul, shift, d;
@@ -263,8 +264,9 @@ cudaError_t launch_chunk_biased(const PrefillParams& p, const CUtensorMap& tm_k,
 inline int64_t chunk_biased_units(int num_tokens, int num_seqs, int group, int heads) {
   return ((int64_t)num_tokens / (2 * (128 / group)) + num_seqs) * heads;
 }
-// Slots per SM for cut units (a slot: one part of one unit, 256 rows; with 4
-// the 256 units of two long chunks were halved too, and took 415 us, not 344).
+// Slots per SM for cut units (a slot: one part of one unit, 256 rows).  Two
+// keep the workspace at 39 MB (head_dim 128) and leave steps of more units than
+// SMs whole.
 constexpr int kPartSlots = 2;
 cudaError_t launch_prefill_tc(const PrefillParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                               int head_dim, int block_size, int num_tokens, cudaStream_t stream);
