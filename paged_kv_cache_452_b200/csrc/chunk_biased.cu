@@ -749,7 +749,7 @@ __global__ void __launch_bounds__(C<KV, D, BS>::THREADS, 1)
         // it in f16's range (its scores' factors take it back)
         wait_ok(q_raw, (uint32_t)(n & 1));
         uint32_t most = 0;
-#pragma unroll
+#pragma unroll 4  // (whole, its registers spill others': two 1024-row chunks 350 us, so 344)
         for (int v = 0; v < T::NCH * 8; ++v) {
           const uint4 b = *reinterpret_cast<const uint4*>(qs + (v >> 3) * kTileRow + r * 128 + (v & 7) * 16);
           most = dev::max_bf16_bits(dev::max_bf16_bits(most, b.x), b.y);
