@@ -410,7 +410,7 @@ def pa_decode_biased(desc, mod, q, k_cache, v_cache, block_tables, seq_lens, sca
         raise PaError(1, f"{who}: {q.shape[0]} query rows for {n} sequences")
     _call(who, dev, stream, lib().pa_decode_biased, ctypes.byref(desc), ctypes.byref(mod), q.data_ptr(),
           k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), block_tables.shape[1], seq_lens.data_ptr(), n,
-          scale, out.data_ptr(), workspace.data_ptr(), workspace.nbytes)
+          float(scale), out.data_ptr(), workspace.data_ptr(), workspace.nbytes)
 
 
 def pa_decode_chunked_prefill_biased(desc, mod, q, k_cache, v_cache, block_tables, query_start_loc, seq_lens,
@@ -421,7 +421,7 @@ def pa_decode_chunked_prefill_biased(desc, mod, q, k_cache, v_cache, block_table
     _array(who, "query_start_loc", query_start_loc, torch.int32, dev, (n + 1,))
     _call(who, dev, stream, lib().pa_decode_chunked_prefill_biased, ctypes.byref(desc), ctypes.byref(mod), q.data_ptr(),
           k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
-          query_start_loc.data_ptr(), seq_lens.data_ptr(), n, q.shape[0], max_q_len, scale, out.data_ptr(),
+          query_start_loc.data_ptr(), seq_lens.data_ptr(), n, q.shape[0], int(max_q_len), float(scale), out.data_ptr(),
           workspace.data_ptr(), workspace.nbytes)
 
 

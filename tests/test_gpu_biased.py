@@ -427,6 +427,26 @@ def test_cut_units_of_many_chunks(kv, cuda_device):
     assert torch.equal(b.out, was)
 
 
+@pytest.mark.parametrize("group", [17, 65, 127, 131, 256])
+@pytest.mark.parametrize("kv,q", [("bf16", "bf16"), ("e4m3", "bf16"), ("f32", "f32")])
+def test_large_groups(group, kv, q, cuda_device):
+    """Groups past a query tile's rows or with no divisor that fits, in chunks and single rows."""
+    b = Batch(cuda_device, [1, 9, 0, 1, 40], [30, 200, 5, 700, 64], group, 1, 64, 16, kv, q, cap=20.0, window=60,
+              slopes=True, prefix=[4] * 5, seed=group)
+    b.run(decode=False)
+    b.check()
+
+
+def test_scalars_as_the_plain_calls_take_them(cuda_device):
+    """A scale and a max_q_len that are tensors of one element."""
+    b = Batch(cuda_device, [3, 1], [40, 90], 8, 2, 64, 16, "bf16", "bf16", seed=3)
+    b.scale = torch.tensor(b.scale, dtype=torch.float64)
+    pa.pa_decode_chunked_prefill_biased(b.desc, b.mod, b.q, b.k, b.v, b.tables, b.qsl, b.sl, torch.tensor(3), b.scale,
+                                        b.out, b.ws)
+    b.scale = float(b.scale)
+    b.check()
+
+
 def test_a_group_of_more_than_128(cuda_device):
     b = Batch(cuda_device, [3, 1], [40, 90], 130, 1, 64, 16, "bf16", "bf16", cap=10.0, seed=3)
     b.run(decode=False)
