@@ -454,17 +454,17 @@ BiasedWs biased_workspace(const pa_cache_desc* d, int32_t num_seqs, int32_t num_
 
 bool biased_tc(const pa_cache_desc* d) { return d->q_dtype == kBF16; }
 
-// Sizes that the kernels of a biased step index in 32 bits; asked before
-// anything of the step is launched.
-int check_biased_sizes(const pa_cache_desc* d, int32_t num_seqs, int32_t num_tokens, int32_t max_blocks, bool chunks,
-                       const char* who) {
+// Sizes that the kernels of a biased step (the decode for single rows, the
+// chunk kernel) index in 32 bits; asked before anything of it is launched.
+int check_biased_sizes(const pa_cache_desc* d, int32_t num_seqs, int32_t num_tokens, int32_t max_blocks, bool decodes,
+                       bool chunks, const char* who) {
   const int group = d->num_q_heads / d->num_kv_heads;
   if (!biased_tc(d)) {
     if (!biased_simt_fits(num_tokens, num_seqs, d->num_q_heads, d->num_kv_heads))
       return fail(PA_ERR_UNSUPPORTED, "%s: %d rows of %d heads", who, num_tokens, d->num_q_heads);
     return PA_OK;
   }
-  if ((int64_t)num_seqs * max_blocks * (d->num_q_heads / cut_group(group, 8)) >= (int64_t)INT32_MAX)
+  if (decodes && (int64_t)num_seqs * max_blocks * (d->num_q_heads / cut_group(group, 8)) >= (int64_t)INT32_MAX)
     return fail(PA_ERR_UNSUPPORTED, "%s: num_seqs * max_blocks_per_seq * heads reaches 2^31", who);
   const int cut = cut_group(group, 128);
   if (chunks && chunk_biased_units(num_tokens, num_seqs, cut, d->num_q_heads / cut) >= (int64_t)INT32_MAX)
@@ -1093,7 +1093,7 @@ int pa_decode_biased(const pa_cache_desc* d, const pa_score_mod* mod, const void
                            workspace, who);
   if (rc) return rc;
   if ((rc = check_mod(mod, scale, d, max_blocks_per_seq, who)) || num_seqs == 0) return rc;
-  if ((rc = check_biased_sizes(d, num_seqs, num_seqs, max_blocks_per_seq, false, who))) return rc;
+  if ((rc = check_biased_sizes(d, num_seqs, num_seqs, max_blocks_per_seq, true, false, who))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (biased_tc(d)) {
     int sms = 0;
@@ -1132,12 +1132,12 @@ int pa_decode_chunked_prefill_biased(const pa_cache_desc* d, const pa_score_mod*
   if (num_tokens < 0 || max_q_len < 0) return fail(PA_ERR_INVALID_ARG, "%s: negative size", who);
   if (num_tokens == 0) return PA_OK;
   if (max_q_len == 0) return fail(PA_ERR_INVALID_ARG, "%s: max_q_len 0 with %d tokens", who, num_tokens);
-  if ((rc = check_biased_sizes(d, num_seqs, num_tokens, max_blocks_per_seq, max_q_len > 1, who))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   // single-token rows on the decode kernel, the others on the chunk kernel.
   // Rows that would fill every sequence up to max_q_len leave no single ones,
   // unless some of them lie past the last sequence's: the chunk kernel has all.
   const bool decodes = max_q_len == 1 || (int64_t)num_seqs * max_q_len != num_tokens;
+  if ((rc = check_biased_sizes(d, num_seqs, num_tokens, max_blocks_per_seq, decodes, max_q_len > 1, who))) return rc;
   if (!biased_tc(d)) {
     if (workspace_bytes < 256) return fail(PA_ERR_INVALID_ARG, "%s: workspace < 256 bytes", who);
     return run_biased_simt(d, mod, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, query_start_loc,

@@ -148,6 +148,9 @@ def test_biased_steps_check_sizes_before_the_first_launch():
     wide = pa.CacheDesc.make(64, 16, 8, 128, 64, "bf16", "bf16")
     assert chunk(wide, 16000, 10000, 20000, 300) == 2 and b"2^31" in pa.lib().pa_last_error()
     assert pa.lib().pa_decode_biased(ctypes.byref(wide), mod, P, P, P, P, 10000, P, 16000, 0.125, P, P, 1 << 40, None) == 2
+    # ... which no kernel indexes in a step of full chunks: as far as the device, which this test does not have
+    if not torch.cuda.is_available():
+        assert chunk(wide, 16000, 10000, 32000, 2) == 4
     # 2^31 units of chunk rows
     many = pa.CacheDesc.make(64, 16, 512, 512, 64, "bf16", "bf16")
     assert chunk(many, 2, 4, 2**30 + 2**21, 2**30) == 2 and b"chunks" in pa.lib().pa_last_error()
